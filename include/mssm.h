@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define MSSM_ABI_VERSION 6
+#define MSSM_ABI_VERSION 7
 
 typedef enum {
     MSSM_SUCCESS = 0,
@@ -456,6 +456,146 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
                                           float *dDskip, float *dz, float *dh0, void *workspace,
                                           size_t workspace_bytes, int64_t batch, int64_t L,
                                           int64_t D, int64_t N, mssm_dtype dtype, void *stream);
+
+/*
+ * ---- linear attention with a decay for each head -------------------------------------------
+ *
+ * The recurrence with a matrix for a state: per sequence and head h, with a
+ * log decay g (of each token and head, or one for each head) and S [dk, dv],
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T
+ *     o_t = scale * S_t^T q_t
+ * i.e. the scan's h = Abar h + Bbar x, y = C . h with one decay for the whole
+ * head instead of one for each state index.  Head h reads the queries and keys
+ * of key head h / (heads / key_heads).
+ *
+ *   q, k      : [tokens, key_heads, dk] of `dtype`, consecutive tokens q_row,
+ *               k_row elements apart (key_heads * dk when dense; larger for a
+ *               view into a fused projection's output)
+ *   v         : [tokens, heads, dv] of `dtype`, consecutive tokens v_row apart
+ *   log_decay : float32, [tokens, heads] (MSSM_DECAY_PER_TOKEN) or [heads]
+ *               (MSSM_DECAY_PER_HEAD), dense.  Usually <= 0.  Minus infinity
+ *               (or anything below -1e4) forgets the state completely.
+ *   o         : [tokens, heads, dv] of `dtype`, dense
+ *   state, last_state : [seqs, heads, dk, dv] float32, dense, or NULL (start
+ *               from zero; not wanted).  last_state may be state itself.
+ * Sequences: with seq_offsets NULL, `seqs` sequences of `L` tokens each, tokens
+ * = seqs * L.  With seq_offsets (a device array of seqs + 1 int64 that starts
+ * at 0, does not decrease and ends at L) L is the number of tokens in all and
+ * sequence i has tokens seq_offsets[i] .. seq_offsets[i + 1] - 1; a sequence
+ * may be empty (its last state is its first).  Offsets outside 0 .. L are taken
+ * as 0 or L; tokens that no sequence holds get no output.
+ *
+ * Precision: float32 inputs are multiplied and summed in float32.  bfloat16
+ * inputs are multiplied on the bf16 matrix cores with float32 sums; states are
+ * float32 and accurate to about 1e-6, outputs are rounded to bfloat16 once and
+ * their operands (decayed scores, state) once before.  A sequence is worked on
+ * in chunks of 64 (float32: 32) tokens: infinities or NaN in a token's q, k, v
+ * can reach every output of its chunk and what follows, never another sequence.
+ *
+ * Supported: dk and dv multiples of 16 from 16 to 128
+ * (mssm_linear_attention_supports); heads a multiple of key_heads.
+ * Any element-aligned address; 16-byte aligned tensors and rows are faster.
+ * The workspace (256-byte aligned, at least the size the query gives, which
+ * may be 0) holds the states of the segments that long sequences are cut into.
+ * tokens, seqs or heads equal to zero are valid: last states are still set.
+ *
+ * mssm_linear_attention_step: one token for each of `seqs` sequences, the state
+ *   read and overwritten (single-token serving).  q, k [seqs, key_heads, dk],
+ *   v, o [seqs, heads, dv], log_decay [seqs, heads] or [heads]; rows as above.
+ *   No workspace.
+ *
+ * mssm_linear_attention_bwd: gradients of sum(dout * o) + sum(dlast * last_state).
+ *   dout        : [tokens, heads, dv] of `dtype`, dense
+ *   dlast       : [seqs, heads, dk, dv] float32, or NULL
+ *   dq, dk_out  : [tokens, key_heads, dk] of `dtype`, dense, summed over the
+ *                 heads that share a key head
+ *   dv_out      : [tokens, heads, dv] of `dtype`, dense
+ *   dlog_decay  : float32, as log_decay
+ *   dstate      : gradient of the initial state [seqs, heads, dk, dv] float32,
+ *                 or NULL
+ *   Every gradient is overwritten.  The states are recomputed.  Sums over
+ *   tokens, heads and segments run in a fixed order: results are deterministic.
+ */
+typedef enum {
+    MSSM_DECAY_PER_HEAD = 0,
+    MSSM_DECAY_PER_TOKEN = 1
+} mssm_decay;
+
+/* 1 if the kernels are built for these head sizes, else 0. */
+int mssm_linear_attention_supports(int64_t dk, int64_t dv);
+
+/* Workspace bytes of the forward (backward == 0) or backward call; `packed`:
+ * whether seq_offsets are given (then L is the number of tokens in all). */
+mssm_status mssm_linear_attention_workspace_size(int64_t seqs, int64_t L, int64_t key_heads,
+                                                 int64_t heads, int64_t dk, int64_t dv,
+                                                 int packed, int backward, mssm_dtype dtype,
+                                                 size_t *bytes);
+
+mssm_status mssm_linear_attention_fwd(const void *q, const void *k, const void *v,
+                                      const float *log_decay, const int64_t *seq_offsets,
+                                      const float *state, void *o, float *last_state,
+                                      float scale, mssm_decay decay, void *workspace,
+                                      size_t workspace_bytes, int64_t seqs, int64_t L,
+                                      int64_t key_heads, int64_t heads, int64_t dk, int64_t dv,
+                                      int64_t q_row, int64_t k_row, int64_t v_row,
+                                      mssm_dtype dtype, void *stream);
+
+mssm_status mssm_linear_attention_step(const void *q, const void *k, const void *v,
+                                       const float *log_decay, float *state, void *o,
+                                       float scale, mssm_decay decay, int64_t seqs,
+                                       int64_t key_heads, int64_t heads, int64_t dk, int64_t dv,
+                                       int64_t q_row, int64_t k_row, int64_t v_row,
+                                       mssm_dtype dtype, void *stream);
+
+mssm_status mssm_linear_attention_bwd(const void *q, const void *k, const void *v,
+                                      const float *log_decay, const int64_t *seq_offsets,
+                                      const float *state, const void *dout, const float *dlast,
+                                      void *dq, void *dk_out, void *dv_out, float *dlog_decay,
+                                      float *dstate, float scale, mssm_decay decay,
+                                      void *workspace, size_t workspace_bytes, int64_t seqs,
+                                      int64_t L, int64_t key_heads, int64_t heads, int64_t dk,
+                                      int64_t dv, int64_t q_row, int64_t k_row, int64_t v_row,
+                                      mssm_dtype dtype, void *stream);
+
+/*
+ * ---- layer norm --------------------------------------------------------------------------------
+ *
+ * The norm and residual add that stand around a block ("Understanding Mamba",
+ * section 8.2: they belong to the model, not the block), per row of D values:
+ *     t = x + residual      rounded to `dtype`; t = x without a residual
+ *     y = (t - mean) * rstd * weight + bias,    rstd = 1 / sqrt(var + eps)
+ * with the row's mean and (biased) variance, in float32.
+ *
+ *   x, y          : [rows, D] of `dtype`
+ *   residual, sum : [rows, D] of `dtype`, given together or both NULL; sum
+ *                   receives t and may be residual or x itself
+ *   weight, bias  : [D] float32; bias may be NULL
+ *   mean, rstd    : [rows] float32, given together (for the backward pass) or
+ *                   both NULL
+ * D up to 32768 (MSSM_ERROR_NOT_SUPPORTED above).  eps >= 0.
+ *
+ * mssm_layer_norm_bwd: gradients of sum(dy * y) (+ sum(dsum * t)) from what was
+ * normalised (x of this call: t of the forward pass) and its mean and rstd.
+ *   dsum            : gradient that reaches t itself, or NULL
+ *   dx              : gradient of t (so of x and of residual), `dtype`
+ *   dweight, dbias  : [D] float32, dbias may be NULL; sums over the rows in a
+ *                     fixed order (deterministic)
+ * The workspace holds the blocks' partial sums (256-byte aligned).  rows or D
+ * equal to zero: nothing is read; dweight and dbias are set to zero.
+ */
+mssm_status mssm_layer_norm_fwd(const void *x, const void *residual, const float *weight,
+                                const float *bias, void *y, void *sum, float *mean, float *rstd,
+                                float eps, int64_t rows, int64_t D, mssm_dtype dtype,
+                                void *stream);
+
+mssm_status mssm_layer_norm_bwd_workspace_size(int64_t rows, int64_t D, mssm_dtype dtype,
+                                               size_t *bytes);
+
+mssm_status mssm_layer_norm_bwd(const void *dy, const void *dsum, const void *x,
+                                const float *weight, const float *mean, const float *rstd,
+                                void *dx, float *dweight, float *dbias, void *workspace,
+                                size_t workspace_bytes, int64_t rows, int64_t D,
+                                mssm_dtype dtype, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,11 @@
+// Linear attention, fp32: dv.
+#include "la_pass_launch.h"
+#include "linear_attention.h"
+
+namespace mssm {
+namespace la {
+hipError_t pass_dv_fp32(const PassArgs& p, hipStream_t stream) {
+  return launch_pass<float, true, true, 0>(p, stream);
+}
+}  // namespace la
+}  // namespace mssm

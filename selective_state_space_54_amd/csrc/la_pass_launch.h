@@ -1,0 +1,29 @@
+// Picks the instance of la_pass for the sizes of a call.
+#pragma once
+
+#include "linear_attention.h"
+#include "mssm_internal.h"
+
+namespace mssm {
+namespace la {
+
+template <typename T, int DA, int NT, bool kRev, bool kOut, int kDot>
+hipError_t launch_pass_as(const PassArgs& p, hipStream_t stream) {
+  constexpr int C = sizeof(T) == 2 ? 64 : 32;
+  const int64_t blocks = p.grid.slots * p.heads;
+  hipLaunchKernelGGL((la_pass<T, C, DA, NT, kRev, kOut, kDot>), dim3(static_cast<uint32_t>(blocks)),
+                     dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <typename T, bool kRev, bool kOut, int kDot>
+hipError_t launch_pass(const PassArgs& p, hipStream_t stream) {
+  if (p.dA <= 64)
+    return p.dB <= 64 ? launch_pass_as<T, 64, 1, kRev, kOut, kDot>(p, stream)
+                      : launch_pass_as<T, 64, 2, kRev, kOut, kDot>(p, stream);
+  return p.dB <= 64 ? launch_pass_as<T, 128, 1, kRev, kOut, kDot>(p, stream)
+                    : launch_pass_as<T, 128, 2, kRev, kOut, kDot>(p, stream);
+}
+
+}  // namespace la
+}  // namespace mssm

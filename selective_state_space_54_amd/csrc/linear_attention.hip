@@ -1,0 +1,440 @@
+// Linear attention with a decay for each head: how a call is cut into
+// segments, the pass that joins the segments' states, the single-token step,
+// the sums over heads that share queries and keys, and the order of launches.
+// The matrix products are in linear_attention.h.
+#include "la_args.h"
+#include "linear_attention.h"
+#include "mssm_internal.h"
+
+namespace mssm {
+
+namespace la {
+#define MSSM_LA_PASS(NAME)                                              \
+  hipError_t pass_##NAME##_bf16(const PassArgs& p, hipStream_t stream); \
+  hipError_t pass_##NAME##_fp32(const PassArgs& p, hipStream_t stream); \
+  static hipError_t pass_##NAME(mssm_dtype t, const PassArgs& p, hipStream_t stream) { \
+    return t == MSSM_BFLOAT16 ? pass_##NAME##_bf16(p, stream) : pass_##NAME##_fp32(p, stream); \
+  }
+MSSM_LA_PASS(fwd)
+MSSM_LA_PASS(state)
+MSSM_LA_PASS(state_rev)
+MSSM_LA_PASS(dq)
+MSSM_LA_PASS(dk)
+MSSM_LA_PASS(dv)
+#undef MSSM_LA_PASS
+}  // namespace la
+
+namespace {
+
+using la::Grid;
+using la::PassArgs;
+using la::View;
+
+// ---- the state before each segment ---------------------------------------------------------------
+
+// Runs over a sequence's segments in order (kRev: from the last): `st` holds
+// each segment's own state on entry and the state the segment starts from on
+// return; `last` the state after all of them.  A thread owns four values of one
+// head's state; the segments' loads do not depend on each other and run kAhead
+// ahead of the chain of multiply-adds.
+template <bool kRev>
+__global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t size,
+                                                const float* __restrict__ init,
+                                                const float* __restrict__ decay,
+                                                float* __restrict__ st, float* __restrict__ last) {
+  using la::f32x4;
+  constexpr int kAhead = 8;
+  const int64_t i = 4 * (int64_t(blockIdx.y) * 256 + threadIdx.x);
+  if (i >= size) return;
+  const int64_t seq = blockIdx.x / heads;
+  const int h = blockIdx.x % heads;
+  int64_t first, count;
+  if (grid.offsets) {
+    auto at = [&](int64_t s) {
+      const int64_t o = grid.offsets[s];
+      return o < 0 ? int64_t(0) : (o > grid.tokens ? grid.tokens : o);
+    };
+    const int64_t a = at(seq), b = max(at(seq + 1), a);
+    first = a / grid.seg_len + seq;
+    count = max((b - a + grid.seg_len - 1) / grid.seg_len, int64_t(1));
+  } else {
+    first = seq * grid.segs;
+    count = grid.segs;
+  }
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t sh = (seq * heads + h) * size + i;
+  if (init) s = f32x4{init[sh], init[sh + 1], init[sh + 2], init[sh + 3]};
+  // the segment that comes last has a state of its own only where `last` is asked for
+  const int64_t own = last ? count : count - 1;
+  for (int64_t c0 = 0; c0 < count; c0 += kAhead) {
+    f32x4 u[kAhead];
+    float e[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t c = c0 + k;
+      const int64_t slot = first + (kRev ? count - 1 - c : c);
+      u[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      e[k] = 1.0f;
+      if (c < own) {
+        u[k] = *reinterpret_cast<const f32x4*>(st + (slot * heads + h) * size + i);
+        e[k] = decay[slot * heads + h];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t c = c0 + k;
+      if (c >= count) break;
+      const int64_t slot = first + (kRev ? count - 1 - c : c);
+      *reinterpret_cast<f32x4*>(st + (slot * heads + h) * size + i) = s;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r] = __builtin_fmaf(e[k], s[r], u[k][r]);
+    }
+  }
+  if (last)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) last[sh + r] = s[r];
+}
+
+hipError_t launch_carry_states(bool rev, const Grid& grid, int heads, int64_t size,
+                               const float* init, const float* decay, float* st, float* last,
+                               hipStream_t stream) {
+  const dim3 g(static_cast<uint32_t>(grid.seqs * heads),
+               static_cast<uint32_t>((size / 4 + 255) / 256));
+  if (rev)
+    hipLaunchKernelGGL(la_carry<true>, g, dim3(256), 0, stream, grid, heads, size, init, decay, st,
+                       last);
+  else
+    hipLaunchKernelGGL(la_carry<false>, g, dim3(256), 0, stream, grid, heads, size, init, decay,
+                       st, last);
+  return hipGetLastError();
+}
+
+// ---- sums --------------------------------------------------------------------------------------------
+
+// out[t, hk, :] = the sum over the `rep` heads that share key head hk, in their order.
+template <typename T>
+__global__ __launch_bounds__(256) void la_sum_heads(const float* __restrict__ part, T* out,
+                                                    int64_t quads, int d, int rep) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const int per = d / 4;                               // quads of a head
+  const int64_t head = i / per;                        // t * key_heads + hk
+  const int c = static_cast<int>(i - head * per) * 4;
+  la::f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < rep; ++r)
+    s += *reinterpret_cast<const la::f32x4*>(part + (head * rep + r) * d + c);
+  la::store4(out + head * d + c, s);
+}
+
+// out[h] = sum over slots of part[slot, h]; one block per head.
+__global__ __launch_bounds__(256) void la_sum_slots(const float* __restrict__ part, float* out,
+                                                    int64_t slots, int heads) {
+  __shared__ float m[4];
+  float s = 0.0f;
+  for (int64_t i = threadIdx.x; i < slots; i += 256) s += part[i * heads + blockIdx.x];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) m[threadIdx.x >> 6] = s;
+  block_sync();
+  if (threadIdx.x == 0) out[blockIdx.x] = (m[0] + m[1]) + (m[2] + m[3]);
+}
+
+// ---- one token -----------------------------------------------------------------------------------------
+
+struct StepLaunch {
+  const void *q, *k, *v;
+  int64_t q_row, k_row, v_row;
+  const float* g;
+  int64_t g_row;
+  float* state;
+  void* o;
+  float scale;
+  int heads, rep, dk, dv;
+};
+
+// S = exp(g) S + k v^T, o = scale S^T q for one (sequence, head) per block: the
+// state is read and written once, which is all the time there is (HBM bound).
+// A thread owns four columns of S and every (256 / (dv / 4))-th row; the rows'
+// parts of o meet in LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void la_step(StepLaunch p) {
+  using la::f32x4;
+  __shared__ float red[64 * 16 * 4];                   // rows in flight * dv <= 1024 values
+  __shared__ float sk[128], sq[128];
+  const int64_t b = blockIdx.x / p.heads;
+  const int h = blockIdx.x % p.heads;
+  const int tid = threadIdx.x;
+  const int quads = p.dv / 4, groups = 256 / quads;    // 4 .. 32, 64 .. 8
+  const T* q = static_cast<const T*>(p.q) + b * p.q_row + (h / p.rep) * p.dk;
+  const T* k = static_cast<const T*>(p.k) + b * p.k_row + (h / p.rep) * p.dk;
+  const T* v = static_cast<const T*>(p.v) + b * p.v_row + h * p.dv;
+  const int rg = tid / quads, c = (tid % quads) * 4;
+  const bool on = rg < groups;
+  float* s = p.state + (int64_t(blockIdx.x) * p.dk) * p.dv;
+  for (int i = tid; i < p.dk; i += 256) {
+    sk[i] = to_float(k[i]);
+    sq[i] = p.scale * to_float(q[i]);
+  }
+  const float a = fast_exp2(p.g[b * p.g_row + h] * kLog2e);
+  f32x4 vv = {0.0f, 0.0f, 0.0f, 0.0f}, o = vv;
+  if (on)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) vv[r] = to_float(v[c + r]);
+  block_sync();
+  if (on) {
+    for (int i = rg; i < p.dk; i += groups) {
+      f32x4 x;
+      __builtin_memcpy(&x, s + i * p.dv + c, 16);
+      const float kk = sk[i], qq = sq[i];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = __builtin_fmaf(a, x[r], kk * vv[r]);
+        o[r] = __builtin_fmaf(qq, x[r], o[r]);
+      }
+      __builtin_memcpy(s + i * p.dv + c, &x, 16);
+    }
+    *reinterpret_cast<f32x4*>(&red[rg * p.dv + c]) = o;
+  }
+  block_sync();
+  if (tid < p.dv) {
+    float t = 0.0f;
+    for (int r = 0; r < groups; ++r) t += red[r * p.dv + tid];
+    T* out = static_cast<T*>(p.o) + (b * p.heads + h) * int64_t(p.dv) + tid;
+    if constexpr (sizeof(T) == 2) *out = static_cast<T>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(t)));
+    else *out = t;
+  }
+}
+
+View view_of(const void* p, int64_t row, int div, int e) {
+  View v;
+  v.p = p;
+  v.row = row;
+  v.div = div;
+  v.vec = reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * e % 16 == 0;
+  return v;
+}
+
+constexpr size_t kAlign = 256;
+size_t round_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+}  // namespace
+
+// Segments.  One block runs a segment of one head in order.  Where sequences
+// times heads do not fill the compute units, sequences are cut: each segment's
+// own state is found first (reading k and v once more), the states are joined,
+// then all segments run at once.
+LaPlan plan_la(const LaShape& s, bool backward) {
+  LaPlan p;
+  Grid& g = p.grid;
+  g.seqs = s.seqs;
+  g.tokens = s.tokens;
+  g.L = s.packed ? 0 : (s.seqs > 0 ? s.tokens / s.seqs : 0);
+  const int64_t kBlocks = 1024, kLeast = 512, kChunk = 64;
+  const int64_t rows = s.seqs * s.heads;
+  int64_t len = s.packed ? s.tokens : g.L;      // the longest a sequence can be
+  int64_t seg = len;
+  if (rows < 512 || s.packed) {
+    seg = (s.tokens * s.heads + kBlocks - 1) / kBlocks;
+    if (seg < kLeast) seg = kLeast;
+  }
+  if (backward && seg > 1024) seg = 1024;
+  if (seg > len) seg = len;
+  seg = (seg + kChunk - 1) / kChunk * kChunk;
+  if (seg < kChunk) seg = kChunk;
+  g.seg_len = seg;
+  g.segs = s.packed ? 0 : (len + seg - 1) / seg;
+  if (!s.packed && g.segs < 1) g.segs = 1;
+  g.slots = s.packed ? s.tokens / seg + s.seqs : s.seqs * g.segs;
+  p.cut = len > seg;
+
+  const size_t state = static_cast<size_t>(s.dk) * s.dv * s.heads * 4;
+  const size_t per_slot = round_up(static_cast<size_t>(g.slots) * s.heads * 4);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += round_up(bytes);
+    return o;
+  };
+  if (p.cut || backward) {
+    p.states = take(state * g.slots);
+    p.decay = take(per_slot);
+  }
+  if (backward) {
+    p.rev_states = take(state * g.slots);
+    p.rev_decay = take(per_slot);
+    p.fwd_last = take(state * s.seqs);
+    p.u = take(static_cast<size_t>(s.tokens) * s.heads * 4);
+    p.head_part = take(per_slot);
+    if (s.heads != s.key_heads) {
+      p.dq = take(static_cast<size_t>(s.tokens) * s.heads * s.dk * 4);
+      p.dk = take(static_cast<size_t>(s.tokens) * s.heads * s.dk * 4);
+    }
+  }
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream) {
+  const LaShape& s = a.shape;
+  const int e = a.dtype == MSSM_BFLOAT16 ? 2 : 4;
+  const int rep = static_cast<int>(s.heads / s.key_heads);
+  char* w = static_cast<char*>(ws);
+  PassArgs p;
+  p.grid = plan.grid;
+  p.grid.offsets = a.offsets;
+  p.x = view_of(a.q, a.q_row, rep, e);
+  p.y = view_of(a.k, a.k_row, rep, e);
+  p.z = view_of(a.v, a.v_row, 1, e);
+  p.g = a.g;
+  p.g_row = a.per_token ? s.heads : 0;
+  p.heads = static_cast<int>(s.heads);
+  p.dA = static_cast<int>(s.dk);
+  p.dB = static_cast<int>(s.dv);
+  p.scale = a.scale;
+  p.sA = s.dv;
+  p.sB = 1;
+  hipError_t err;
+  if (plan.cut) {
+    float* st = reinterpret_cast<float*>(w + plan.states);
+    float* dec = reinterpret_cast<float*>(w + plan.decay);
+    PassArgs q = p;
+    q.seg_out = st;
+    q.seg_decay = dec;
+    if ((err = la::pass_state(a.dtype, q, stream)) != hipSuccess) return err;
+    if ((err = launch_carry_states(false, p.grid, p.heads, s.dk * s.dv, a.state, dec, st, nullptr,
+                                   stream)) != hipSuccess)
+      return err;
+    p.seg_states = st;
+  }
+  p.init = a.state;
+  p.last = a.last;
+  p.out = a.o;
+  return la::pass_fwd(a.dtype, p, stream);
+}
+
+hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, void* ws,
+                         hipStream_t stream) {
+  const LaShape& s = a.shape;
+  const bool bf16 = a.dtype == MSSM_BFLOAT16;
+  const int e = bf16 ? 2 : 4;
+  const int rep = static_cast<int>(s.heads / s.key_heads);
+  char* w = static_cast<char*>(ws);
+  auto at = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
+  const View q = view_of(a.q, a.q_row, rep, e), k = view_of(a.k, a.k_row, rep, e);
+  const View v = view_of(a.v, a.v_row, 1, e);
+  const View g = view_of(d.dout, s.heads * s.dv, 1, e);
+  PassArgs c;
+  c.grid = plan.grid;
+  c.grid.offsets = a.offsets;
+  c.g = a.g;
+  c.g_row = a.per_token ? s.heads : 0;
+  c.heads = static_cast<int>(s.heads);
+  c.scale = a.scale;
+  const int64_t size = s.dk * s.dv;
+  hipError_t err;
+  const bool fwd_last = d.dlast != nullptr;     // dg needs <dS_last, S_last>
+  const bool fwd_states = plan.cut || fwd_last;
+  if (fwd_states) {
+    PassArgs p = c;
+    p.y = k, p.z = v;
+    p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
+    p.sA = s.dv, p.sB = 1;
+    p.every_segment = fwd_last;
+    p.seg_out = at(plan.states);
+    p.seg_decay = at(plan.decay);
+    if ((err = la::pass_state(a.dtype, p, stream)) != hipSuccess) return err;
+    if ((err = launch_carry_states(false, c.grid, c.heads, size, a.state, at(plan.decay),
+                                   at(plan.states), fwd_last ? at(plan.fwd_last) : nullptr,
+                                   stream)) != hipSuccess)
+      return err;
+  }
+  if (plan.cut) {
+    PassArgs p = c;
+    p.y = q, p.z = g;
+    p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
+    p.sA = s.dv, p.sB = 1;
+    p.seg_out = at(plan.rev_states);
+    p.seg_decay = at(plan.rev_decay);
+    if ((err = la::pass_state_rev(a.dtype, p, stream)) != hipSuccess) return err;
+    if ((err = launch_carry_states(true, c.grid, c.heads, size, d.dlast, at(plan.rev_decay),
+                                   at(plan.rev_states), nullptr, stream)) != hipSuccess)
+      return err;
+  }
+  {
+    PassArgs p = c;
+    p.x = g, p.y = v, p.z = k, p.e = q;
+    p.dA = static_cast<int>(s.dv), p.dB = static_cast<int>(s.dk);
+    p.sA = 1, p.sB = s.dv;
+    p.init = a.state;
+    p.seg_states = fwd_states ? at(plan.states) : nullptr;
+    p.out = rep > 1 ? at(plan.dq) : d.dq;
+    p.out_f32 = rep > 1;
+    p.u = at(plan.u);
+    if ((err = la::pass_dq(a.dtype, p, stream)) != hipSuccess) return err;
+  }
+  {
+    PassArgs p = c;
+    p.x = v, p.y = g, p.z = q, p.e = k;
+    p.dA = static_cast<int>(s.dv), p.dB = static_cast<int>(s.dk);
+    p.sA = 1, p.sB = s.dv;
+    p.init = d.dlast;
+    p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
+    p.fwd_states = plan.cut ? at(plan.states) : nullptr;
+    p.fwd_last = fwd_last ? at(plan.fwd_last) : nullptr;
+    p.out = rep > 1 ? at(plan.dk) : d.dk;
+    p.out_f32 = rep > 1;
+    p.u = at(plan.u);
+    p.dg = a.per_token ? d.dg : nullptr;
+    p.head_part = a.per_token ? nullptr : at(plan.head_part);
+    if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;
+  }
+  {
+    PassArgs p = c;
+    p.x = k, p.y = q, p.z = g;
+    p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
+    p.sA = s.dv, p.sB = 1;
+    p.init = d.dlast;
+    p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
+    p.last = d.dstate;
+    p.out = d.dv;
+    if ((err = la::pass_dv(a.dtype, p, stream)) != hipSuccess) return err;
+  }
+  if (rep > 1 && s.tokens > 0) {
+    const int64_t quads = s.tokens * s.key_heads * s.dk / 4;
+    const dim3 grid(static_cast<uint32_t>((quads + 255) / 256));
+    const int dk = static_cast<int>(s.dk);
+    for (int i = 0; i < 2; ++i) {
+      const float* part = at(i ? plan.dk : plan.dq);
+      void* out = i ? d.dk : d.dq;
+      if (bf16)
+        hipLaunchKernelGGL(la_sum_heads<uint16_t>, grid, dim3(256), 0, stream, part,
+                           static_cast<uint16_t*>(out), quads, dk, rep);
+      else
+        hipLaunchKernelGGL(la_sum_heads<float>, grid, dim3(256), 0, stream, part,
+                           static_cast<float*>(out), quads, dk, rep);
+      if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+  }
+  if (!a.per_token) {
+    hipLaunchKernelGGL(la_sum_slots, dim3(static_cast<uint32_t>(s.heads)), dim3(256), 0, stream,
+                       at(plan.head_part), d.dg, plan.grid.slots, c.heads);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_la_step(const LaArgs& a, float* state, hipStream_t stream) {
+  const LaShape& s = a.shape;
+  StepLaunch p{a.q, a.k, a.v, a.q_row, a.k_row, a.v_row, a.g, a.per_token ? s.heads : 0,
+               state, a.o, a.scale, static_cast<int>(s.heads),
+               static_cast<int>(s.heads / s.key_heads), static_cast<int>(s.dk),
+               static_cast<int>(s.dv)};
+  const dim3 grid(static_cast<uint32_t>(s.seqs * s.heads));
+  if (a.dtype == MSSM_BFLOAT16)
+    hipLaunchKernelGGL(la_step<uint16_t>, grid, dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL(la_step<float>, grid, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mssm

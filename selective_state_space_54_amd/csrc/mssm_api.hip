@@ -12,10 +12,7 @@ namespace {
 
 thread_local char g_last_error[256] = "";
 
-void set_hip_error(hipError_t e, const char* where) {
-  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", where, hipGetErrorString(e),
-                static_cast<int>(e));
-}
+using mssm::set_hip_error;
 
 bool mul_ok(int64_t a, int64_t b, int64_t* out) {
   if (a == 0 || b == 0) { *out = 0; return true; }
@@ -53,6 +50,15 @@ mssm_status check_grid(const mssm::ScanPlan& p, int64_t batch, int64_t D, int64_
 }
 
 }  // namespace
+
+namespace mssm {
+
+void set_hip_error(hipError_t e, const char* where) {
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", where, hipGetErrorString(e),
+                static_cast<int>(e));
+}
+
+}  // namespace mssm
 
 extern "C" {
 

@@ -8,9 +8,13 @@
 
 #include <mutex>
 
+#include "la_args.h"
 #include "mssm.h"
 
 namespace mssm {
+
+// Records what mssm_last_error_string returns on this thread.
+void set_hip_error(hipError_t e, const char* where);
 
 // Current value of a tuning setting (settings.hip): from the environment,
 // read once, or from mssm_set_tuning.
@@ -396,5 +400,90 @@ size_t fused_workspace_bound(int64_t batch, int64_t L, int64_t D, int64_t N, int
 int choose_fused_cpl(int64_t D);
 FusedStatus launch_fused(const FusedArgs& a, const FusedPlan& f, void* workspace,
                          hipStream_t stream);
+
+// ---- linear attention with a decay for each head ------------------------------------------------
+
+struct LaShape {
+  int64_t seqs = 0, tokens = 0;   // tokens of all sequences together
+  bool packed = false;            // lengths from device offsets; else tokens / seqs each
+  int64_t key_heads = 0, heads = 0, dk = 0, dv = 0;
+};
+
+struct LaArgs {
+  LaShape shape;
+  const void* q = nullptr;        // [tokens, key_heads, dk], token rows q_row elements apart
+  const void* k = nullptr;
+  const void* v = nullptr;        // [tokens, heads, dv]
+  int64_t q_row = 0, k_row = 0, v_row = 0;
+  const float* g = nullptr;       // [tokens, heads], or [heads]
+  bool per_token = true;
+  const int64_t* offsets = nullptr;
+  const float* state = nullptr;   // [seqs, heads, dk, dv] or null
+  float* last = nullptr;          // the same, or null
+  void* o = nullptr;              // [tokens, heads, dv]
+  float scale = 1.0f;
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+
+struct LaGrads {
+  const void* dout = nullptr;     // [tokens, heads, dv]
+  const float* dlast = nullptr;   // gradient of the last states, or null
+  void* dq = nullptr;
+  void* dk = nullptr;
+  void* dv = nullptr;
+  float* dg = nullptr;            // as g
+  float* dstate = nullptr;        // gradient of the initial states, or null
+};
+
+// Segments of a call (`cut`: some sequence may have more than one) and the
+// workspace: each segment's state and decay; backward also those of the
+// adjoint, the states after the sequences, the queries' part of dg, and with
+// shared keys the heads' dq and dk in float32.
+struct LaPlan {
+  la::Grid grid;
+  bool cut = false;
+  size_t states = 0, decay = 0, rev_states = 0, rev_decay = 0, fwd_last = 0, u = 0;
+  size_t head_part = 0, dq = 0, dk = 0;
+  size_t bytes = 0;
+};
+LaPlan plan_la(const LaShape& s, bool backward);
+hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream);
+hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, void* ws,
+                         hipStream_t stream);
+// One token for each sequence (shape.tokens == shape.seqs), the state in place.
+hipError_t launch_la_step(const LaArgs& a, float* state, hipStream_t stream);
+
+// ---- layer norm ----------------------------------------------------------------------------------
+
+struct NormArgs {
+  const void* x = nullptr;        // [rows, D]
+  const void* residual = nullptr; // or null
+  const float* weight = nullptr;  // [D]
+  const float* bias = nullptr;    // [D] or null
+  void* y = nullptr;
+  void* sum = nullptr;            // x + residual, with residual
+  float* mean = nullptr;          // [rows], or null
+  float* rstd = nullptr;          // with mean
+  float eps = 0.0f;
+  int64_t rows = 0, D = 0;
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+struct NormBwdArgs {
+  const void* dy = nullptr;
+  const void* dsum = nullptr;     // or null
+  const void* x = nullptr;        // what was normalised
+  const float* weight = nullptr;
+  const float* mean = nullptr;
+  const float* rstd = nullptr;
+  void* dx = nullptr;
+  float* dweight = nullptr;
+  float* dbias = nullptr;         // or null
+  int64_t rows = 0, D = 0;
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+bool norm_size_supported(int64_t D);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+size_t norm_bwd_workspace(int64_t rows, int64_t D, mssm_dtype dtype);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, void* ws, hipStream_t stream);
 
 }  // namespace mssm

@@ -28,6 +28,8 @@ MSSM_BFLOAT16 = 1
 MSSM_BBAR_EULER = 0
 MSSM_BBAR_ZOH = 1
 _BBAR = {"euler": MSSM_BBAR_EULER, "zoh": MSSM_BBAR_ZOH}
+MSSM_DECAY_PER_HEAD = 0
+MSSM_DECAY_PER_TOKEN = 1
 MSSM_TUNE_SCAN_ORDER = 0
 MSSM_TUNE_CHUNK_LEN = 1
 MSSM_TUNE_CHAINS_PER_LANE = 2
@@ -93,6 +95,23 @@ _SIGNATURES = {
     "mssm_selective_ssm_fused_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                                     ctypes.c_size_t, _i64, _i64, _i64, _i64,
                                                     _i64, ctypes.c_int, _vp]),
+    "mssm_linear_attention_supports": (ctypes.c_int, [_i64, _i64]),
+    "mssm_linear_attention_workspace_size": (ctypes.c_int, [_i64] * 6 + [ctypes.c_int] * 3 +
+                                             [ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_linear_attention_fwd": (ctypes.c_int, [_vp] * 8 + [ctypes.c_float, ctypes.c_int, _vp,
+                                                             ctypes.c_size_t] + [_i64] * 9 +
+                                  [ctypes.c_int, _vp]),
+    "mssm_linear_attention_step": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float, ctypes.c_int] +
+                                   [_i64] * 8 + [ctypes.c_int, _vp]),
+    "mssm_linear_attention_bwd": (ctypes.c_int, [_vp] * 13 + [ctypes.c_float, ctypes.c_int, _vp,
+                                                              ctypes.c_size_t] + [_i64] * 9 +
+                                  [ctypes.c_int, _vp]),
+    "mssm_layer_norm_fwd": (ctypes.c_int, [_vp] * 8 + [ctypes.c_float, _i64, _i64, ctypes.c_int,
+                                                       _vp]),
+    "mssm_layer_norm_bwd_workspace_size": (ctypes.c_int, [_i64, _i64, ctypes.c_int,
+                                                          ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_layer_norm_bwd": (ctypes.c_int, [_vp] * 10 + [ctypes.c_size_t, _i64, _i64, ctypes.c_int,
+                                                        _vp]),
 }
 
 
@@ -698,3 +717,294 @@ def selective_scan_bwd(x, delta, A, B, C, dout, *, Dskip=None, z=None, h0=None, 
     grads, ws = _alloc_grads(x, A, Dskip, z, h0, stream)
     return mssm_selective_scan_bwd(x, delta, A, B, C, dout, grads, ws, Dskip=Dskip, z=z, h0=h0,
                                    stream=stream)
+
+
+# ---- linear attention with a decay for each head ---------------------------------------------
+
+def mssm_linear_attention_supports(dk: int, dv: int) -> bool:
+    return bool(load().mssm_linear_attention_supports(dk, dv))
+
+
+def mssm_linear_attention_workspace_size(seqs, L, key_heads, heads, dk, dv, dtype, *,
+                                         packed=False, backward=False) -> int:
+    """Workspace bytes; ``packed``: with seq_offsets (L is then all tokens)."""
+    out = ctypes.c_size_t(0)
+    _check(load().mssm_linear_attention_workspace_size(
+        seqs, L, key_heads, heads, dk, dv, int(packed), int(backward), _dtype_code(dtype),
+        ctypes.byref(out)), "mssm_linear_attention_workspace_size")
+    return out.value
+
+
+def _token_rows(t, name, dtype, shape, device):
+    """Checks a [tokens.., heads, d] tensor whose tokens are evenly spaced (a view into a
+    wider projection's output is one) and returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return shape[-2] * shape[-1]
+    st, dense = t.stride(), shape[-2] * shape[-1]
+    lead = [i for i in range(len(shape) - 2) if shape[i] > 1]      # strides of single entries say nothing
+    row = st[lead[-1]] if lead else dense
+    even = len(lead) < 2 or st[0] == shape[1] * row
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]) or row < dense or not even:
+        raise ValueError(f"{name} must hold its heads densely, at an even token stride")
+    return row
+
+
+def _la_check(q, k, v, log_decay, seq_offsets, single=False):
+    """Sizes, token rows and the decay's form of a linear attention call: (lead, seqs, L, Hk, H,
+    dk, dv, rows, decay), lead the token dimensions."""
+    lead_dims = 1 if single or seq_offsets is not None else 2
+    if q.dim() != lead_dims + 2 or v.dim() != lead_dims + 2:
+        lead = "[tokens" if lead_dims == 1 else "[batch, L"
+        raise ValueError(f"q, k and v must be {lead}, heads, head size]")
+    _dtype_code(q.dtype)
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    lead = q.shape[:lead_dims]
+    key_heads, dk = q.shape[-2:]
+    heads, dv = v.shape[-2:]
+    rows = (_token_rows(q, "q", q.dtype, q.shape, dev), _token_rows(k, "k", q.dtype, q.shape, dev),
+            _token_rows(v, "v", q.dtype, lead + (heads, dv), dev))
+    if log_decay.dim() == 1:
+        _dense(log_decay, "log_decay", torch.float32, (heads,), dev)
+        decay = MSSM_DECAY_PER_HEAD
+    else:
+        _dense(log_decay, "log_decay", torch.float32, lead + (heads,), dev)
+        decay = MSSM_DECAY_PER_TOKEN
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+            raise ValueError("seq_offsets must be [sequences + 1]")
+        _dense(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
+        seqs, L = seq_offsets.shape[0] - 1, lead[0]
+    else:
+        seqs, L = lead[0], 1 if single else lead[1]
+    return lead, seqs, L, key_heads, heads, dk, dv, rows, decay
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def mssm_linear_attention_fwd(q, k, v, log_decay, o, workspace, *, scale, state=None,
+                              last_state=None, seq_offsets=None, stream=None):
+    """o (and last_state) <- linear attention (see linear_attention); workspace is a uint8
+    GPU tensor of mssm_linear_attention_workspace_size bytes, or None where that is 0."""
+    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
+    dev = q.device
+    _dense(o, "o", q.dtype, lead + (H, dv), dev)
+    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    _check_optional(last_state, "last_state", torch.float32, (seqs, H, dk, dv), dev)
+    _check(load().mssm_linear_attention_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(o),
+        _ptr(last_state), scale, decay, _ptr(workspace), _bytes_of(workspace), seqs, L, Hk, H, dk,
+        dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_fwd")
+    return o
+
+
+def linear_attention(q, k, v, log_decay, *, scale=None, state=None, seq_offsets=None,
+                     return_state=False, stream=None):
+    """Linear attention with a decay for each head over whole prompts:
+    S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t.
+
+    q, k [batch, L, key_heads, dk], v [batch, L, heads, dv]; or with ``seq_offsets`` (int64
+    [sequences + 1] on the GPU) packed sequences, q, k [tokens, key_heads, dk] and v [tokens,
+    heads, dv].  Views whose tokens are evenly spaced (slices of a fused projection) are taken
+    as they are.  log_decay float32 [batch, L, heads] ([tokens, heads]) or [heads].  scale
+    defaults to dk ** -0.5.  ``state`` float32 [sequences, heads, dk, dv] is the state before
+    the first token (default zero).  Returns o, or (o, last state)."""
+    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
+    dev = q.device
+    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    nbytes = mssm_linear_attention_workspace_size(seqs, L, Hk, H, dk, dv, q.dtype,
+                                                  packed=seq_offsets is not None)
+    with _on(stream):
+        o = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
+        last = (torch.empty((seqs, H, dk, dv), dtype=torch.float32, device=dev)
+                if return_state else None)
+        ws = _workspace(nbytes, dev)
+    _check(load().mssm_linear_attention_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(o),
+        _ptr(last), dk ** -0.5 if scale is None else scale, decay, _ptr(ws), nbytes, seqs, L, Hk,
+        H, dk, dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_fwd")
+    return (o, last) if return_state else o
+
+
+def mssm_linear_attention_step(q, k, v, log_decay, state, o, *, scale, stream=None):
+    """One token for each sequence: state [batch, heads, dk, dv] float32 is updated in place,
+    o [batch, heads, dv] receives the output; q, k are [batch, key_heads, dk], v [batch, heads,
+    dv], log_decay [batch, heads] or [heads]."""
+    lead, seqs, _, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, None, single=True)
+    _dense(state, "state", torch.float32, (seqs, H, dk, dv), q.device)
+    _dense(o, "o", q.dtype, (seqs, H, dv), q.device)
+    _check(load().mssm_linear_attention_step(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o), scale, decay, seqs, Hk,
+        H, dk, dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_step")
+    return o
+
+
+def linear_attention_step(q, k, v, log_decay, state, *, scale=None, stream=None):
+    """Allocate o, run mssm_linear_attention_step (state updated in place), return o.  scale
+    defaults to dk ** -0.5."""
+    if v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head size]")
+    with _on(stream):
+        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    return mssm_linear_attention_step(q, k, v, log_decay, state, o,
+                                      scale=q.shape[-1] ** -0.5 if scale is None else scale,
+                                      stream=stream)
+
+
+def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, scale, state=None,
+                              dstate=None, seq_offsets=None, stream=None):
+    """Gradients of sum(dout * o) + sum(dstate * last state) of linear_attention.  ``grads``
+    maps dq, dk, dv (of the inputs' dtype), dlog_decay (float32) and, for the initial state's,
+    dstate to dense tensors that are overwritten."""
+    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
+    dev = q.device
+    _dense(dout, "dout", q.dtype, lead + (H, dv), dev)
+    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    _check_optional(dstate, "dstate", torch.float32, (seqs, H, dk, dv), dev)
+    shapes = {"dq": (q.dtype, tuple(q.shape)), "dk": (q.dtype, tuple(q.shape)),
+              "dv": (q.dtype, tuple(v.shape)),
+              "dlog_decay": (torch.float32, tuple(log_decay.shape)),
+              "dstate": (torch.float32, (seqs, H, dk, dv))}
+    for name, t in grads.items():
+        if name not in shapes:
+            raise ValueError(f"unknown gradient {name}")
+        _dense(t, name, *shapes[name], dev)
+    g = lambda name: _ptr(grads.get(name))
+    _check(load().mssm_linear_attention_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(dout),
+        _ptr(dstate), g("dq"), g("dk"), g("dv"), g("dlog_decay"), g("dstate"), scale, decay,
+        _ptr(workspace), _bytes_of(workspace), seqs, L, Hk, H, dk, dv, *rows, _DTYPES[q.dtype],
+        _stream_handle(stream)), "mssm_linear_attention_bwd")
+    return grads
+
+
+def linear_attention_bwd(q, k, v, log_decay, dout, *, scale=None, state=None, dstate=None,
+                         seq_offsets=None, stream=None):
+    """Allocate the gradients and the workspace with torch, then run mssm_linear_attention_bwd;
+    returns the dict of gradients (dq, dk, dv, dlog_decay, and dstate, the initial state's,
+    where ``state`` is given).  ``dstate`` is the gradient of the last state, if it has one."""
+    _, seqs, L, Hk, H, dk, dv, _, _ = _la_check(q, k, v, log_decay, seq_offsets)
+    dev = q.device
+    nbytes = mssm_linear_attention_workspace_size(seqs, L, Hk, H, dk, dv, q.dtype, backward=True,
+                                                  packed=seq_offsets is not None)
+    with _on(stream):
+        empty = lambda like, shape: torch.empty(shape, dtype=like.dtype, device=dev)
+        grads = {"dq": empty(q, q.shape), "dk": empty(k, k.shape), "dv": empty(v, v.shape),
+                 "dlog_decay": empty(log_decay, log_decay.shape)}
+        if state is not None:
+            grads["dstate"] = empty(state, state.shape)
+        ws = _workspace(nbytes, dev)
+    return mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, ws, state=state,
+                                     dstate=dstate, seq_offsets=seq_offsets, stream=stream,
+                                     scale=dk ** -0.5 if scale is None else scale)
+
+
+# ---- layer norm ----------------------------------------------------------------------------------
+
+def _norm_rows(x, weight):
+    if x.dim() < 1:
+        raise ValueError("x must be [.., D]")
+    _dtype_code(x.dtype)
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    D = x.shape[-1]
+    _dense(x, "x", x.dtype, x.shape, x.device)
+    _dense(weight, "weight", torch.float32, (D,), x.device)
+    return x.numel() // D if D else 0, D
+
+
+def mssm_layer_norm_fwd(x, weight, bias, y, *, residual=None, total=None, mean=None, rstd=None,
+                        eps=1e-5, stream=None):
+    """y <- layer norm of x (of total <- x + residual where a residual is given) over the last
+    dimension; mean and rstd (float32, one value a row) receive the rows' statistics."""
+    rows, D = _norm_rows(x, weight)
+    dev = x.device
+    _check_optional(bias, "bias", torch.float32, (D,), dev)
+    _dense(y, "y", x.dtype, x.shape, dev)
+    _check_optional(residual, "residual", x.dtype, x.shape, dev)
+    _check_optional(total, "total", x.dtype, x.shape, dev)
+    _check_optional(mean, "mean", torch.float32, x.shape[:-1], dev)
+    _check_optional(rstd, "rstd", torch.float32, x.shape[:-1], dev)
+    _check(load().mssm_layer_norm_fwd(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(total), _ptr(mean),
+        _ptr(rstd), eps, rows, D, _DTYPES[x.dtype], _stream_handle(stream)),
+        "mssm_layer_norm_fwd")
+    return y
+
+
+def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, return_stats=False, stream=None):
+    """Layer norm over the last dimension of x (float32 or bfloat16, dense; weight and bias
+    float32).  With ``residual``, x + residual is normalised and returned too (rounded to x's
+    type).  ``return_stats``: also the rows' mean and rstd, for layer_norm_bwd.  Returns y, or
+    (y[, total][, mean, rstd])."""
+    dev = x.device
+    with _on(stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        total = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
+        mean = rstd = None
+        if return_stats:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    mssm_layer_norm_fwd(x, weight, bias, y, residual=residual, total=total, mean=mean, rstd=rstd,
+                        eps=eps, stream=stream)
+    if total is None and not return_stats:
+        return y
+    return (y,) + ((total,) if total is not None else ()) + ((mean, rstd) if return_stats else ())
+
+
+def mssm_layer_norm_bwd_workspace_size(rows, D, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().mssm_layer_norm_bwd_workspace_size(rows, D, _dtype_code(dtype),
+                                                     ctypes.byref(out)),
+           "mssm_layer_norm_bwd_workspace_size")
+    return out.value
+
+
+def mssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, *, dsum=None,
+                        stream=None):
+    """dx, dweight (and dbias, unless None) <- gradients of the layer norm of x (what was
+    normalised) with its mean and rstd; dsum, the gradient that reaches x itself, is added to
+    dx."""
+    rows, D = _norm_rows(x, weight)
+    dev = x.device
+    _dense(dy, "dy", x.dtype, x.shape, dev)
+    _dense(mean, "mean", torch.float32, x.shape[:-1], dev)
+    _dense(rstd, "rstd", torch.float32, x.shape[:-1], dev)
+    _check_optional(dsum, "dsum", x.dtype, x.shape, dev)
+    _dense(dx, "dx", x.dtype, x.shape, dev)
+    _dense(dweight, "dweight", torch.float32, (D,), dev)
+    _check_optional(dbias, "dbias", torch.float32, (D,), dev)
+    _check(load().mssm_layer_norm_bwd(
+        _ptr(dy), _ptr(dsum), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+        _ptr(dweight), _ptr(dbias), _ptr(workspace), _bytes_of(workspace), rows, D,
+        _DTYPES[x.dtype], _stream_handle(stream)), "mssm_layer_norm_bwd")
+    return dx
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, *, dsum=None, bias=True, stream=None):
+    """Allocate the gradients and the workspace with torch, then run mssm_layer_norm_bwd;
+    returns a dict of dx, dweight and (``bias``) dbias.  x is what was normalised: with a
+    residual, the total that layer_norm returned."""
+    rows, D = _norm_rows(x, weight)
+    dev = x.device
+    nbytes = mssm_layer_norm_bwd_workspace_size(rows, D, x.dtype)
+    with _on(stream):
+        grads = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
+                 "dweight": torch.empty((D,), dtype=torch.float32, device=dev)}
+        if bias:
+            grads["dbias"] = torch.empty((D,), dtype=torch.float32, device=dev)
+        ws = _workspace(nbytes, dev)
+    mssm_layer_norm_bwd(dy, x, weight, mean, rstd, grads["dx"], grads["dweight"],
+                        grads.get("dbias"), ws, dsum=dsum, stream=stream)
+    return grads
