@@ -46,10 +46,11 @@ mssm_status shape_of(int64_t seqs, int64_t L, int64_t key_heads, int64_t heads, 
 }
 
 // A plan whose workspace and grids fit their types.
-mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm::LaPlan* plan) {
-  *plan = mssm::plan_la(s, backward);
+mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm_dtype dtype,
+                    mssm::LaPlan* plan) {
+  *plan = mssm::plan_la(s, backward, dtype == MSSM_BFLOAT16);
   int64_t n;
-  if (!product({plan->grid.slots, s.heads, s.dk, s.dv, 4 * 4}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
+  if (!product({plan->grid.slots, s.heads, 128 * 128, 4 * 4, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (!product({plan->grid.slots, s.heads}, &n) || n > kMaxBlocks) return MSSM_ERROR_NOT_SUPPORTED;
   if (backward && s.heads != s.key_heads &&
       (!product({s.tokens, s.key_heads, s.dk}, &n) || n / 1024 > kMaxBlocks - 1))
@@ -57,11 +58,14 @@ mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm::LaPlan* plan) {
   return MSSM_SUCCESS;
 }
 
+// Rows hold their heads, and a chunk's rows are reached with 32-bit offsets.
 mssm_status check_rows(const mssm::LaArgs& a) {
   const mssm::LaShape& s = a.shape;
-  return a.q_row < s.key_heads * s.dk || a.k_row < s.key_heads * s.dk || a.v_row < s.heads * s.dv
-             ? MSSM_ERROR_INVALID_VALUE
-             : MSSM_SUCCESS;
+  const int64_t most = int64_t(1) << 24;
+  if (a.q_row < s.key_heads * s.dk || a.k_row < s.key_heads * s.dk || a.v_row < s.heads * s.dv)
+    return MSSM_ERROR_INVALID_VALUE;
+  if (a.q_row > most || a.k_row > most || a.v_row > most) return MSSM_ERROR_NOT_SUPPORTED;
+  return MSSM_SUCCESS;
 }
 
 mssm_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -94,7 +98,7 @@ mssm_status mssm_linear_attention_workspace_size(int64_t seqs, int64_t L, int64_
   if (st != MSSM_SUCCESS) return st;
   *bytes = 0;
   if (seqs == 0 || heads == 0) return MSSM_SUCCESS;
-  st = plan_of(s, backward != 0, &plan);
+  st = plan_of(s, backward != 0, dtype, &plan);
   if (st == MSSM_SUCCESS) *bytes = plan.bytes;
   return st;
 }
@@ -121,7 +125,7 @@ mssm_status mssm_linear_attention_fwd(const void* q, const void* k, const void* 
   } else if (!last_state) {
     return MSSM_SUCCESS;
   }
-  if ((st = plan_of(a.shape, false, &plan)) != MSSM_SUCCESS) return st;
+  if ((st = plan_of(a.shape, false, dtype, &plan)) != MSSM_SUCCESS) return st;
   if ((st = check_workspace(workspace, workspace_bytes, plan.bytes)) != MSSM_SUCCESS) return st;
   a.q = q, a.k = k, a.v = v, a.g = log_decay;
   a.per_token = decay == MSSM_DECAY_PER_TOKEN;
@@ -190,7 +194,7 @@ mssm_status mssm_linear_attention_bwd(const void* q, const void* k, const void* 
                   "linear attention backward launch");
     }
   }
-  if ((st = plan_of(a.shape, true, &plan)) != MSSM_SUCCESS) return st;
+  if ((st = plan_of(a.shape, true, dtype, &plan)) != MSSM_SUCCESS) return st;
   if ((st = check_workspace(workspace, workspace_bytes, plan.bytes)) != MSSM_SUCCESS) return st;
   a.q = q, a.k = k, a.v = v, a.g = log_decay;
   a.per_token = per_token;

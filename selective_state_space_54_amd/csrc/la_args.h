@@ -7,13 +7,11 @@ namespace mssm {
 namespace la {
 
 // One of the tensors as a pass reads it: token rows `row` elements apart, the
-// values of head h / div at (h / div) * its head size.  vec: 16-byte loads
-// are aligned.
+// values of head h / div at (h / div) * its head size.
 struct View {
   const void* p = nullptr;
   int64_t row = 0;
   int div = 1;
-  bool vec = false;
 };
 
 // Where sequences and their segments lie.
@@ -40,16 +38,17 @@ struct PassArgs {
   float* last = nullptr;             // [seqs, heads, ..], or null
   const float* seg_states = nullptr; // [slots, heads, ..]: the state each segment starts from
   // state-only passes
-  bool every_segment = false;
   float* seg_out = nullptr;          // [slots, heads, ..]: each segment's own state
   float* seg_decay = nullptr;        // [slots, heads]
   // output
   void* out = nullptr;               // [tokens, heads, dB]
   bool out_f32 = false;              // else of the inputs' type
-  // gradient of the log decays
-  float* u = nullptr;                // [tokens, heads]: written by dq, read by dk
-  const float* fwd_states = nullptr; // dk: the forward states each segment starts from
-  const float* fwd_last = nullptr;   // dk: the forward state after each sequence
+  // gradient of the log decays: written by dq, read by dk
+  float* u = nullptr;                // [tokens, heads]
+  float* q_sums = nullptr;           // [slots, chunks_per_slot, heads]
+  float* dumps = nullptr;            // [slots, dumps_per_slot, heads, ..]: states as dq holds them
+  int64_t chunks_per_slot = 0, dumps_per_slot = 0;
+  // written by dk
   float* dg = nullptr;               // [tokens, heads], or null
   float* head_part = nullptr;        // [slots, heads]: sums of dg, or null
 };

@@ -28,7 +28,9 @@
 // and W_ij = scale exp(G_i - G_j)(q_i . k_j)(do_i . v_j).  The usual suffix sum
 // of q.dq - k.dk over the whole sequence is the same number, but as a small
 // difference of sums that grow with the length; here the sums stay inside a
-// segment, whose end value <D, S> is computed from the two states themselves.
+// chunk, and <D, S> is computed from the two states themselves, for every fourth
+// chunk from the last (the forward states are kept for those); between them it
+// follows from what q.dqc and k.dkc add and take away.
 //
 // Layout on the compute unit.  A block of four wavefronts owns one segment of
 // one head.  Wavefront w owns 16 NT columns of the value dimension: its part
@@ -49,9 +51,8 @@
 // scores and the state are rounded to bfloat16 where they are operands of the
 // output's products (the output is rounded to bfloat16 itself); where float32
 // results depend on them (the state's own update, dg) the operand is split in
-// a bfloat16 pair, hi + lo, about 16 bits (relative error about 7e-7 on
-// average).  Decays, their sums (float64 inside a chunk, kept as a float32
-// pair) and the state are 32 bits or more.
+// three bfloat16 parts, 24 bits.  Decays, their sums (float64 inside a chunk,
+// kept as a float32 pair) and the state are 32 bits or more.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -94,104 +95,131 @@ __device__ __forceinline__ void mma(f32x4& acc, const Frag<float>& a, const Frag
     acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
 }
 
-// Eight consecutive values of an LDS row.
-__device__ __forceinline__ Frag<uint16_t> frag_row(const uint16_t* p) {
+// Where an LDS tile of D columns keeps value c of row r.  A row's 16-byte
+// pieces are permuted by a pattern of the row's number modulo 8, its bits in
+// reverse, so that the same piece of eight consecutive rows falls on eight
+// different groups of four banks (row reads), and four consecutive rows of
+// eight columns spread as evenly as 8-byte accesses allow (column reads).
+template <typename T, int D>
+__device__ __forceinline__ int tile_at(int r, int c) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int f = (r & 1) << 2 | (r & 2) | (r >> 2 & 1);
+  return r * D + ((c / kPer) ^ f) * kPer + c % kPer;
+}
+
+// Eight consecutive values from p (16-byte aligned).
+__device__ __forceinline__ Frag<uint16_t> frag_at(const uint16_t* p) {
   Frag<uint16_t> f;
   const uint4 u = *reinterpret_cast<const uint4*>(p);
   __builtin_memcpy(&f.v, &u, 16);
   return f;
 }
-__device__ __forceinline__ Frag<float> frag_row(const float* p) {
+__device__ __forceinline__ Frag<float> frag_at(const float* p, const float* q) {
   Frag<float> f;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
 #pragma unroll
   for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
   return f;
 }
+__device__ __forceinline__ Frag<float> frag_at(const float* p) { return frag_at(p, p + 4); }
 
-// Values 0..3 and 16..19 from p: the order in which two 16-row result tiles
-// hold the rows of a 32-row operand.
-__device__ __forceinline__ Frag<uint16_t> frag_split(const uint16_t* p) {
-  Frag<uint16_t> f;
-  uint2 u[2] = {*reinterpret_cast<const uint2*>(p), *reinterpret_cast<const uint2*>(p + 16)};
-  __builtin_memcpy(&f.v, u, 16);
-  return f;
+// Values c .. c + 7 of row r.
+template <int D>
+__device__ __forceinline__ Frag<uint16_t> frag_row(const uint16_t* t, int r, int c) {
+  return frag_at(t + tile_at<uint16_t, D>(r, c));
 }
-__device__ __forceinline__ Frag<float> frag_split(const float* p) {
-  Frag<float> f;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
-  return f;
+template <int D>
+__device__ __forceinline__ Frag<float> frag_row(const float* t, int r, int c) {
+  return frag_at(t + tile_at<float, D>(r, c), t + tile_at<float, D>(r, c + 4));
 }
 
-// Column of an LDS tile with row pitch P over eight consecutive rows r0 + 8
-// (lane / 16) ..: lane l gets the column of its index l % 16, where indices
-// 4 c .. 4 c + 3 are the columns c0 + cstep c ...  For bfloat16 the transposing
-// LDS read gives 16 lanes four rows of sixteen columns: lane l % 16 addresses
-// four columns of one row and receives one column of the four rows.
-template <int P>
-__device__ __forceinline__ Frag<uint16_t> frag_col(const uint16_t* t, int r0, int c0, int cstep,
-                                                   int lane) {
+// Column of a tile over eight consecutive rows r0 + 8 (lane / 16) ..: lane l
+// gets the column of its index l % 16, where indices 4 c .. 4 c + 3 are the
+// columns c0 + kStep c ...  For bfloat16 the transposing LDS read gives 16 lanes
+// four rows of sixteen columns: lane l % 16 addresses four columns of one row
+// and receives one column of the four rows.
+template <int D, int kStep>
+__device__ __forceinline__ Frag<uint16_t> frag_col(const uint16_t* t, int r0, int c0, int lane) {
   using lds_ptr = __attribute__((address_space(3))) s16x4*;
-  const int r = r0 + 8 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + cstep * (lane & 3);
+  const int r = r0 + 8 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + kStep * (lane & 3);
   const s16x4 u[2] = {
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + r * P + c)),
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + (r + 4) * P + c))};
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + tile_at<uint16_t, D>(r, c))),
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + tile_at<uint16_t, D>(r + 4, c)))};
   Frag<uint16_t> f;
   __builtin_memcpy(&f.v, u, 16);
   return f;
 }
-template <int P>
-__device__ __forceinline__ Frag<float> frag_col(const float* t, int r0, int c0, int cstep,
-                                                int lane) {
+template <int D, int kStep>
+__device__ __forceinline__ Frag<float> frag_col(const float* t, int r0, int c0, int lane) {
   Frag<float> f;
-  const int c = c0 + cstep * ((lane & 15) >> 2) + (lane & 3);
+  const int c = c0 + kStep * ((lane & 15) >> 2) + (lane & 3);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = t[(r0 + 8 * (lane >> 4) + e) * P + c];
+  for (int e = 0; e < 8; ++e) f.v[e] = t[tile_at<float, D>(r0 + 8 * (lane >> 4) + e, c)];
   return f;
 }
 
-__device__ __forceinline__ void pack(Frag<uint16_t>& f, const float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = static_cast<__bf16>(v[e]);
+// Four consecutive values.
+__device__ __forceinline__ f32x4 lds_load4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
 }
-__device__ __forceinline__ void pack(Frag<float>& f, const float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = v[e];
+__device__ __forceinline__ f32x4 lds_load4(const float* p) {
+  return *reinterpret_cast<const f32x4*>(p);
 }
+
+// Two values rounded to bfloat16, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  bf16x2 v;
+  v[0] = static_cast<__bf16>(a);
+  v[1] = static_cast<__bf16>(b);
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float low_half(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_half(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
 __device__ __forceinline__ void unpack(const Frag<uint16_t>& f, float (&v)[8]) {
+  uint32_t u[4];
+  __builtin_memcpy(u, &f.v, 16);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(f.v[e]);
+  for (int i = 0; i < 4; ++i) v[2 * i] = low_half(u[i]), v[2 * i + 1] = high_half(u[i]);
 }
 __device__ __forceinline__ void unpack(const Frag<float>& f, float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = f.v[e];
 }
-// hi and lo with v = hi + lo to about 16 bits (float32: hi = v alone).
-__device__ __forceinline__ void split(const float (&v)[8], Frag<uint16_t>& hi, Frag<uint16_t>& lo) {
+
+// v as a sum of N bfloat16 parts, each the rounding of what is left: to about
+// 17 bits with two, exactly float32 with three.  (float32: v itself.)
+template <int N>
+__device__ __forceinline__ void split(const float (&v)[8], Frag<uint16_t> (&part)[N]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    hi.v[e] = static_cast<__bf16>(v[e]);
-    lo.v[e] = static_cast<__bf16>(v[e] - static_cast<float>(hi.v[e]));
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const uint32_t u = pack2(a, b);
+      __builtin_memcpy(reinterpret_cast<char*>(&part[q].v) + 4 * i, &u, 4);
+      a -= low_half(u);
+      b -= high_half(u);
+    }
   }
+}
+template <int N>
+__device__ __forceinline__ void split(const float (&v)[8], Frag<float> (&part)[N]) {
+  static_assert(N == 1, "float32 needs one part");
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[0].v[e] = v[e];
 }
 
 __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
-  bf16x2 a, b;
-  a[0] = static_cast<__bf16>(v[0]), a[1] = static_cast<__bf16>(v[1]);
-  b[0] = static_cast<__bf16>(v[2]), b[1] = static_cast<__bf16>(v[3]);
-  uint2 u;
-  __builtin_memcpy(&u.x, &a, 4);
-  __builtin_memcpy(&u.y, &b, 4);
+  const uint2 u = {pack2(v[0], v[1]), pack2(v[2], v[3])};
   __builtin_memcpy(p, &u, 8);
 }
 __device__ __forceinline__ void store4(float* p, f32x4 v) { __builtin_memcpy(p, &v, 16); }
 
 __device__ __forceinline__ void lds_store4(uint16_t* p, f32x4 v) {
-  uint2 u;
-  store4(reinterpret_cast<uint16_t*>(&u), v);
-  *reinterpret_cast<uint2*>(p) = u;
+  *reinterpret_cast<uint2*>(p) = uint2{pack2(v[0], v[1]), pack2(v[2], v[3])};
 }
 __device__ __forceinline__ void lds_store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 
@@ -250,40 +278,52 @@ __device__ __forceinline__ uint32_t logical_block() {
 // ---- tiles ----------------------------------------------------------------------------------------
 
 // C rows of D values, staged through registers: fetch issues the loads, stash
-// writes them to LDS (row pitch P).  Rows past n and columns past d are zero.
-template <typename T, int C, int D, int P>
+// writes them to LDS.  Rows past n and columns past d load a valid piece
+// instead and become zero when stashed: no branch stands between the loads, so
+// all are in flight at once (a conditional load's result is copied where the
+// branches meet, which waits for it).  In a whole chunk a thread's rows are a
+// fixed distance apart: one addition for each piece's address.  Pieces are read
+// at any alignment.
+template <typename T, int C, int D>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);              // values in a 16-byte piece
   static constexpr int kRowPieces = D / kPer;
   static constexpr int kPieces = C * kRowPieces / kThreads;
-  static_assert(C * kRowPieces % kThreads == 0, "whole pieces per thread");
+  static constexpr int kRowsApart = kThreads / kRowPieces;
+  static_assert(C * kRowPieces % kThreads == 0 && kThreads % kRowPieces == 0, "whole pieces");
   uint4 v[kPieces];
 
-  __device__ __forceinline__ void fetch(const T* base, int64_t row, int n, int d, bool vec) {
+  __device__ __forceinline__ void fetch(const T* base, uint32_t row, int n, int d) {
+    const int r = threadIdx.x / kRowPieces;
+    const int c = min(static_cast<int>(threadIdx.x % kRowPieces) * kPer, d - kPer);
+    const char* from = reinterpret_cast<const char*>(base);
+    const uint32_t bytes = row * static_cast<uint32_t>(sizeof(T));
+    if (n == C) {
+      uint32_t off = r * bytes + c * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + kThreads * i;
-      const int r = p / kRowPieces, c = (p % kRowPieces) * kPer;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n && c < d) {
-        const T* src = base + r * row + c;
-        if (vec) {
-          v[i] = *reinterpret_cast<const uint4*>(src);
-        } else {
-          T e[kPer];
+      for (int i = 0; i < kPieces; ++i, off += kRowsApart * bytes)
+        __builtin_memcpy(&v[i], from + off, 16);
+    } else {
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) e[j] = src[j];
-          __builtin_memcpy(&v[i], e, 16);
-        }
+      for (int i = 0; i < kPieces; ++i) {
+        const uint32_t off = min(r + i * kRowsApart, n - 1) * bytes + c * static_cast<uint32_t>(sizeof(T));
+        __builtin_memcpy(&v[i], from + off, 16);
       }
     }
   }
-  __device__ __forceinline__ void stash(T* lds) const {
+  __device__ __forceinline__ void stash(T* lds, int n, int d) const {
+    const int r = threadIdx.x / kRowPieces, c = static_cast<int>(threadIdx.x % kRowPieces) * kPer;
+    static_assert(kRowsApart % 8 == 0, "one pattern for all of a thread's rows");
+    uint4* to = reinterpret_cast<uint4*>(lds + tile_at<T, D>(r, c));
+    if (n == C && d == D) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + kThreads * i;
-      const int r = p / kRowPieces, c = (p % kRowPieces) * kPer;
-      *reinterpret_cast<uint4*>(lds + r * P + c) = v[i];
+      for (int i = 0; i < kPieces; ++i) to[i * kThreads] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const bool in = r + i * kRowsApart < n && c < d;
+        to[i * kThreads] = in ? v[i] : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
 };
@@ -294,21 +334,40 @@ struct Decay {
   float hi[C], lo[C];      // G, inclusive, as a float32 pair
   float ein[C];            // factor of the carried state at each token
   float w[C];              // factor of each token in the state's update
+  float fac[C];            // forward: from the token to the end of its 16 tokens;
+                           // backward: from the end of the 16 before to the token
   float all;               // exp(G_C)
 };
+
+// v of the lane a DPP control names, 0 where it names none.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), kCtrl, kRows, 0xF, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), kCtrl, kRows, 0xF, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 template <int C, bool kRev>
 __device__ __forceinline__ void decays(Decay<C>& d, float g, float scale, int lane) {
   // far below what exp can represent, so that a decay to zero (minus infinity)
   // leaves the differences finite
   g = g < -1e4f ? -1e4f : g;
+  // inclusive sums: shifts by 1, 2, 4, 8 inside rows of 16 lanes, then the last
+  // lane of row 0 (and 2) to row 1 (and 3), then lane 31 to rows 2 and 3
   double s = static_cast<double>(g) * 1.4426950408889634074;
-#pragma unroll
-  for (int o = 1; o < C; o <<= 1) {
-    const double u = __shfl_up(s, o, 64);
-    if (lane >= o) s += u;
-  }
-  const double total = __shfl(s, C - 1, 64);
+  s += dpp_f64<0x111, 0xF>(s);
+  s += dpp_f64<0x112, 0xF>(s);
+  s += dpp_f64<0x114, 0xF>(s);
+  s += dpp_f64<0x118, 0xF>(s);
+  const float fac = fast_exp2(static_cast<float>(kRev ? s : dpp_f64<0x15F, 0xF>(s) - s));
+  s += dpp_f64<0x142, 0xA>(s);
+  s += dpp_f64<0x143, 0xC>(s);
+  const uint64_t u = __builtin_bit_cast(uint64_t, s);
+  const uint32_t tl = __builtin_amdgcn_readlane(static_cast<int>(u), C - 1);
+  const uint32_t th = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), C - 1);
+  const double total = __builtin_bit_cast(double, static_cast<uint64_t>(th) << 32 | tl);
   if (lane < C) {
     const float hi = static_cast<float>(s);
     d.hi[lane] = hi;
@@ -316,42 +375,64 @@ __device__ __forceinline__ void decays(Decay<C>& d, float g, float scale, int la
     const float in = fast_exp2(hi), out = fast_exp2(static_cast<float>(total - s));
     d.ein[lane] = kRev ? out : scale * in;
     d.w[lane] = kRev ? scale * in : out;
+    d.fac[lane] = fac;
     if (lane == 0) d.all = fast_exp2(static_cast<float>(total));
   }
 }
 
+// Sum over the 16 lanes of a row, in every one of them (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float row16_sum(float v) {
+#define MSSM_LA_ROT(CTRL) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+  MSSM_LA_ROT(0x128)
+  MSSM_LA_ROT(0x124)
+  MSSM_LA_ROT(0x122)
+  MSSM_LA_ROT(0x121)
+#undef MSSM_LA_ROT
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
 // ---- the pass ----------------------------------------------------------------------------------------
 
-// kDot 0: nothing more.  1 (dq): also W and q . dqc, as one sum u for each
-// token.  2 (dk): also k . dkc, and dg from it and u.
 // kOut false: only the state over the segment (no x, no output).
-// kExact: the state enters the output's product as a bfloat16 pair.
-template <typename T, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
-struct Shape {
+// kDot 0: nothing more.  1 (dq): also W and q . dqc, as one sum u for each
+// token, and the state before some of the chunks.  2 (dk): also k . dkc, and dg
+// from it, u and those states.
+template <typename T, int C, int DA, int NT, bool kOut, int kDot>
+struct Lds {
   static constexpr int TB = 64 * NT;                        // columns of z
-  static constexpr int kPad = 32 / sizeof(T);               // 32 bytes
-  static constexpr int PA = DA + kPad, PB = TB + kPad, PP = C + 16 / sizeof(T);
-  struct Lds {
-    T x[kOut ? C * PA : 8];
-    T y[C * PA];
-    T z[C * PB];
-    T e[kDot == 1 ? C * PB : 8];
-    T p[kOut ? C * PP : 8];
-    Decay<C> d;
-    float dot[kDot ? 4 : 1][C];
-    float col[kDot == 1 ? 4 : 1][C];
-    float sum[kDot ? C : 1];
-  };
+  static constexpr int PP = C + 16 / sizeof(T);             // row pitch of p
+  T x[kOut ? C * DA : 8];
+  T y[C * DA];
+  T z[C * TB];
+  T e[kDot == 1 ? C * TB : 8];
+  T p[kOut ? C * PP : 8];
+  Decay<C> d[2];
+  float dot[kDot ? 4 : 1][C];
+  float rows[kDot == 1 ? 2 : 1][C];
+  float cols[kDot == 1 ? 4 : 1][C];
+  float edge[4];
 };
 
+// Of the chunks of a segment, those whose carried-through part of dg is computed
+// from the two states themselves: the last and every kStride-th before it.  The
+// others get it from the next chunk's, by what enters and leaves in between.
+template <int C>
+constexpr int kStride = 256 / C;
+
 template <typename T, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
-__global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
-  using S = Shape<T, C, DA, NT, kRev, kOut, kDot>;
+__global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr bool kExact = kBf16 && kDot != 0;
-  constexpr int NR = C / 16, NK = C / 32, NM = DA / 16;
-  constexpr int PA = S::PA, PB = S::PB, PP = S::PP;
-  __shared__ __align__(16) typename S::Lds m;
+  constexpr int kParts = kBf16 ? 3 : 1;                    // of the weighted z
+  constexpr int kStateParts = kBf16 && kDot != 0 ? 3 : 1;  // of the state as an operand
+  constexpr int NR = C / 16, NK = C / 32, NM = DA / 16, TB = 64 * NT;
+  constexpr int PP = Lds<T, C, DA, NT, kOut, kDot>::PP;
+  __shared__ __align__(16) Lds<T, C, DA, NT, kOut, kDot> m;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -368,24 +449,21 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
   }
   // a state-only pass has nothing to do for the segment that no other follows
   const bool last_seg = kRev ? at.local == 0 : at.local == at.count - 1;
-  const bool first_seg = kRev ? at.local == at.count - 1 : at.local == 0;
-  if (!kOut && last_seg && !p.every_segment) return;
+  if (!kOut && last_seg) return;
 
   // columns of this wavefront: with two tiles, lane group g4's rows 4 g4 + r of
-  // both are the eight consecutive columns 8 g4 + 4 t + r
+  // both are the eight consecutive columns 8 g4 + 4 t + r.  The state's rows are
+  // paired the same way.
   constexpr int kStep = NT == 2 ? 8 : 4;
   const int c_wave = 16 * NT * wave;
   auto col_of = [&](int t, int c) { return c_wave + kStep * (c >> 2) + 4 * t + (c & 3); };
 
-  const T* X = kOut ? static_cast<const T*>(p.x.p) + at.start * p.x.row + (h / p.x.div) * int64_t(p.dA) : nullptr;
-  const T* Y = static_cast<const T*>(p.y.p) + at.start * p.y.row + (h / p.y.div) * int64_t(p.dA);
-  const T* Z = static_cast<const T*>(p.z.p) + at.start * p.z.row + (h / p.z.div) * int64_t(p.dB);
-  const T* E = kDot ? static_cast<const T*>(p.e.p) + at.start * p.e.row + (h / p.e.div) * int64_t(p.dB) : nullptr;
-  const float* G = p.g + (p.g_row ? at.start * p.g_row : 0) + h;
   const int64_t sh = (at.seq * p.heads + h) * (int64_t(p.dA) * p.dB);        // per sequence
   const int64_t wh = (slot * p.heads + h) * (int64_t(p.dA) * p.dB);          // per segment
 
-  // the state: rows 16 mt + 4 g4 + r of dA, column col_of(t, l16)
+  // the state: tile mt's row 4 g4 + r is row 32 (mt / 2) + 8 g4 + 4 (mt % 2) + r
+  // of dA, its column l16 is column col_of(t, l16)
+  auto row_of = [&](int mt, int r) { return 32 * (mt >> 1) + 8 * g4 + 4 * (mt & 1) + r; };
   f32x4 s[NM][NT];
   {
     const float* init = !kOut ? nullptr
@@ -398,7 +476,7 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
         const int c = col_of(t, l16);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int a = 16 * mt + 4 * g4 + r;
+          const int a = row_of(mt, r);
           s[mt][t][r] = init && a < p.dA && c < p.dB ? init[a * p.sA + c * p.sB] : 0.0f;
         }
       }
@@ -406,50 +484,108 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
 
   const int chunks = static_cast<int>((at.len + C - 1) / C);
   const float scale = p.scale;
-  Tile<T, C, DA, PA> tx, ty;
-  Tile<T, C, S::TB, PB> tz, te;
-  float gv = 0.0f;
-  auto fetch = [&](int c) {
-    const int64_t t0 = int64_t(c) * C;
-    const int n = static_cast<int>(min(at.len - t0, int64_t(C)));
-    if constexpr (kOut) tx.fetch(X + t0 * p.x.row, p.x.row, n, p.dA, p.x.vec);
-    ty.fetch(Y + t0 * p.y.row, p.y.row, n, p.dA, p.y.vec);
-    tz.fetch(Z + t0 * p.z.row, p.z.row, n, p.dB, p.z.vec);
-    if constexpr (kDot == 1) te.fetch(E + t0 * p.e.row, p.e.row, n, p.dB, p.e.vec);
-    if (wave == 0) gv = lane < n ? G[p.g_row ? (t0 + lane) * p.g_row : 0] : 0.0f;
+  // A chunk's tiles on their way from memory.  The loads run one chunk ahead of
+  // their use, or two, with a second set of registers where state, results and
+  // both sets leave room for two blocks on a compute unit (256 registers).
+  // The log decays come first, they are wanted first.
+  struct Stage {
+    float g;
+    Tile<T, C, DA> x, y;
+    Tile<T, C, TB> z, e;
   };
-
-  // dg: what crosses the segment's end, <D, S> of the states there
-  float edge = 0.0f, head_sum = 0.0f;
-  if constexpr (kDot == 2) {
-    const float* ds = p.seg_states ? p.seg_states + wh : nullptr;
-    const float* ss = p.fwd_states ? p.fwd_states + wh + int64_t(p.heads) * p.dA * p.dB : nullptr;
-    if (first_seg) ds = p.init ? p.init + sh : nullptr, ss = p.fwd_last ? p.fwd_last + sh : nullptr;
-    if (ds && ss) {
-      float part = 0.0f;
-      const int n = p.dA * p.dB;
-      for (int i = tid; i < n; i += kThreads) part = __builtin_fmaf(ds[i], ss[i], part);
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o, 64);
-      if (lane == 0) m.dot[0][wave] = part;
-      block_sync();
-      edge = (m.dot[0][0] + m.dot[0][1]) + (m.dot[0][2] + m.dot[0][3]);
-      block_sync();
+  constexpr int kStage = (kOut ? Tile<T, C, DA>::kPieces : 0) * 4 + Tile<T, C, DA>::kPieces * 4 +
+                         Tile<T, C, TB>::kPieces * 4 * (kDot == 1 ? 2 : 1);
+  constexpr int kHeld = NM * NT * 4 + (kOut ? NR * NT * 4 : 0) + (kDot == 2 ? NR * NT * 4 : 0);
+  constexpr int kSets = kHeld + 2 * kStage <= (kOut ? 112 : 128) ? 2 : 1;
+  Stage sets[kSets];
+  // Tokens of the it-th chunk worked on, and the pointers to the next chunk to load.
+  const int len = static_cast<int>(at.len);
+  auto tokens_of = [&](int it) { return min(len - (kRev ? chunks - 1 - it : it) * C, C); };
+  const int64_t first = at.start + (kRev && chunks > 0 ? int64_t(chunks - 1) * C : 0);
+  auto begin = [&](const View& v, int size) {
+    return static_cast<const T*>(v.p) + first * v.row + int64_t(h / v.div) * size;
+  };
+  const T* X = kOut ? begin(p.x, p.dA) : nullptr;
+  const T* Y = begin(p.y, p.dA);
+  const T* Z = begin(p.z, p.dB);
+  const T* E = kDot == 1 ? begin(p.e, p.dB) : nullptr;
+  const float* G = p.g + (p.g_row ? first * p.g_row : 0) + h;
+  constexpr int kAhead = kRev ? -C : C;                     // tokens from chunk to chunk
+  const uint32_t x_row = static_cast<uint32_t>(p.x.row), y_row = static_cast<uint32_t>(p.y.row);
+  const uint32_t z_row = static_cast<uint32_t>(p.z.row), e_row = static_cast<uint32_t>(p.e.row);
+  const uint32_t g_row = static_cast<uint32_t>(p.g_row);
+  auto fetch = [&](Stage& f, int it) __attribute__((always_inline)) {
+    const int n = tokens_of(it);
+    f.g = G[static_cast<uint32_t>(min(lane, n - 1)) * g_row];
+    G += kAhead * static_cast<int64_t>(g_row);
+    if constexpr (kOut) {
+      f.x.fetch(X, x_row, n, p.dA);
+      X += kAhead * static_cast<int64_t>(x_row);
     }
-  }
+    f.y.fetch(Y, y_row, n, p.dA);
+    Y += kAhead * static_cast<int64_t>(y_row);
+    f.z.fetch(Z, z_row, n, p.dB);
+    Z += kAhead * static_cast<int64_t>(z_row);
+    if constexpr (kDot == 1) {
+      f.e.fetch(E, e_row, n, p.dB);
+      E += kAhead * static_cast<int64_t>(e_row);
+    }
+  };
+  // The chunk being worked on: where its output, and what is dotted with it, begin.
+  const uint32_t o_row = static_cast<uint32_t>(p.heads) * p.dB;
+  char* out = kOut ? static_cast<char*>(p.out) +
+                         (first * o_row + int64_t(h) * p.dB) * (p.out_f32 ? 4 : int(sizeof(T)))
+                   : nullptr;
+  const T* dotted = kDot == 2 ? begin(p.e, p.dB) : nullptr;
+  float* u_at = kDot != 0 ? p.u + first * p.heads + h : nullptr;
+  float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
 
-  if (chunks > 0) fetch(kRev ? chunks - 1 : 0);
-  for (int it = 0; it < chunks; ++it) {
+  constexpr int kDumpSize = DA * TB;
+  float edge = 0.0f, head_sum = 0.0f;      // of wavefront 0
+
+  auto step = [&](int it, Stage& f, const Stage& next) __attribute__((always_inline)) {
     const int ck = kRev ? chunks - 1 - it : it;
-    const int64_t t0 = int64_t(ck) * C;
-    const int n = static_cast<int>(min(at.len - t0, int64_t(C)));
-    if constexpr (kOut) tx.stash(m.x);
-    ty.stash(m.y);
-    tz.stash(m.z);
-    if constexpr (kDot == 1) te.stash(m.e);
-    if (wave == 0) decays<C, kRev>(m.d, gv, scale, lane);
+    const int n = tokens_of(it);
+    const Decay<C>& d = m.d[it & 1];
+    if constexpr (kOut) f.x.stash(m.x, n, p.dA);
+    f.y.stash(m.y, n, p.dA);
+    f.z.stash(m.z, n, p.dB);
+    if constexpr (kDot == 1) f.e.stash(m.e, n, p.dB);
     block_sync();
-    if (it + 1 < chunks) fetch(kRev ? ck - 1 : ck + 1);
+    if (it + kSets < chunks) fetch(f, it + kSets);
+    const int back = (chunks - 1 - ck) % kStride<C>;
+    float* dump = nullptr;
+    if constexpr (kDot != 0) {
+      if (back == 0)
+        dump = p.dumps + ((slot * p.dumps_per_slot + (chunks - 1 - ck) / kStride<C>) * p.heads + h) *
+                             int64_t(kDumpSize) + tid * 4;
+    }
+    if constexpr (kDot == 1) {
+      if (dump) {
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            *reinterpret_cast<f32x4*>(dump + (mt * NT + t) * (kThreads * 4)) = s[mt][t];
+      }
+    }
+    // the tensor that the carried part is dotted with, and u: used further on
+    f32x4 ev[kDot == 2 ? NR : 1][NT];
+    float uv = 0.0f, qs = 0.0f;
+    if constexpr (kDot == 2) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t i = min(16 * r + l16, n - 1), c = min(col_of(t, 4 * g4), p.dB - 4);
+          T raw[4];
+          __builtin_memcpy(raw, dotted + (i * e_row + c), sizeof(raw));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ev[r][t][q] = to_float(raw[q]);
+        }
+      uv = u_at[static_cast<uint32_t>(min(lane, n - 1) * p.heads)];
+      qs = p.q_sums[(slot * p.chunks_per_slot + ck) * p.heads + h];
+    }
 
     f32x4 acc[NR][NT];
     if constexpr (kOut) {
@@ -458,57 +594,64 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
       constexpr int kWaveTiles = NR == 4 ? 4 : 1;
       const int rt = NR == 4 ? wave : wave >> 1;
       const int i = 16 * rt + l16;
-      const float gi = m.d.hi[i], gil = m.d.lo[i];
+      const float gi = d.hi[i], gil = d.lo[i];
       float row_sum = 0.0f;
 #pragma unroll
       for (int u = 0; u < kWaveTiles; ++u) {
         const int ct = NR == 4 ? u : wave & 1;
         const bool live = kRev ? ct >= rt : ct <= rt;
-        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = {0.0f, 0.0f, 0.0f, 0.0f};
-        f32x4 wsum = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int j0 = 16 * ct + 4 * g4;
         if (live) {
+          f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int k = 0; k < DA / 32; ++k)
-            mma(a, frag_row(m.y + (16 * ct + l16) * PA + 32 * k + 8 * g4),
-                frag_row(m.x + i * PA + 32 * k + 8 * g4));
+            mma(a, frag_row<DA>(m.y, 16 * ct + l16, 32 * k + 8 * g4),
+                frag_row<DA>(m.x, i, 32 * k + 8 * g4));
           if constexpr (kDot == 1) {
 #pragma unroll
-            for (int k = 0; k < S::TB / 32; ++k)
-              mma(b, frag_row(m.z + (16 * ct + l16) * PB + 32 * k + 8 * g4),
-                  frag_row(m.e + i * PB + 32 * k + 8 * g4));
+            for (int k = 0; k < TB / 32; ++k)
+              mma(b, frag_row<TB>(m.z, 16 * ct + l16, 32 * k + 8 * g4),
+                  frag_row<TB>(m.e, i, 32 * k + 8 * g4));
           }
-          const int j0 = 16 * ct + 4 * g4;
-          const f32x4 gj = *reinterpret_cast<const f32x4*>(&m.d.hi[j0]);
-          const f32x4 gjl = *reinterpret_cast<const f32x4*>(&m.d.lo[j0]);
+          if (ct == rt) {
+            const f32x4 gj = *reinterpret_cast<const f32x4*>(&d.hi[j0]);
+            const f32x4 gjl = *reinterpret_cast<const f32x4*>(&d.lo[j0]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const bool in = kRev ? j0 + r >= i : j0 + r <= i;
-            const float diff = (gi - gj[r]) + (gil - gjl[r]);
-            const float f = scale * fast_exp2(kRev ? -diff : diff);
-            a[r] = in ? a[r] * f : 0.0f;
-            if constexpr (kDot == 1) wsum[r] = in && j0 + r != i ? a[r] * b[r] : 0.0f;
+            for (int r = 0; r < 4; ++r) {
+              const bool in = kRev ? j0 + r >= i : j0 + r <= i;
+              const float diff = (gi - gj[r]) + (gil - gjl[r]);
+              a[r] = in ? a[r] * (scale * fast_exp2(kRev ? -diff : diff)) : 0.0f;
+              if constexpr (kDot == 1) b[r] = j0 + r != i ? a[r] * b[r] : 0.0f;
+            }
+          } else {
+            // through the boundary between the 16 tokens and what is nearer to i
+            const int edge16 = kRev ? 16 * ct - 1 : 16 * ct + 15;
+            const float diff = (gi - d.hi[edge16]) + (gil - d.lo[edge16]);
+            const float fi = scale * fast_exp2(kRev ? -diff : diff);
+            const f32x4 fj = *reinterpret_cast<const f32x4*>(&d.fac[j0]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              a[r] *= fi * fj[r];
+              if constexpr (kDot == 1) b[r] *= a[r];
+            }
           }
-          if constexpr (kDot == 1) row_sum += (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
-        }
-        lds_store4(m.p + i * PP + 16 * ct + 4 * g4, a);
-        if constexpr (kDot == 1) {
-          // sums over this wavefront's 16 rows i, for each of the four j
+          lds_store4(m.p + i * PP + j0, a);
+          if constexpr (kDot == 1) {
+            row_sum += (b[0] + b[1]) + (b[2] + b[3]);
+            // sums over this wavefront's 16 rows i, for each of the four j
 #pragma unroll
-          for (int o = 1; o < 16; o <<= 1)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) wsum[r] += __shfl_xor(wsum[r], o, 64);
-          if (l16 == 0) *reinterpret_cast<f32x4*>(&m.col[NR == 4 ? wave : rt][16 * ct + 4 * g4]) = wsum;
+            for (int r = 0; r < 4; ++r) b[r] = row16_sum(b[r]);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(&m.cols[rt][j0]) = b;
+          }
+        } else if ((ct ^ rt) == 1) {
+          lds_store4(m.p + i * PP + j0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});   // read with its neighbour
         }
       }
       if constexpr (kDot == 1) {
         row_sum += __shfl_xor(row_sum, 16, 64);
         row_sum += __shfl_xor(row_sum, 32, 64);
-        // with two row tiles, the two wavefronts of a row tile hold one column
-        // tile each: their sums are kept apart
-        if (g4 == 0) {
-          if constexpr (NR == 4) m.sum[i] = row_sum;
-          else m.col[2 + (wave & 1)][i] = row_sum;
-        }
+        // with two row tiles, each of a row tile's two wavefronts has a part
+        if (g4 == 0) m.rows[NR == 4 ? 0 : wave & 1][i] = row_sum;
       }
 
       // the carried part: x S
@@ -518,55 +661,60 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
         for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < DA / 32; ++k) {
-        Frag<T> hi[NT], lo[NT];
+        Frag<T> part[NT][kStateParts];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float v[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = s[2 * k][t][r], v[4 + r] = s[2 * k + 1][t][r];
-          if constexpr (kExact) split(v, hi[t], lo[t]);
-          else pack(hi[t], v);
+          split(v, part[t]);
         }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const Frag<T> xf = frag_split(m.x + (16 * r + l16) * PA + 32 * k + 4 * g4);
+          const Frag<T> xf = frag_row<DA>(m.x, 16 * r + l16, 32 * k + 8 * g4);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma(acc[r][t], hi[t], xf);
-            if constexpr (kExact) mma(acc[r][t], lo[t], xf);
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < kStateParts; ++q) mma(acc[r][t], part[t][q], xf);
         }
       }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float f = m.d.ein[16 * r + l16];
+        const float fe = d.ein[16 * r + l16];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] *= f;
+        for (int t = 0; t < NT; ++t) acc[r][t] *= fe;
       }
       if constexpr (kDot != 0) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int i = 16 * r + l16;
+          const int i2 = 16 * r + l16;
           float dot = 0.0f;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const int c = col_of(t, 4 * g4);
-            float ev[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (kDot == 1) {
+            f32x4 e4;
+            if constexpr (kDot == 1) e4 = lds_load4(m.e + tile_at<T, TB>(i2, col_of(t, 4 * g4)));
+            else e4 = ev[r][t];       // past n or dB: acc is zero there, of finite values
 #pragma unroll
-              for (int q = 0; q < 4; ++q) ev[q] = to_float(m.e[i * PB + c + q]);
-            } else if (i < n && c < p.dB) {
-              T raw[4];
-              __builtin_memcpy(raw, E + (t0 + i) * p.e.row + c, sizeof(raw));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) ev[q] = to_float(raw[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) dot = __builtin_fmaf(acc[r][t][q], ev[q], dot);
+            for (int q = 0; q < 4; ++q) dot = __builtin_fmaf(acc[r][t][q], e4[q], dot);
           }
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
-          if (g4 == 0) m.dot[wave][i] = dot;
+          if (g4 == 0) m.dot[wave][i2] = dot;
+        }
+      }
+      if constexpr (kDot == 2) {
+        if (dump) {
+          float part = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const f32x4 q = *reinterpret_cast<const f32x4*>(dump + (mt * NT + t) * (kThreads * 4));
+#pragma unroll
+              for (int r = 0; r < 4; ++r) part = __builtin_fmaf(q[r], s[mt][t][r], part);
+            }
+          part = wave_sum(part);
+          if (lane == 0) m.edge[wave] = part;
         }
       }
       block_sync();
@@ -578,7 +726,7 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
     for (int k = 0; k < NK; ++k)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        zf[k][t] = frag_col<PB>(m.z, 32 * k, c_wave + 4 * t, kStep, lane);
+        zf[k][t] = frag_col<TB, kStep>(m.z, 32 * k, c_wave + 4 * t, lane);
 
     if constexpr (kOut) {
 #pragma unroll
@@ -586,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (kRev ? k < r / 2 : k > r / 2) continue;
-          const Frag<T> pf = frag_row(m.p + (16 * r + l16) * PP + 32 * k + 8 * g4);
+          const Frag<T> pf = frag_at(m.p + (16 * r + l16) * PP + 32 * k + 8 * g4);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
         }
@@ -594,101 +742,119 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
       for (int r = 0; r < NR; ++r) {
         const int i = 16 * r + l16;
         if (i >= n) continue;
-        const int64_t row = ((at.start + t0 + i) * p.heads + h) * int64_t(p.dB);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int c = col_of(t, 4 * g4);
           if (c >= p.dB) continue;
-          if (p.out_f32) store4(static_cast<float*>(p.out) + row + c, acc[r][t]);
-          else store4(static_cast<T*>(p.out) + row + c, acc[r][t]);
+          const uint32_t to = i * o_row + c;
+          if (p.out_f32) store4(reinterpret_cast<float*>(out) + to, acc[r][t]);
+          else store4(reinterpret_cast<T*>(out) + to, acc[r][t]);
         }
       }
       if constexpr (kDot == 1) {
-        if (tid < C && tid < n) {
-          float u = (m.dot[0][tid] + m.dot[1][tid]) + (m.dot[2][tid] + m.dot[3][tid]);
-          float rows, cols = 0.0f;
-          const int rt = tid >> 4;          // column sums exist for row tiles >= this one
-          if constexpr (NR == 4) {
-            rows = m.sum[tid];
-            for (int q = rt; q < 4; ++q) cols += m.col[q][tid];
-          } else {
-            rows = m.col[2][tid] + (rt == 1 ? m.col[3][tid] : 0.0f);
-            for (int q = rt; q < 2; ++q) cols += m.col[q][tid];
-          }
-          p.u[(at.start + t0 + tid) * p.heads + h] = u + (rows - cols);
+        if (wave == 0) {
+          const int t = min(lane, C - 1), tt = t >> 4;
+          const float qd = (m.dot[0][t] + m.dot[1][t]) + (m.dot[2][t] + m.dot[3][t]);
+          float rows = m.rows[0][t], cols = 0.0f;
+          if (NR == 2 && tt == 1) rows += m.rows[1][t];
+#pragma unroll
+          for (int q = 0; q < NR; ++q)          // row tiles from this one on
+            if (q >= tt) cols += m.cols[q][t];
+          const bool in = lane < n;
+          if (in) u_at[static_cast<uint32_t>(lane * p.heads)] = qd + (rows - cols);
+          const float sum = wave_sum(in ? qd : 0.0f);
+          if (lane == 0) p.q_sums[(slot * p.chunks_per_slot + ck) * p.heads + h] = sum;
         }
       }
       if constexpr (kDot == 2) {
         if (wave == 0) {
-          const int64_t ti = (at.start + t0 + lane) * p.heads + h;
           const bool in = lane < n;
-          const float kd = lane < C ? (m.dot[0][lane] + m.dot[1][lane]) + (m.dot[2][lane] + m.dot[3][lane]) : 0.0f;
-          const float u = in ? p.u[ti] : 0.0f;
-          float before = kd, after = u;     // inclusive sums up to, and from, this token
+          const int t = min(lane, C - 1);
+          const float kd = in ? (m.dot[0][t] + m.dot[1][t]) + (m.dot[2][t] + m.dot[3][t]) : 0.0f;
+          float before = kd, after = in ? uv : 0.0f;     // inclusive sums up to, and from, this token
 #pragma unroll
           for (int o = 1; o < 64; o <<= 1) {
             const float a = __shfl_up(before, o, 64), b = __shfl_down(after, o, 64);
             if (lane >= o) before += a;
             if (lane + o < 64) after += b;
           }
-          const float through = edge - __shfl(before, 63, 64);
+          // what passes through the whole chunk
+          const float through = dump ? d.all * ((m.edge[0] + m.edge[1]) + (m.edge[2] + m.edge[3]))
+                                     : edge - __shfl(before, 63, 64);
           const float prior = __shfl_up(before, 1, 64);
           const float dg = after + (lane > 0 ? prior : 0.0f) + through;
-          edge = through + __shfl(after, 0, 64);
+          edge = through + qs;
           if (in) {
-            if (p.dg) p.dg[ti] = dg;
+            if (p.dg) dg_at[static_cast<uint32_t>(lane * p.heads)] = dg;
             head_sum += dg;
           }
         }
       }
     }
 
+    if constexpr (kOut) out += kAhead * static_cast<int64_t>(o_row) * (p.out_f32 ? 4 : int(sizeof(T)));
+    if constexpr (kDot == 2) {
+      dotted += kAhead * static_cast<int64_t>(e_row);
+      dg_at += kAhead * p.heads;
+    }
+    if constexpr (kDot != 0) u_at += kAhead * p.heads;
+
     // the state after the chunk
-    const bool more = it + 1 < chunks || !kOut || (last_seg && p.last);
-    if (more) {
-      const float all = m.d.all;
+    if (it + 1 < chunks || !kOut || (last_seg && p.last)) {
+      const float all = d.all;
 #pragma unroll
       for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[mt][t] *= all;
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        Frag<T> hi[NT], lo[NT];
-        float w[8];
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&m.d.w[32 * k + 8 * g4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&m.d.w[32 * k + 8 * g4 + 4]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = w0[e], w[4 + e] = w1[e];
+        Frag<T> part[NT][kParts];
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 8 * g4]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 8 * g4 + 4]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float v[8];
           unpack(zf[k][t], v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= w[e];
-          if constexpr (kBf16) split(v, hi[t], lo[t]);
-          else pack(hi[t], v);
+          for (int e = 0; e < 4; ++e) v[e] *= w0[e], v[4 + e] *= w1[e];
+          split(v, part[t]);
         }
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt) {
-          const Frag<T> yf = frag_col<PA>(m.y, 32 * k, 16 * mt, 4, lane);
+          const Frag<T> yf = frag_col<DA, 8>(m.y, 32 * k, 32 * (mt >> 1) + 4 * (mt & 1), lane);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma(s[mt][t], yf, hi[t]);
-            if constexpr (kBf16) mma(s[mt][t], yf, lo[t]);
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) mma(s[mt][t], yf, part[t][q]);
         }
       }
     }
     if constexpr (!kOut) {
-      if (tid == 0) head_sum += m.d.hi[C - 1];     // the segment's log decay
+      if (tid == 0) head_sum += d.hi[C - 1];     // the segment's log decay
     }
+    if (wave == 0 && it + 1 < chunks)
+      decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? next.g : 0.0f, scale, lane);
     block_sync();
+  };
+  if (chunks > 0) {
+    fetch(sets[0], 0);
+    if (kSets == 2 && chunks > 1) fetch(sets[kSets - 1], 1);
+    if (wave == 0) decays<C, kRev>(m.d[0], lane < tokens_of(0) ? sets[0].g : 0.0f, scale, lane);
+  }
+  if constexpr (kSets == 2) {
+    int it = 0;
+    for (; it + 1 < chunks; it += 2) {
+      step(it, sets[0], sets[1]);
+      step(it + 1, sets[1], sets[0]);
+    }
+    if (it < chunks) step(it, sets[0], sets[1]);
+  } else {
+    for (int it = 0; it < chunks; ++it) step(it, sets[0], sets[0]);
   }
 
   if constexpr (kDot == 2) {
     if (p.head_part && wave == 0) {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) head_sum += __shfl_xor(head_sum, o, 64);
+      head_sum = wave_sum(head_sum);
       if (lane == 0) p.head_part[slot * p.heads + h] = head_sum;
     }
   }
@@ -707,7 +873,7 @@ __global__ __launch_bounds__(kThreads) void la_pass(PassArgs p) {
       const int c = col_of(t, l16);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int a = 16 * mt + 4 * g4 + r;
+        const int a = row_of(mt, r);
         if (a < p.dA && c < p.dB) dst[a * p.sA + c * p.sB] = s[mt][t][r];
       }
     }

@@ -34,14 +34,14 @@ using la::View;
 
 // Runs over a sequence's segments in order (kRev: from the last): `st` holds
 // each segment's own state on entry and the state the segment starts from on
-// return; `last` the state after all of them.  A thread owns four values of one
+// return.  A thread owns four values of one
 // head's state; the segments' loads do not depend on each other and run kAhead
 // ahead of the chain of multiply-adds.
 template <bool kRev>
 __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t size,
                                                 const float* __restrict__ init,
                                                 const float* __restrict__ decay,
-                                                float* __restrict__ st, float* __restrict__ last) {
+                                                float* __restrict__ st) {
   using la::f32x4;
   constexpr int kAhead = 8;
   const int64_t i = 4 * (int64_t(blockIdx.y) * 256 + threadIdx.x);
@@ -64,8 +64,7 @@ __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t si
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   const int64_t sh = (seq * heads + h) * size + i;
   if (init) s = f32x4{init[sh], init[sh + 1], init[sh + 2], init[sh + 3]};
-  // the segment that comes last has a state of its own only where `last` is asked for
-  const int64_t own = last ? count : count - 1;
+  const int64_t own = count - 1;            // nothing follows the one that comes last
   for (int64_t c0 = 0; c0 < count; c0 += kAhead) {
     f32x4 u[kAhead];
     float e[kAhead];
@@ -90,22 +89,18 @@ __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t si
       for (int r = 0; r < 4; ++r) s[r] = __builtin_fmaf(e[k], s[r], u[k][r]);
     }
   }
-  if (last)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) last[sh + r] = s[r];
 }
 
 hipError_t launch_carry_states(bool rev, const Grid& grid, int heads, int64_t size,
-                               const float* init, const float* decay, float* st, float* last,
+                               const float* init, const float* decay, float* st,
                                hipStream_t stream) {
   const dim3 g(static_cast<uint32_t>(grid.seqs * heads),
                static_cast<uint32_t>((size / 4 + 255) / 256));
   if (rev)
-    hipLaunchKernelGGL(la_carry<true>, g, dim3(256), 0, stream, grid, heads, size, init, decay, st,
-                       last);
+    hipLaunchKernelGGL(la_carry<true>, g, dim3(256), 0, stream, grid, heads, size, init, decay, st);
   else
     hipLaunchKernelGGL(la_carry<false>, g, dim3(256), 0, stream, grid, heads, size, init, decay,
-                       st, last);
+                       st);
   return hipGetLastError();
 }
 
@@ -205,12 +200,11 @@ __global__ __launch_bounds__(256) void la_step(StepLaunch p) {
   }
 }
 
-View view_of(const void* p, int64_t row, int div, int e) {
+View view_of(const void* p, int64_t row, int div) {
   View v;
   v.p = p;
   v.row = row;
   v.div = div;
-  v.vec = reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * e % 16 == 0;
   return v;
 }
 
@@ -223,7 +217,7 @@ size_t round_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 // times heads do not fill the compute units, sequences are cut: each segment's
 // own state is found first (reading k and v once more), the states are joined,
 // then all segments run at once.
-LaPlan plan_la(const LaShape& s, bool backward) {
+LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   LaPlan p;
   Grid& g = p.grid;
   g.seqs = s.seqs;
@@ -255,14 +249,21 @@ LaPlan plan_la(const LaShape& s, bool backward) {
     at += round_up(bytes);
     return o;
   };
-  if (p.cut || backward) {
+  if (p.cut) {
     p.states = take(state * g.slots);
     p.decay = take(per_slot);
   }
   if (backward) {
-    p.rev_states = take(state * g.slots);
-    p.rev_decay = take(per_slot);
-    p.fwd_last = take(state * s.seqs);
+    if (p.cut) {
+      p.rev_states = take(state * g.slots);
+      p.rev_decay = take(per_slot);
+    }
+    const int chunk = bf16 ? 64 : 32, every = 256 / chunk;
+    p.chunks_per_slot = seg / chunk;
+    p.dumps_per_slot = (p.chunks_per_slot + every - 1) / every;
+    const size_t held = static_cast<size_t>(s.dk <= 64 ? 64 : 128) * (s.dv <= 64 ? 64 : 128) * 4;
+    p.dumps = take(held * s.heads * p.dumps_per_slot * g.slots);
+    p.q_sums = take(static_cast<size_t>(p.chunks_per_slot) * g.slots * s.heads * 4);
     p.u = take(static_cast<size_t>(s.tokens) * s.heads * 4);
     p.head_part = take(per_slot);
     if (s.heads != s.key_heads) {
@@ -276,15 +277,14 @@ LaPlan plan_la(const LaShape& s, bool backward) {
 
 hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream) {
   const LaShape& s = a.shape;
-  const int e = a.dtype == MSSM_BFLOAT16 ? 2 : 4;
   const int rep = static_cast<int>(s.heads / s.key_heads);
   char* w = static_cast<char*>(ws);
   PassArgs p;
   p.grid = plan.grid;
   p.grid.offsets = a.offsets;
-  p.x = view_of(a.q, a.q_row, rep, e);
-  p.y = view_of(a.k, a.k_row, rep, e);
-  p.z = view_of(a.v, a.v_row, 1, e);
+  p.x = view_of(a.q, a.q_row, rep);
+  p.y = view_of(a.k, a.k_row, rep);
+  p.z = view_of(a.v, a.v_row, 1);
   p.g = a.g;
   p.g_row = a.per_token ? s.heads : 0;
   p.heads = static_cast<int>(s.heads);
@@ -301,8 +301,7 @@ hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStrea
     q.seg_out = st;
     q.seg_decay = dec;
     if ((err = la::pass_state(a.dtype, q, stream)) != hipSuccess) return err;
-    if ((err = launch_carry_states(false, p.grid, p.heads, s.dk * s.dv, a.state, dec, st, nullptr,
-                                   stream)) != hipSuccess)
+    if ((err = launch_carry_states(false, p.grid, p.heads, s.dk * s.dv, a.state, dec, st, stream)) != hipSuccess)
       return err;
     p.seg_states = st;
   }
@@ -316,13 +315,12 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
                          hipStream_t stream) {
   const LaShape& s = a.shape;
   const bool bf16 = a.dtype == MSSM_BFLOAT16;
-  const int e = bf16 ? 2 : 4;
   const int rep = static_cast<int>(s.heads / s.key_heads);
   char* w = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
-  const View q = view_of(a.q, a.q_row, rep, e), k = view_of(a.k, a.k_row, rep, e);
-  const View v = view_of(a.v, a.v_row, 1, e);
-  const View g = view_of(d.dout, s.heads * s.dv, 1, e);
+  const View q = view_of(a.q, a.q_row, rep), k = view_of(a.k, a.k_row, rep);
+  const View v = view_of(a.v, a.v_row, 1);
+  const View g = view_of(d.dout, s.heads * s.dv, 1);
   PassArgs c;
   c.grid = plan.grid;
   c.grid.offsets = a.offsets;
@@ -332,44 +330,39 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
   c.scale = a.scale;
   const int64_t size = s.dk * s.dv;
   hipError_t err;
-  const bool fwd_last = d.dlast != nullptr;     // dg needs <dS_last, S_last>
-  const bool fwd_states = plan.cut || fwd_last;
-  if (fwd_states) {
+  if (plan.cut) {
     PassArgs p = c;
     p.y = k, p.z = v;
     p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
     p.sA = s.dv, p.sB = 1;
-    p.every_segment = fwd_last;
     p.seg_out = at(plan.states);
     p.seg_decay = at(plan.decay);
     if ((err = la::pass_state(a.dtype, p, stream)) != hipSuccess) return err;
     if ((err = launch_carry_states(false, c.grid, c.heads, size, a.state, at(plan.decay),
-                                   at(plan.states), fwd_last ? at(plan.fwd_last) : nullptr,
-                                   stream)) != hipSuccess)
+                                   at(plan.states), stream)) != hipSuccess)
       return err;
-  }
-  if (plan.cut) {
-    PassArgs p = c;
     p.y = q, p.z = g;
-    p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
-    p.sA = s.dv, p.sB = 1;
     p.seg_out = at(plan.rev_states);
     p.seg_decay = at(plan.rev_decay);
     if ((err = la::pass_state_rev(a.dtype, p, stream)) != hipSuccess) return err;
     if ((err = launch_carry_states(true, c.grid, c.heads, size, d.dlast, at(plan.rev_decay),
-                                   at(plan.rev_states), nullptr, stream)) != hipSuccess)
+                                   at(plan.rev_states), stream)) != hipSuccess)
       return err;
   }
+  c.u = at(plan.u);
+  c.q_sums = at(plan.q_sums);
+  c.dumps = at(plan.dumps);
+  c.chunks_per_slot = plan.chunks_per_slot;
+  c.dumps_per_slot = plan.dumps_per_slot;
   {
     PassArgs p = c;
     p.x = g, p.y = v, p.z = k, p.e = q;
     p.dA = static_cast<int>(s.dv), p.dB = static_cast<int>(s.dk);
     p.sA = 1, p.sB = s.dv;
     p.init = a.state;
-    p.seg_states = fwd_states ? at(plan.states) : nullptr;
+    p.seg_states = plan.cut ? at(plan.states) : nullptr;
     p.out = rep > 1 ? at(plan.dq) : d.dq;
     p.out_f32 = rep > 1;
-    p.u = at(plan.u);
     if ((err = la::pass_dq(a.dtype, p, stream)) != hipSuccess) return err;
   }
   {
@@ -379,11 +372,8 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.sA = 1, p.sB = s.dv;
     p.init = d.dlast;
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
-    p.fwd_states = plan.cut ? at(plan.states) : nullptr;
-    p.fwd_last = fwd_last ? at(plan.fwd_last) : nullptr;
     p.out = rep > 1 ? at(plan.dk) : d.dk;
     p.out_f32 = rep > 1;
-    p.u = at(plan.u);
     p.dg = a.per_token ? d.dg : nullptr;
     p.head_part = a.per_token ? nullptr : at(plan.head_part);
     if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;

@@ -437,16 +437,17 @@ struct LaGrads {
 
 // Segments of a call (`cut`: some sequence may have more than one) and the
 // workspace: each segment's state and decay; backward also those of the
-// adjoint, the states after the sequences, the queries' part of dg, and with
+// adjoint, the queries' part of dg, the states before every 256 tokens, and with
 // shared keys the heads' dq and dk in float32.
 struct LaPlan {
   la::Grid grid;
   bool cut = false;
-  size_t states = 0, decay = 0, rev_states = 0, rev_decay = 0, fwd_last = 0, u = 0;
+  size_t states = 0, decay = 0, rev_states = 0, rev_decay = 0, u = 0, q_sums = 0, dumps = 0;
   size_t head_part = 0, dq = 0, dk = 0;
+  int64_t chunks_per_slot = 0, dumps_per_slot = 0;
   size_t bytes = 0;
 };
-LaPlan plan_la(const LaShape& s, bool backward);
+LaPlan plan_la(const LaShape& s, bool backward, bool bf16);
 hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream);
 hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, void* ws,
                          hipStream_t stream);
