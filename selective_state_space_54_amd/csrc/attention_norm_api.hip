@@ -6,6 +6,9 @@
 
 namespace {
 
+// A token's values in any tensor: its bytes fit 24 bits, a chunk's 32, which is
+// how the kernels reach them.
+constexpr int64_t kMaxRow = int64_t(1) << 22;
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;   // blocks of 256 threads
 
 bool product(std::initializer_list<int64_t> f, int64_t* out) {
@@ -31,10 +34,11 @@ mssm_status shape_of(int64_t seqs, int64_t L, int64_t key_heads, int64_t heads, 
   if (!mssm_linear_attention_supports(dk, dv)) return MSSM_ERROR_NOT_SUPPORTED;
   int64_t tokens = L, n;
   if (!packed && !product({seqs, L}, &tokens)) return MSSM_ERROR_SIZE_OVERFLOW;
+  if (heads >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
   if (!product({tokens, heads, dk, 8}, &n) || !product({tokens, heads, dv, 8}, &n) ||
       !product({seqs, heads, dk, dv, 8}, &n))
     return MSSM_ERROR_SIZE_OVERFLOW;
-  if (heads > std::numeric_limits<int32_t>::max()) return MSSM_ERROR_NOT_SUPPORTED;
+  if (heads * dk >= kMaxRow || heads * dv >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
   s->seqs = seqs;
   s->tokens = tokens;
   s->packed = packed;
@@ -58,13 +62,12 @@ mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm_dtype dtype,
   return MSSM_SUCCESS;
 }
 
-// Rows hold their heads, and a chunk's rows are reached with 32-bit offsets.
+// Rows hold their heads.
 mssm_status check_rows(const mssm::LaArgs& a) {
   const mssm::LaShape& s = a.shape;
-  const int64_t most = int64_t(1) << 24;
   if (a.q_row < s.key_heads * s.dk || a.k_row < s.key_heads * s.dk || a.v_row < s.heads * s.dv)
     return MSSM_ERROR_INVALID_VALUE;
-  if (a.q_row > most || a.k_row > most || a.v_row > most) return MSSM_ERROR_NOT_SUPPORTED;
+  if (a.q_row >= kMaxRow || a.k_row >= kMaxRow || a.v_row >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
   return MSSM_SUCCESS;
 }
 

@@ -43,6 +43,7 @@ struct PassArgs {
   // output
   void* out = nullptr;               // [tokens, heads, dB]
   bool out_f32 = false;              // else of the inputs' type
+  bool out_aligned = true;           // to 4 bytes
   // gradient of the log decays: written by dq, read by dk
   float* u = nullptr;                // [tokens, heads]
   float* q_sums = nullptr;           // [slots, chunks_per_slot, heads]

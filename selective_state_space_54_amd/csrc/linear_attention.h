@@ -34,11 +34,11 @@
 //
 // Layout on the compute unit.  A block of four wavefronts owns one segment of
 // one head.  Wavefront w owns 16 NT columns of the value dimension: its part
-// of S [DA, 16 NT] stays in the accumulator registers for the whole segment,
-// and is used as a matrix operand straight from them: a 16 x 16 result holds
-// four consecutive rows per lane, and the rows of a matrix product's sum may
-// be taken in any order if both operands take the same, so two result tiles
-// are one 32-row operand without a trip through LDS.  The tiles of x, y and z
+// of S [DA, 16 NT] stays in registers for the whole segment, and is used as a
+// matrix operand straight from them: a 16 x 16 result holds four consecutive
+// rows per lane, and the terms of a matrix product's sum may be taken in any
+// order if both operands take the same, so two result tiles are one 32-row
+// operand without a trip through LDS.  The tiles of x, y and z
 // are staged in LDS row by row; products that sum over tokens read them
 // transposed (ds_read_b64_tr_b16).  The C x C products are shared out over the
 // wavefronts by rows and exchanged through LDS.
@@ -57,6 +57,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "la_args.h"
 #include "scan_device.h"
@@ -96,55 +98,66 @@ __device__ __forceinline__ void mma(f32x4& acc, const Frag<float>& a, const Frag
 }
 
 // Where an LDS tile of D columns keeps value c of row r.  A row's 16-byte
-// pieces are permuted by a pattern of the row's number modulo 8, its bits in
-// reverse, so that the same piece of eight consecutive rows falls on eight
-// different groups of four banks (row reads), and four consecutive rows of
-// eight columns spread as evenly as 8-byte accesses allow (column reads).
+// pieces are permuted by the row's number, so that the 8-byte reads of 32 lanes
+// (16 rows of two neighbouring halves, or 8 rows of two neighbouring pieces)
+// fall on all 64 banks once.  Reads of 16 bytes would take half the
+// instructions, but their measured rate is a third of the 8-byte reads' (75
+// against 256 bytes a cycle).
 template <typename T, int D>
 __device__ __forceinline__ int tile_at(int r, int c) {
   constexpr int kPer = 16 / sizeof(T);
-  const int f = (r & 1) << 2 | (r & 2) | (r >> 2 & 1);
+  const int f = D / kPer > 8 ? (r & 7) << 1 | (r >> 3 & 1) : r >> 1 & 7;
   return r * D + ((c / kPer) ^ f) * kPer + c % kPer;
 }
 
-// Eight consecutive values from p (16-byte aligned).
-__device__ __forceinline__ Frag<uint16_t> frag_at(const uint16_t* p) {
+// A fragment's eight terms are numbers 0 .. 3 and 16 .. 19 from 4 (lane / 16) of
+// a run of 32: the order in which two 16-row results hold the rows of an operand.
+__device__ __forceinline__ Frag<uint16_t> frag_of(uint2 a, uint2 b) {
   Frag<uint16_t> f;
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  __builtin_memcpy(&f.v, &u, 16);
+  const uint2 u[2] = {a, b};
+  __builtin_memcpy(&f.v, u, 16);
   return f;
 }
-__device__ __forceinline__ Frag<float> frag_at(const float* p, const float* q) {
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ Frag<float> frag_of(const float* a, const float* b) {
   Frag<float> f;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
+  for (int e = 0; e < 4; e += 2) {
+    const f32x2 u = *reinterpret_cast<const f32x2*>(a + e);
+    const f32x2 v = *reinterpret_cast<const f32x2*>(b + e);
+    f.v[e] = u[0], f.v[e + 1] = u[1], f.v[4 + e] = v[0], f.v[5 + e] = v[1];
+  }
   return f;
 }
-__device__ __forceinline__ Frag<float> frag_at(const float* p) { return frag_at(p, p + 4); }
 
-// Values c .. c + 7 of row r.
+// Terms c .. c + 31 of row r of a tile; c = 32 k + 4 (lane / 16).
 template <int D>
 __device__ __forceinline__ Frag<uint16_t> frag_row(const uint16_t* t, int r, int c) {
-  return frag_at(t + tile_at<uint16_t, D>(r, c));
+  return frag_of(*reinterpret_cast<const uint2*>(t + tile_at<uint16_t, D>(r, c)),
+                 *reinterpret_cast<const uint2*>(t + tile_at<uint16_t, D>(r, c + 16)));
 }
 template <int D>
 __device__ __forceinline__ Frag<float> frag_row(const float* t, int r, int c) {
-  return frag_at(t + tile_at<float, D>(r, c), t + tile_at<float, D>(r, c + 4));
+  return frag_of(t + tile_at<float, D>(r, c), t + tile_at<float, D>(r, c + 16));
 }
+// The same of a plain row.
+__device__ __forceinline__ Frag<uint16_t> frag_at(const uint16_t* p) {
+  return frag_of(*reinterpret_cast<const uint2*>(p), *reinterpret_cast<const uint2*>(p + 16));
+}
+__device__ __forceinline__ Frag<float> frag_at(const float* p) { return frag_of(p, p + 16); }
 
-// Column of a tile over eight consecutive rows r0 + 8 (lane / 16) ..: lane l
-// gets the column of its index l % 16, where indices 4 c .. 4 c + 3 are the
-// columns c0 + kStep c ...  For bfloat16 the transposing LDS read gives 16 lanes
-// four rows of sixteen columns: lane l % 16 addresses four columns of one row
-// and receives one column of the four rows.
+// Terms r0 .. r0 + 31 down a column of a tile: lane l gets the column of its
+// index l % 16, where indices 4 c .. 4 c + 3 are the columns c0 + kStep c ...
+// For bfloat16 the transposing LDS read gives 16 lanes four rows of sixteen
+// columns: lane l % 16 addresses four columns of one row and receives one column
+// of the four rows.
 template <int D, int kStep>
 __device__ __forceinline__ Frag<uint16_t> frag_col(const uint16_t* t, int r0, int c0, int lane) {
   using lds_ptr = __attribute__((address_space(3))) s16x4*;
-  const int r = r0 + 8 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + kStep * (lane & 3);
+  const int r = r0 + 4 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + kStep * (lane & 3);
   const s16x4 u[2] = {
       __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + tile_at<uint16_t, D>(r, c))),
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + tile_at<uint16_t, D>(r + 4, c)))};
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + tile_at<uint16_t, D>(r + 16, c)))};
   Frag<uint16_t> f;
   __builtin_memcpy(&f.v, u, 16);
   return f;
@@ -154,7 +167,8 @@ __device__ __forceinline__ Frag<float> frag_col(const float* t, int r0, int c0, 
   Frag<float> f;
   const int c = c0 + kStep * ((lane & 15) >> 2) + (lane & 3);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = t[tile_at<float, D>(r0 + 8 * (lane >> 4) + e, c)];
+  for (int e = 0; e < 8; ++e)
+    f.v[e] = t[tile_at<float, D>(r0 + 4 * (lane >> 4) + 16 * (e >> 2) + (e & 3), c)];
   return f;
 }
 
@@ -198,7 +212,8 @@ __device__ __forceinline__ void split(const float (&v)[8], Frag<uint16_t> (&part
     float a = v[2 * i], b = v[2 * i + 1];
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const uint32_t u = pack2(a, b);
+      uint32_t u = pack2(a, b);
+      asm("" : "+v"(u));      // read the halves back, rather than round a and b once more
       __builtin_memcpy(reinterpret_cast<char*>(&part[q].v) + 4 * i, &u, 4);
       a -= low_half(u);
       b -= high_half(u);
@@ -222,6 +237,26 @@ __device__ __forceinline__ void lds_store4(uint16_t* p, f32x4 v) {
   *reinterpret_cast<uint2*>(p) = uint2{pack2(v[0], v[1]), pack2(v[2], v[3])};
 }
 __device__ __forceinline__ void lds_store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+
+// NT consecutive fours at byte offset `off`, rounded to V, as 8- or 16-byte stores.
+template <typename V, int NT>
+__device__ __forceinline__ void buf_store(buf_t to, uint32_t off, const f32x4 (&v)[NT]) {
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (sizeof(V) == 4) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v[t]), to,
+                                             static_cast<int>(off + 16 * t), 0, 0);
+  } else if constexpr (NT == 1) {
+    __builtin_amdgcn_raw_buffer_store_b64(
+        u32x2{pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3])}, to, static_cast<int>(off), 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b128(
+        u32x4{pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]), pack2(v[1][0], v[1][1]),
+              pack2(v[1][2], v[1][3])},
+        to, static_cast<int>(off), 0, 0);
+  }
+}
 
 // ---- a sequence's place -------------------------------------------------------------------------
 
@@ -279,11 +314,10 @@ __device__ __forceinline__ uint32_t logical_block() {
 
 // C rows of D values, staged through registers: fetch issues the loads, stash
 // writes them to LDS.  Rows past n and columns past d load a valid piece
-// instead and become zero when stashed: no branch stands between the loads, so
-// all are in flight at once (a conditional load's result is copied where the
-// branches meet, which waits for it).  In a whole chunk a thread's rows are a
-// fixed distance apart: one addition for each piece's address.  Pieces are read
-// at any alignment.
+// instead and become zero when stashed: no branch stands around or between the
+// loads, so that all are in flight at once and the wait for them counts what
+// was issued since (where branches meet, it would wait for everything).  Pieces
+// are read at any alignment.
 template <typename T, int C, int D>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);              // values in a 16-byte piece
@@ -297,32 +331,27 @@ struct Tile {
     const int r = threadIdx.x / kRowPieces;
     const int c = min(static_cast<int>(threadIdx.x % kRowPieces) * kPer, d - kPer);
     const char* from = reinterpret_cast<const char*>(base);
-    const uint32_t bytes = row * static_cast<uint32_t>(sizeof(T));
-    if (n == C) {
-      uint32_t off = r * bytes + c * static_cast<uint32_t>(sizeof(T));
+    const uint32_t bytes = row * static_cast<uint32_t>(sizeof(T));   // below 2^24
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i, off += kRowsApart * bytes)
-        __builtin_memcpy(&v[i], from + off, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const uint32_t off = min(r + i * kRowsApart, n - 1) * bytes + c * static_cast<uint32_t>(sizeof(T));
-        __builtin_memcpy(&v[i], from + off, 16);
-      }
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t off = __umul24(min(r + i * kRowsApart, n - 1), bytes) +
+                           c * static_cast<uint32_t>(sizeof(T));
+      __builtin_memcpy(&v[i], from + off, 16);
     }
   }
   __device__ __forceinline__ void stash(T* lds, int n, int d) const {
     const int r = threadIdx.x / kRowPieces, c = static_cast<int>(threadIdx.x % kRowPieces) * kPer;
-    static_assert(kRowsApart % 8 == 0, "one pattern for all of a thread's rows");
-    uint4* to = reinterpret_cast<uint4*>(lds + tile_at<T, D>(r, c));
+    auto at = [&](int i) {
+      return reinterpret_cast<uint4*>(lds + tile_at<T, D>(r + i * kRowsApart, c));
+    };
     if (n == C && d == D) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) to[i * kThreads] = v[i];
+      for (int i = 0; i < kPieces; ++i) *at(i) = v[i];
     } else {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const bool in = r + i * kRowsApart < n && c < d;
-        to[i * kThreads] = in ? v[i] : make_uint4(0u, 0u, 0u, 0u);
+        *at(i) = in ? v[i] : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   }
@@ -428,7 +457,6 @@ constexpr int kStride = 256 / C;
 template <typename T, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
 __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int kParts = kBf16 ? 3 : 1;                    // of the weighted z
   constexpr int kStateParts = kBf16 && kDot != 0 ? 3 : 1;  // of the state as an operand
   constexpr int NR = C / 16, NK = C / 32, NM = DA / 16, TB = 64 * NT;
   constexpr int PP = Lds<T, C, DA, NT, kOut, kDot>::PP;
@@ -452,8 +480,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   if (!kOut && last_seg) return;
 
   // columns of this wavefront: with two tiles, lane group g4's rows 4 g4 + r of
-  // both are the eight consecutive columns 8 g4 + 4 t + r.  The state's rows are
-  // paired the same way.
+  // both are the eight consecutive columns 8 g4 + 4 t + r (16-byte stores)
   constexpr int kStep = NT == 2 ? 8 : 4;
   const int c_wave = 16 * NT * wave;
   auto col_of = [&](int t, int c) { return c_wave + kStep * (c >> 2) + 4 * t + (c & 3); };
@@ -461,9 +488,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   const int64_t sh = (at.seq * p.heads + h) * (int64_t(p.dA) * p.dB);        // per sequence
   const int64_t wh = (slot * p.heads + h) * (int64_t(p.dA) * p.dB);          // per segment
 
-  // the state: tile mt's row 4 g4 + r is row 32 (mt / 2) + 8 g4 + 4 (mt % 2) + r
-  // of dA, its column l16 is column col_of(t, l16)
-  auto row_of = [&](int mt, int r) { return 32 * (mt >> 1) + 8 * g4 + 4 * (mt & 1) + r; };
+  // the state: rows 16 mt + 4 g4 + r of dA, column col_of(t, l16)
+  auto row_of = [&](int mt, int r) { return 16 * mt + 4 * g4 + r; };
   f32x4 s[NM][NT];
   {
     const float* init = !kOut ? nullptr
@@ -486,10 +512,10 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   const float scale = p.scale;
   // A chunk's tiles on their way from memory.  The loads run one chunk ahead of
   // their use, or two, with a second set of registers where state, results and
-  // both sets leave room for two blocks on a compute unit (256 registers).
-  // The log decays come first, they are wanted first.
+  // both sets leave room for two blocks on a compute unit (256 registers).  The
+  // log decays run two ahead: a chunk's factors are made while the one before is
+  // worked on.
   struct Stage {
-    float g;
     Tile<T, C, DA> x, y;
     Tile<T, C, TB> z, e;
   };
@@ -497,6 +523,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
                          Tile<T, C, TB>::kPieces * 4 * (kDot == 1 ? 2 : 1);
   constexpr int kHeld = NM * NT * 4 + (kOut ? NR * NT * 4 : 0) + (kDot == 2 ? NR * NT * 4 : 0);
   constexpr int kSets = kHeld + 2 * kStage <= (kOut ? 112 : 128) ? 2 : 1;
+  constexpr bool kLate = kOut && kHeld + kStage > 100;
   Stage sets[kSets];
   // Tokens of the it-th chunk worked on, and the pointers to the next chunk to load.
   const int len = static_cast<int>(at.len);
@@ -514,21 +541,26 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   const uint32_t x_row = static_cast<uint32_t>(p.x.row), y_row = static_cast<uint32_t>(p.y.row);
   const uint32_t z_row = static_cast<uint32_t>(p.z.row), e_row = static_cast<uint32_t>(p.e.row);
   const uint32_t g_row = static_cast<uint32_t>(p.g_row);
+  // Past the last chunk these load it again (unused).
+  auto fetch_g = [&](int it) __attribute__((always_inline)) {
+    const float g = G[static_cast<uint32_t>(min(lane, tokens_of(it) - 1)) * g_row];
+    if (it + 1 < chunks) G += kAhead * static_cast<int64_t>(g_row);
+    return g;
+  };
   auto fetch = [&](Stage& f, int it) __attribute__((always_inline)) {
     const int n = tokens_of(it);
-    f.g = G[static_cast<uint32_t>(min(lane, n - 1)) * g_row];
-    G += kAhead * static_cast<int64_t>(g_row);
+    const int64_t next = it + 1 < chunks ? kAhead : 0;
     if constexpr (kOut) {
       f.x.fetch(X, x_row, n, p.dA);
-      X += kAhead * static_cast<int64_t>(x_row);
+      X += next * x_row;
     }
     f.y.fetch(Y, y_row, n, p.dA);
-    Y += kAhead * static_cast<int64_t>(y_row);
+    Y += next * y_row;
     f.z.fetch(Z, z_row, n, p.dB);
-    Z += kAhead * static_cast<int64_t>(z_row);
+    Z += next * z_row;
     if constexpr (kDot == 1) {
       f.e.fetch(E, e_row, n, p.dB);
-      E += kAhead * static_cast<int64_t>(e_row);
+      E += next * e_row;
     }
   };
   // The chunk being worked on: where its output, and what is dotted with it, begin.
@@ -542,8 +574,9 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
 
   constexpr int kDumpSize = DA * TB;
   float edge = 0.0f, head_sum = 0.0f;      // of wavefront 0
+  float g_next = 0.0f;                     // log decays of the next chunk
 
-  auto step = [&](int it, Stage& f, const Stage& next) __attribute__((always_inline)) {
+  auto step = [&](int it, Stage& f) __attribute__((always_inline)) {
     const int ck = kRev ? chunks - 1 - it : it;
     const int n = tokens_of(it);
     const Decay<C>& d = m.d[it & 1];
@@ -552,7 +585,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
     f.z.stash(m.z, n, p.dB);
     if constexpr (kDot == 1) f.e.stash(m.e, n, p.dB);
     block_sync();
-    if (it + kSets < chunks) fetch(f, it + kSets);
+    const float g_after = fetch_g(min(it + 2, chunks - 1));
+    if constexpr (!kLate) fetch(f, min(it + kSets, chunks - 1));
     const int back = (chunks - 1 - ck) % kStride<C>;
     float* dump = nullptr;
     if constexpr (kDot != 0) {
@@ -596,23 +630,43 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       const int i = 16 * rt + l16;
       const float gi = d.hi[i], gil = d.lo[i];
       float row_sum = 0.0f;
+      // All of a row tile's products are formed, also those that the mask then
+      // drops: without branches between them the loads and products of one hide
+      // the latency of the others.
+      f32x4 as[kWaveTiles], bs[kDot == 1 ? kWaveTiles : 1];
+      {
+        Frag<T> xf[DA / 32];
+#pragma unroll
+        for (int k = 0; k < DA / 32; ++k) xf[k] = frag_row<DA>(m.x, i, 32 * k + 4 * g4);
+#pragma unroll
+        for (int u = 0; u < kWaveTiles; ++u) {
+          const int ct = NR == 4 ? u : wave & 1;
+          as[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < DA / 32; ++k)
+            mma(as[u], frag_row<DA>(m.y, 16 * ct + l16, 32 * k + 4 * g4), xf[k]);
+        }
+      }
+      if constexpr (kDot == 1) {
+        Frag<T> ef[TB / 32];
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) ef[k] = frag_row<TB>(m.e, i, 32 * k + 4 * g4);
+#pragma unroll
+        for (int u = 0; u < kWaveTiles; ++u) {
+          const int ct = NR == 4 ? u : wave & 1;
+          bs[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < TB / 32; ++k)
+            mma(bs[u], frag_row<TB>(m.z, 16 * ct + l16, 32 * k + 4 * g4), ef[k]);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < kWaveTiles; ++u) {
         const int ct = NR == 4 ? u : wave & 1;
         const bool live = kRev ? ct >= rt : ct <= rt;
         const int j0 = 16 * ct + 4 * g4;
         if (live) {
-          f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < DA / 32; ++k)
-            mma(a, frag_row<DA>(m.y, 16 * ct + l16, 32 * k + 8 * g4),
-                frag_row<DA>(m.x, i, 32 * k + 8 * g4));
-          if constexpr (kDot == 1) {
-#pragma unroll
-            for (int k = 0; k < TB / 32; ++k)
-              mma(b, frag_row<TB>(m.z, 16 * ct + l16, 32 * k + 8 * g4),
-                  frag_row<TB>(m.e, i, 32 * k + 8 * g4));
-          }
+          f32x4 a = as[u], b = bs[kDot == 1 ? u : 0];
           if (ct == rt) {
             const f32x4 gj = *reinterpret_cast<const f32x4*>(&d.hi[j0]);
             const f32x4 gjl = *reinterpret_cast<const f32x4*>(&d.lo[j0]);
@@ -647,6 +701,9 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
           lds_store4(m.p + i * PP + j0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});   // read with its neighbour
         }
       }
+      // the wavefront with the fewest scores prepares the next chunk's decays
+      if (wave == (kRev ? 3 : 0) && it + 1 < chunks)
+        decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
       if constexpr (kDot == 1) {
         row_sum += __shfl_xor(row_sum, 16, 64);
         row_sum += __shfl_xor(row_sum, 32, 64);
@@ -671,7 +728,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const Frag<T> xf = frag_row<DA>(m.x, 16 * r + l16, 32 * k + 8 * g4);
+          const Frag<T> xf = frag_row<DA>(m.x, 16 * r + l16, 32 * k + 4 * g4);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -719,6 +776,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       }
       block_sync();
     }
+    if constexpr (kLate) fetch(f, min(it + 1, chunks - 1));
 
     // z by columns, for the scores' product and for the state
     Frag<T> zf[NK][NT];
@@ -734,23 +792,35 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (kRev ? k < r / 2 : k > r / 2) continue;
-          const Frag<T> pf = frag_at(m.p + (16 * r + l16) * PP + 32 * k + 8 * g4);
+          const Frag<T> pf = frag_at(m.p + (16 * r + l16) * PP + 32 * k + 4 * g4);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
         }
+      // Stores through a descriptor that ends with the chunk's last value: rows and
+      // columns past it are dropped by the hardware, so no branch stands around them.
+      auto store = [&](auto value) __attribute__((always_inline)) {
+        using V = decltype(value);
+        if (p.out_aligned) {
+          const buf_t to = make_buf(out, ((n - 1) * o_row + p.dB) * static_cast<uint32_t>(sizeof(V)));
+          const uint32_t c = col_of(0, 4 * g4);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int i = 16 * r + l16;
-        if (i >= n) continue;
+          for (int r = 0; r < NR; ++r) {
+            const uint32_t off = c < static_cast<uint32_t>(p.dB) ? (16 * r + l16) * o_row + c : 0x3ffffff0u;
+            buf_store<V, NT>(to, off * static_cast<uint32_t>(sizeof(V)), acc[r]);
+          }
+        } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int c = col_of(t, 4 * g4);
-          if (c >= p.dB) continue;
-          const uint32_t to = i * o_row + c;
-          if (p.out_f32) store4(reinterpret_cast<float*>(out) + to, acc[r][t]);
-          else store4(reinterpret_cast<T*>(out) + to, acc[r][t]);
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const int i = 16 * r + l16, c = col_of(t, 4 * g4);
+              if (i < n && c < p.dB)
+                store4(reinterpret_cast<V*>(out) + static_cast<uint32_t>(i) * o_row + c, acc[r][t]);
+            }
         }
-      }
+      };
+      if (p.out_f32) store(0.0f);
+      else store(T());
       if constexpr (kDot == 1) {
         if (wave == 0) {
           const int t = min(lane, C - 1), tt = t >> 4;
@@ -799,8 +869,11 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
     }
     if constexpr (kDot != 0) u_at += kAhead * p.heads;
 
-    // the state after the chunk
+    // The state after the chunk.  Three parts of the weighted z where the state
+    // itself is a result or dg depends on it; two where only outputs rounded to
+    // bfloat16 do.
     if (it + 1 < chunks || !kOut || (last_seg && p.last)) {
+      constexpr int kParts = !kBf16 ? 1 : kOut && kDot == 0 ? 2 : 3;
       const float all = d.all;
 #pragma unroll
       for (int mt = 0; mt < NM; ++mt)
@@ -809,8 +882,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         Frag<T> part[NT][kParts];
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 8 * g4]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 8 * g4 + 4]);
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 4 * g4]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&d.w[32 * k + 16 + 4 * g4]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float v[8];
@@ -821,35 +894,53 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         }
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt) {
-          const Frag<T> yf = frag_col<DA, 8>(m.y, 32 * k, 32 * (mt >> 1) + 4 * (mt & 1), lane);
+          const Frag<T> yf = frag_col<DA, 4>(m.y, 32 * k, 16 * mt, lane);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int q = 0; q < kParts; ++q) mma(s[mt][t], yf, part[t][q]);
+        }
+        if constexpr (kParts == 2) {
+          if (last_seg && p.last) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              float v[8], v0[8], v1[8];
+              unpack(zf[k][t], v);
+              unpack(part[t][0], v0);
+              unpack(part[t][1], v1);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = __builtin_fmaf(v[e], e < 4 ? w0[e] : w1[e - 4], -v0[e]) - v1[e];
+              split(v, reinterpret_cast<Frag<T>(&)[1]>(part[t][0]));
+            }
+#pragma unroll
+            for (int mt = 0; mt < NM; ++mt) {
+              const Frag<T> yf = frag_col<DA, 4>(m.y, 32 * k, 16 * mt, lane);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma(s[mt][t], yf, part[t][0]);
+            }
+          }
         }
       }
     }
     if constexpr (!kOut) {
       if (tid == 0) head_sum += d.hi[C - 1];     // the segment's log decay
     }
-    if (wave == 0 && it + 1 < chunks)
-      decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? next.g : 0.0f, scale, lane);
+    if (!kOut && wave == 0 && it + 1 < chunks)
+      decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
+    g_next = g_after;
     block_sync();
   };
   if (chunks > 0) {
+    const float g_first = fetch_g(0);
+    g_next = fetch_g(min(1, chunks - 1));
     fetch(sets[0], 0);
-    if (kSets == 2 && chunks > 1) fetch(sets[kSets - 1], 1);
-    if (wave == 0) decays<C, kRev>(m.d[0], lane < tokens_of(0) ? sets[0].g : 0.0f, scale, lane);
+    if constexpr (kSets == 2) fetch(sets[1], min(1, chunks - 1));
+    if (wave == 0) decays<C, kRev>(m.d[0], lane < tokens_of(0) ? g_first : 0.0f, scale, lane);
   }
-  if constexpr (kSets == 2) {
-    int it = 0;
-    for (; it + 1 < chunks; it += 2) {
-      step(it, sets[0], sets[1]);
-      step(it + 1, sets[1], sets[0]);
-    }
-    if (it < chunks) step(it, sets[0], sets[1]);
-  } else {
-    for (int it = 0; it < chunks; ++it) step(it, sets[0], sets[0]);
+  for (int it = 0; it < chunks; it += kSets) {
+    step(it, sets[0]);
+    if (kSets == 2 && it + 1 < chunks) step(it + 1, sets[kSets - 1]);
   }
 
   if constexpr (kDot == 2) {

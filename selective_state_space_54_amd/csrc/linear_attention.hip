@@ -3,6 +3,7 @@
 // the sums over heads that share queries and keys, and the order of launches.
 // The matrix products are in linear_attention.h.
 #include "la_args.h"
+#include <cstdlib>
 #include "linear_attention.h"
 #include "mssm_internal.h"
 
@@ -208,6 +209,8 @@ View view_of(const void* p, int64_t row, int div) {
   return v;
 }
 
+bool word_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 constexpr size_t kAlign = 256;
 size_t round_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
@@ -231,7 +234,7 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
     seg = (s.tokens * s.heads + kBlocks - 1) / kBlocks;
     if (seg < kLeast) seg = kLeast;
   }
-  if (backward && seg > 1024) seg = 1024;
+  if (const char* ev = getenv("LA_SEGS")) { int64_t n = atoll(ev); seg = s.packed ? (s.tokens * s.heads + n - 1) / n : (len + n - 1) / n; }
   if (seg > len) seg = len;
   seg = (seg + kChunk - 1) / kChunk * kChunk;
   if (seg < kChunk) seg = kChunk;
@@ -308,6 +311,7 @@ hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStrea
   p.init = a.state;
   p.last = a.last;
   p.out = a.o;
+  p.out_aligned = word_aligned(p.out);
   return la::pass_fwd(a.dtype, p, stream);
 }
 
@@ -363,6 +367,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.states) : nullptr;
     p.out = rep > 1 ? at(plan.dq) : d.dq;
     p.out_f32 = rep > 1;
+    p.out_aligned = word_aligned(p.out);
     if ((err = la::pass_dq(a.dtype, p, stream)) != hipSuccess) return err;
   }
   {
@@ -374,6 +379,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
     p.out = rep > 1 ? at(plan.dk) : d.dk;
     p.out_f32 = rep > 1;
+    p.out_aligned = word_aligned(p.out);
     p.dg = a.per_token ? d.dg : nullptr;
     p.head_part = a.per_token ? nullptr : at(plan.head_part);
     if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;
@@ -387,6 +393,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
     p.last = d.dstate;
     p.out = d.dv;
+    p.out_aligned = word_aligned(p.out);
     if ((err = la::pass_dv(a.dtype, p, stream)) != hipSuccess) return err;
   }
   if (rep > 1 && s.tokens > 0) {

@@ -720,6 +720,51 @@ def selective_scan_bwd(x, delta, A, B, C, dout, *, Dskip=None, z=None, h0=None, 
 
 
 # ---- linear attention with a decay for each head ---------------------------------------------
+#
+# These calls are made once a layer and token when serving, so their checks are
+# written to cost little: one look at each tensor, the messages only where it fails.
+
+def _fits(t, dtype, shape, dev):
+    """Whether t is a dense tensor of this dtype and shape on GPU number dev."""
+    return (t.dtype is dtype and t.get_device() == dev and t.shape == shape and
+            t.is_contiguous())
+
+
+def _expect(t, name, dtype, shape, dev):
+    if not (isinstance(t, torch.Tensor) and _fits(t, dtype, shape, dev)):
+        _dense(t, name, dtype, shape, torch.device("cuda", dev))
+
+
+def _expect_optional(t, name, dtype, shape, dev):
+    if t is not None:
+        _expect(t, name, dtype, shape, dev)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gpu_of(t, name):
+    """The number of the GPU that t is on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _dtype_code(t.dtype)
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU device")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """The C entry point on GPU `dev`, on `stream` or that GPU's current stream."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    status = getattr(_lib or load(), name)(*args, raw)
+    if status != MSSM_SUCCESS:
+        raise MssmError(status, name)
+
 
 def mssm_linear_attention_supports(dk: int, dv: int) -> bool:
     return bool(load().mssm_linear_attention_supports(dk, dv))
@@ -735,21 +780,18 @@ def mssm_linear_attention_workspace_size(seqs, L, key_heads, heads, dk, dv, dtyp
     return out.value
 
 
-def _token_rows(t, name, dtype, shape, device):
+def _token_rows(t, name, dtype, shape, dev):
     """Checks a [tokens.., heads, d] tensor whose tokens are evenly spaced (a view into a
     wider projection's output is one) and returns the elements between tokens."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _dense(t, name, dtype, shape, torch.device("cuda", dev))
+    dense = shape[-2] * shape[-1]
     if t.is_contiguous():
-        return shape[-2] * shape[-1]
-    st, dense = t.stride(), shape[-2] * shape[-1]
-    lead = [i for i in range(len(shape) - 2) if shape[i] > 1]      # strides of single entries say nothing
+        return dense
+    st = t.stride()
+    lead = [i for i in range(len(shape) - 2) if shape[i] > 1]   # strides of single entries say nothing
     row = st[lead[-1]] if lead else dense
     even = len(lead) < 2 or st[0] == shape[1] * row
     if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]) or row < dense or not even:
@@ -758,54 +800,55 @@ def _token_rows(t, name, dtype, shape, device):
 
 
 def _la_check(q, k, v, log_decay, seq_offsets, single=False):
-    """Sizes, token rows and the decay's form of a linear attention call: (lead, seqs, L, Hk, H,
-    dk, dv, rows, decay), lead the token dimensions."""
-    lead_dims = 1 if single or seq_offsets is not None else 2
-    if q.dim() != lead_dims + 2 or v.dim() != lead_dims + 2:
-        lead = "[tokens" if lead_dims == 1 else "[batch, L"
+    """Checks a linear attention call's inputs.  Returns the GPU, the token dimensions, the
+    sizes (seqs, L, key_heads, heads, dk, dv) and what the C call takes after them."""
+    dev = _gpu_of(q, "q")
+    dt = q.dtype
+    dims = 1 if single or seq_offsets is not None else 2
+    qs, vs = q.shape, v.shape
+    if len(qs) != dims + 2 or len(vs) != dims + 2:
+        lead = "[tokens" if dims == 1 else "[batch, L"
         raise ValueError(f"q, k and v must be {lead}, heads, head size]")
-    _dtype_code(q.dtype)
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a GPU device")
-    lead = q.shape[:lead_dims]
-    key_heads, dk = q.shape[-2:]
-    heads, dv = v.shape[-2:]
-    rows = (_token_rows(q, "q", q.dtype, q.shape, dev), _token_rows(k, "k", q.dtype, q.shape, dev),
-            _token_rows(v, "v", q.dtype, lead + (heads, dv), dev))
-    if log_decay.dim() == 1:
-        _dense(log_decay, "log_decay", torch.float32, (heads,), dev)
-        decay = MSSM_DECAY_PER_HEAD
-    else:
-        _dense(log_decay, "log_decay", torch.float32, lead + (heads,), dev)
-        decay = MSSM_DECAY_PER_TOKEN
+    lead, vt = qs[:dims], vs[dims:]
+    key_heads, dk = qs[dims:]
+    heads, dv = vt
+    rows = (_token_rows(q, "q", dt, qs, dev), _token_rows(k, "k", dt, qs, dev),
+            _token_rows(v, "v", dt, lead + vt, dev))
+    per_token = log_decay.dim() != 1
+    _expect(log_decay, "log_decay", torch.float32, lead + vt[:1] if per_token else vt[:1], dev)
     if seq_offsets is not None:
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
             raise ValueError("seq_offsets must be [sequences + 1]")
-        _dense(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
+        _expect(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
         seqs, L = seq_offsets.shape[0] - 1, lead[0]
     else:
         seqs, L = lead[0], 1 if single else lead[1]
-    return lead, seqs, L, key_heads, heads, dk, dv, rows, decay
+    decay = MSSM_DECAY_PER_TOKEN if per_token else MSSM_DECAY_PER_HEAD
+    return dev, lead, (seqs, L, key_heads, heads, dk, dv), decay, rows + (_DTYPES[dt],)
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _workspace(nbytes, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _fwd(checked, q, k, v, log_decay, seq_offsets, state, o, last_state, scale, workspace, stream):
+    dev, _, sizes, decay, tail = checked
+    _call("mssm_linear_attention_fwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), _address(seq_offsets), _address(state), o.data_ptr(),
+          _address(last_state), sizes[4] ** -0.5 if scale is None else scale, decay,
+          _address(workspace), _bytes_of(workspace), *sizes, *tail)
 
 
 def mssm_linear_attention_fwd(q, k, v, log_decay, o, workspace, *, scale, state=None,
                               last_state=None, seq_offsets=None, stream=None):
     """o (and last_state) <- linear attention (see linear_attention); workspace is a uint8
     GPU tensor of mssm_linear_attention_workspace_size bytes, or None where that is 0."""
-    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
-    dev = q.device
-    _dense(o, "o", q.dtype, lead + (H, dv), dev)
-    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
-    _check_optional(last_state, "last_state", torch.float32, (seqs, H, dk, dv), dev)
-    _check(load().mssm_linear_attention_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(o),
-        _ptr(last_state), scale, decay, _ptr(workspace), _bytes_of(workspace), seqs, L, Hk, H, dk,
-        dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_fwd")
+    checked = _la_check(q, k, v, log_decay, seq_offsets)
+    dev, lead, (seqs, _, _, H, dk, dv), _, _ = checked
+    _expect(o, "o", q.dtype, lead + (H, dv), dev)
+    _expect_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    _expect_optional(last_state, "last_state", torch.float32, (seqs, H, dk, dv), dev)
+    _fwd(checked, q, k, v, log_decay, seq_offsets, state, o, last_state, scale, workspace, stream)
     return o
 
 
@@ -820,20 +863,18 @@ def linear_attention(q, k, v, log_decay, *, scale=None, state=None, seq_offsets=
     as they are.  log_decay float32 [batch, L, heads] ([tokens, heads]) or [heads].  scale
     defaults to dk ** -0.5.  ``state`` float32 [sequences, heads, dk, dv] is the state before
     the first token (default zero).  Returns o, or (o, last state)."""
-    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
-    dev = q.device
-    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
-    nbytes = mssm_linear_attention_workspace_size(seqs, L, Hk, H, dk, dv, q.dtype,
-                                                  packed=seq_offsets is not None)
+    checked = _la_check(q, k, v, log_decay, seq_offsets)
+    dev, lead, sizes, _, _ = checked
+    seqs, _, _, H, dk, dv = sizes
+    if state is not None:
+        _expect(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    nbytes = mssm_linear_attention_workspace_size(*sizes, q.dtype, packed=seq_offsets is not None)
     with _on(stream):
         o = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
         last = (torch.empty((seqs, H, dk, dv), dtype=torch.float32, device=dev)
                 if return_state else None)
         ws = _workspace(nbytes, dev)
-    _check(load().mssm_linear_attention_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(o),
-        _ptr(last), dk ** -0.5 if scale is None else scale, decay, _ptr(ws), nbytes, seqs, L, Hk,
-        H, dk, dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_fwd")
+    _fwd(checked, q, k, v, log_decay, seq_offsets, state, o, last, scale, ws, stream)
     return (o, last) if return_state else o
 
 
@@ -841,25 +882,24 @@ def mssm_linear_attention_step(q, k, v, log_decay, state, o, *, scale, stream=No
     """One token for each sequence: state [batch, heads, dk, dv] float32 is updated in place,
     o [batch, heads, dv] receives the output; q, k are [batch, key_heads, dk], v [batch, heads,
     dv], log_decay [batch, heads] or [heads]."""
-    lead, seqs, _, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, None, single=True)
-    _dense(state, "state", torch.float32, (seqs, H, dk, dv), q.device)
-    _dense(o, "o", q.dtype, (seqs, H, dv), q.device)
-    _check(load().mssm_linear_attention_step(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o), scale, decay, seqs, Hk,
-        H, dk, dv, *rows, _DTYPES[q.dtype], _stream_handle(stream)), "mssm_linear_attention_step")
+    dev, lead, (seqs, _, Hk, H, dk, dv), decay, tail = _la_check(q, k, v, log_decay, None, True)
+    _expect(state, "state", torch.float32, (seqs, H, dk, dv), dev)
+    _expect(o, "o", q.dtype, (seqs, H, dv), dev)
+    _call("mssm_linear_attention_step", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), state.data_ptr(), o.data_ptr(),
+          dk ** -0.5 if scale is None else scale, decay, seqs, Hk, H, dk, dv, *tail)
     return o
 
 
 def linear_attention_step(q, k, v, log_decay, state, *, scale=None, stream=None):
     """Allocate o, run mssm_linear_attention_step (state updated in place), return o.  scale
     defaults to dk ** -0.5."""
-    if v.dim() != 3:
-        raise ValueError("q, k and v must be [tokens, heads, head size]")
-    with _on(stream):
+    if stream is None:
         o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-    return mssm_linear_attention_step(q, k, v, log_decay, state, o,
-                                      scale=q.shape[-1] ** -0.5 if scale is None else scale,
-                                      stream=stream)
+    else:
+        with _on(stream):
+            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    return mssm_linear_attention_step(q, k, v, log_decay, state, o, scale=scale, stream=stream)
 
 
 def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, scale, state=None,
@@ -867,25 +907,24 @@ def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, sca
     """Gradients of sum(dout * o) + sum(dstate * last state) of linear_attention.  ``grads``
     maps dq, dk, dv (of the inputs' dtype), dlog_decay (float32) and, for the initial state's,
     dstate to dense tensors that are overwritten."""
-    lead, seqs, L, Hk, H, dk, dv, rows, decay = _la_check(q, k, v, log_decay, seq_offsets)
-    dev = q.device
-    _dense(dout, "dout", q.dtype, lead + (H, dv), dev)
-    _check_optional(state, "state", torch.float32, (seqs, H, dk, dv), dev)
-    _check_optional(dstate, "dstate", torch.float32, (seqs, H, dk, dv), dev)
-    shapes = {"dq": (q.dtype, tuple(q.shape)), "dk": (q.dtype, tuple(q.shape)),
-              "dv": (q.dtype, tuple(v.shape)),
-              "dlog_decay": (torch.float32, tuple(log_decay.shape)),
-              "dstate": (torch.float32, (seqs, H, dk, dv))}
+    dev, lead, sizes, decay, tail = _la_check(q, k, v, log_decay, seq_offsets)
+    seqs, _, _, H, dk, dv = sizes
+    states = (seqs, H, dk, dv)
+    _expect(dout, "dout", q.dtype, lead + (H, dv), dev)
+    _expect_optional(state, "state", torch.float32, states, dev)
+    _expect_optional(dstate, "dstate", torch.float32, states, dev)
+    shapes = {"dq": (q.dtype, q.shape), "dk": (q.dtype, q.shape), "dv": (q.dtype, v.shape),
+              "dlog_decay": (torch.float32, log_decay.shape), "dstate": (torch.float32, states)}
     for name, t in grads.items():
         if name not in shapes:
             raise ValueError(f"unknown gradient {name}")
-        _dense(t, name, *shapes[name], dev)
-    g = lambda name: _ptr(grads.get(name))
-    _check(load().mssm_linear_attention_bwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(seq_offsets), _ptr(state), _ptr(dout),
-        _ptr(dstate), g("dq"), g("dk"), g("dv"), g("dlog_decay"), g("dstate"), scale, decay,
-        _ptr(workspace), _bytes_of(workspace), seqs, L, Hk, H, dk, dv, *rows, _DTYPES[q.dtype],
-        _stream_handle(stream)), "mssm_linear_attention_bwd")
+        _expect(t, name, *shapes[name], dev)
+    g = lambda name: _address(grads.get(name))
+    _call("mssm_linear_attention_bwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), _address(seq_offsets), _address(state), dout.data_ptr(),
+          _address(dstate), g("dq"), g("dk"), g("dv"), g("dlog_decay"), g("dstate"),
+          dk ** -0.5 if scale is None else scale, decay, _address(workspace),
+          _bytes_of(workspace), *sizes, *tail)
     return grads
 
 
@@ -894,52 +933,48 @@ def linear_attention_bwd(q, k, v, log_decay, dout, *, scale=None, state=None, ds
     """Allocate the gradients and the workspace with torch, then run mssm_linear_attention_bwd;
     returns the dict of gradients (dq, dk, dv, dlog_decay, and dstate, the initial state's,
     where ``state`` is given).  ``dstate`` is the gradient of the last state, if it has one."""
-    _, seqs, L, Hk, H, dk, dv, _, _ = _la_check(q, k, v, log_decay, seq_offsets)
-    dev = q.device
-    nbytes = mssm_linear_attention_workspace_size(seqs, L, Hk, H, dk, dv, q.dtype, backward=True,
+    dev, _, sizes, _, _ = _la_check(q, k, v, log_decay, seq_offsets)
+    nbytes = mssm_linear_attention_workspace_size(*sizes, q.dtype, backward=True,
                                                   packed=seq_offsets is not None)
     with _on(stream):
-        empty = lambda like, shape: torch.empty(shape, dtype=like.dtype, device=dev)
-        grads = {"dq": empty(q, q.shape), "dk": empty(k, k.shape), "dv": empty(v, v.shape),
-                 "dlog_decay": empty(log_decay, log_decay.shape)}
+        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
+        grads = {"dq": empty(q), "dk": empty(k), "dv": empty(v), "dlog_decay": empty(log_decay)}
         if state is not None:
-            grads["dstate"] = empty(state, state.shape)
+            grads["dstate"] = empty(state)
         ws = _workspace(nbytes, dev)
-    return mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, ws, state=state,
-                                     dstate=dstate, seq_offsets=seq_offsets, stream=stream,
-                                     scale=dk ** -0.5 if scale is None else scale)
+    return mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, ws, scale=scale, state=state,
+                                     dstate=dstate, seq_offsets=seq_offsets, stream=stream)
 
 
 # ---- layer norm ----------------------------------------------------------------------------------
 
 def _norm_rows(x, weight):
-    if x.dim() < 1:
+    """The GPU, the rows and the row length of x, which is checked with weight."""
+    dev = _gpu_of(x, "x")
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must be [.., D]")
-    _dtype_code(x.dtype)
-    if x.device.type != "cuda":
-        raise ValueError("tensors must be on a GPU device")
-    D = x.shape[-1]
-    _dense(x, "x", x.dtype, x.shape, x.device)
-    _dense(weight, "weight", torch.float32, (D,), x.device)
-    return x.numel() // D if D else 0, D
+    D = shape[-1]
+    _expect(x, "x", x.dtype, shape, dev)
+    _expect(weight, "weight", torch.float32, (D,), dev)
+    return dev, x.numel() // D if D else 0, D
 
 
 def mssm_layer_norm_fwd(x, weight, bias, y, *, residual=None, total=None, mean=None, rstd=None,
                         eps=1e-5, stream=None):
     """y <- layer norm of x (of total <- x + residual where a residual is given) over the last
     dimension; mean and rstd (float32, one value a row) receive the rows' statistics."""
-    rows, D = _norm_rows(x, weight)
-    dev = x.device
-    _check_optional(bias, "bias", torch.float32, (D,), dev)
-    _dense(y, "y", x.dtype, x.shape, dev)
-    _check_optional(residual, "residual", x.dtype, x.shape, dev)
-    _check_optional(total, "total", x.dtype, x.shape, dev)
-    _check_optional(mean, "mean", torch.float32, x.shape[:-1], dev)
-    _check_optional(rstd, "rstd", torch.float32, x.shape[:-1], dev)
-    _check(load().mssm_layer_norm_fwd(
-        _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(total), _ptr(mean),
-        _ptr(rstd), eps, rows, D, _DTYPES[x.dtype], _stream_handle(stream)),
-        "mssm_layer_norm_fwd")
+    dev, rows, D = _norm_rows(x, weight)
+    dt, shape = x.dtype, x.shape
+    _expect_optional(bias, "bias", torch.float32, (D,), dev)
+    _expect(y, "y", dt, shape, dev)
+    _expect_optional(residual, "residual", dt, shape, dev)
+    _expect_optional(total, "total", dt, shape, dev)
+    _expect_optional(mean, "mean", torch.float32, shape[:-1], dev)
+    _expect_optional(rstd, "rstd", torch.float32, shape[:-1], dev)
+    _call("mssm_layer_norm_fwd", dev, stream, x.data_ptr(), _address(residual), weight.data_ptr(),
+          _address(bias), y.data_ptr(), _address(total), _address(mean), _address(rstd), eps, rows,
+          D, _DTYPES[dt])
     return y
 
 
@@ -976,19 +1011,18 @@ def mssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace
     """dx, dweight (and dbias, unless None) <- gradients of the layer norm of x (what was
     normalised) with its mean and rstd; dsum, the gradient that reaches x itself, is added to
     dx."""
-    rows, D = _norm_rows(x, weight)
-    dev = x.device
-    _dense(dy, "dy", x.dtype, x.shape, dev)
-    _dense(mean, "mean", torch.float32, x.shape[:-1], dev)
-    _dense(rstd, "rstd", torch.float32, x.shape[:-1], dev)
-    _check_optional(dsum, "dsum", x.dtype, x.shape, dev)
-    _dense(dx, "dx", x.dtype, x.shape, dev)
-    _dense(dweight, "dweight", torch.float32, (D,), dev)
-    _check_optional(dbias, "dbias", torch.float32, (D,), dev)
-    _check(load().mssm_layer_norm_bwd(
-        _ptr(dy), _ptr(dsum), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
-        _ptr(dweight), _ptr(dbias), _ptr(workspace), _bytes_of(workspace), rows, D,
-        _DTYPES[x.dtype], _stream_handle(stream)), "mssm_layer_norm_bwd")
+    dev, rows, D = _norm_rows(x, weight)
+    dt, shape = x.dtype, x.shape
+    _expect(dy, "dy", dt, shape, dev)
+    _expect(mean, "mean", torch.float32, shape[:-1], dev)
+    _expect(rstd, "rstd", torch.float32, shape[:-1], dev)
+    _expect_optional(dsum, "dsum", dt, shape, dev)
+    _expect(dx, "dx", dt, shape, dev)
+    _expect(dweight, "dweight", torch.float32, (D,), dev)
+    _expect_optional(dbias, "dbias", torch.float32, (D,), dev)
+    _call("mssm_layer_norm_bwd", dev, stream, dy.data_ptr(), _address(dsum), x.data_ptr(),
+          weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+          _address(dbias), _address(workspace), _bytes_of(workspace), rows, D, _DTYPES[dt])
     return dx
 
 
@@ -996,8 +1030,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, dsum=None, bias=True, stream=No
     """Allocate the gradients and the workspace with torch, then run mssm_layer_norm_bwd;
     returns a dict of dx, dweight and (``bias``) dbias.  x is what was normalised: with a
     residual, the total that layer_norm returned."""
-    rows, D = _norm_rows(x, weight)
-    dev = x.device
+    dev, rows, D = _norm_rows(x, weight)
     nbytes = mssm_layer_norm_bwd_workspace_size(rows, D, x.dtype)
     with _on(stream):
         grads = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
