@@ -41,9 +41,8 @@ struct PassArgs {
   float* seg_out = nullptr;          // [slots, heads, ..]: each segment's own state
   float* seg_decay = nullptr;        // [slots, heads]
   // output
-  void* out = nullptr;               // [tokens, heads, dB]
-  bool out_f32 = false;              // else of the inputs' type
-  bool out_aligned = true;           // to 4 bytes
+  void* out = nullptr;               // [tokens, heads, dB], of the inputs' type
+  bool out_f32 = false;              // dq, dk: float32 instead
   // gradient of the log decays: written by dq, read by dk
   float* u = nullptr;                // [tokens, heads]
   float* q_sums = nullptr;           // [slots, chunks_per_slot, heads]

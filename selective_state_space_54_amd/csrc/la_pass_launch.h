@@ -7,22 +7,30 @@
 namespace mssm {
 namespace la {
 
-template <typename T, int DA, int NT, bool kRev, bool kOut, int kDot>
+template <typename T, typename V, int DA, int NT, bool kRev, bool kOut, int kDot>
 hipError_t launch_pass_as(const PassArgs& p, hipStream_t stream) {
   constexpr int C = sizeof(T) == 2 ? 64 : 32;
   const int64_t blocks = p.grid.slots * p.heads;
-  hipLaunchKernelGGL((la_pass<T, C, DA, NT, kRev, kOut, kDot>), dim3(static_cast<uint32_t>(blocks)),
+  hipLaunchKernelGGL((la_pass<T, V, C, DA, NT, kRev, kOut, kDot>), dim3(static_cast<uint32_t>(blocks)),
                      dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
+template <typename T, typename V, bool kRev, bool kOut, int kDot>
+hipError_t launch_pass_to(const PassArgs& p, hipStream_t stream) {
+  if (p.dA <= 64)
+    return p.dB <= 64 ? launch_pass_as<T, V, 64, 1, kRev, kOut, kDot>(p, stream)
+                      : launch_pass_as<T, V, 64, 2, kRev, kOut, kDot>(p, stream);
+  return p.dB <= 64 ? launch_pass_as<T, V, 128, 1, kRev, kOut, kDot>(p, stream)
+                    : launch_pass_as<T, V, 128, 2, kRev, kOut, kDot>(p, stream);
+}
+
 template <typename T, bool kRev, bool kOut, int kDot>
 hipError_t launch_pass(const PassArgs& p, hipStream_t stream) {
-  if (p.dA <= 64)
-    return p.dB <= 64 ? launch_pass_as<T, 64, 1, kRev, kOut, kDot>(p, stream)
-                      : launch_pass_as<T, 64, 2, kRev, kOut, kDot>(p, stream);
-  return p.dB <= 64 ? launch_pass_as<T, 128, 1, kRev, kOut, kDot>(p, stream)
-                    : launch_pass_as<T, 128, 2, kRev, kOut, kDot>(p, stream);
+  if constexpr (kDot != 0 && sizeof(T) == 2) {
+    if (p.out_f32) return launch_pass_to<T, float, kRev, kOut, kDot>(p, stream);
+  }
+  return launch_pass_to<T, T, kRev, kOut, kDot>(p, stream);
 }
 
 }  // namespace la

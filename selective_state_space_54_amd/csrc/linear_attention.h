@@ -130,11 +130,19 @@ __device__ __forceinline__ Frag<float> frag_of(const float* a, const float* b) {
   return f;
 }
 
+// An 8-byte LDS read of its own: the compiler would join the reads of two rows
+// into one instruction, whose four registers are then no operand of either.
+__device__ __forceinline__ uint2 lds_read8(const uint16_t* p) {
+  using lds_ptr = const volatile __attribute__((address_space(3))) u32x2*;
+  const u32x2 u = *(lds_ptr)(p);
+  return make_uint2(u.x, u.y);
+}
+
 // Terms c .. c + 31 of row r of a tile; c = 32 k + 4 (lane / 16).
 template <int D>
 __device__ __forceinline__ Frag<uint16_t> frag_row(const uint16_t* t, int r, int c) {
-  return frag_of(*reinterpret_cast<const uint2*>(t + tile_at<uint16_t, D>(r, c)),
-                 *reinterpret_cast<const uint2*>(t + tile_at<uint16_t, D>(r, c + 16)));
+  return frag_of(lds_read8(t + tile_at<uint16_t, D>(r, c)),
+                 lds_read8(t + tile_at<uint16_t, D>(r, c + 16)));
 }
 template <int D>
 __device__ __forceinline__ Frag<float> frag_row(const float* t, int r, int c) {
@@ -142,7 +150,7 @@ __device__ __forceinline__ Frag<float> frag_row(const float* t, int r, int c) {
 }
 // The same of a plain row.
 __device__ __forceinline__ Frag<uint16_t> frag_at(const uint16_t* p) {
-  return frag_of(*reinterpret_cast<const uint2*>(p), *reinterpret_cast<const uint2*>(p + 16));
+  return frag_of(lds_read8(p), lds_read8(p + 16));
 }
 __device__ __forceinline__ Frag<float> frag_at(const float* p) { return frag_of(p, p + 16); }
 
@@ -428,6 +436,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // ---- the pass ----------------------------------------------------------------------------------------
 
+// V: the type the output is stored in.
 // kOut false: only the state over the segment (no x, no output).
 // kDot 0: nothing more.  1 (dq): also W and q . dqc, as one sum u for each
 // token, and the state before some of the chunks.  2 (dk): also k . dkc, and dg
@@ -454,7 +463,7 @@ struct Lds {
 template <int C>
 constexpr int kStride = 256 / C;
 
-template <typename T, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
+template <typename T, typename V, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
 __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kStateParts = kBf16 && kDot != 0 ? 3 : 1;  // of the state as an operand
@@ -565,9 +574,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   };
   // The chunk being worked on: where its output, and what is dotted with it, begin.
   const uint32_t o_row = static_cast<uint32_t>(p.heads) * p.dB;
-  char* out = kOut ? static_cast<char*>(p.out) +
-                         (first * o_row + int64_t(h) * p.dB) * (p.out_f32 ? 4 : int(sizeof(T)))
-                   : nullptr;
+  V* out = kOut ? static_cast<V*>(p.out) + first * o_row + int64_t(h) * p.dB : nullptr;
   const T* dotted = kDot == 2 ? begin(p.e, p.dB) : nullptr;
   float* u_at = kDot != 0 ? p.u + first * p.heads + h : nullptr;
   float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
@@ -798,29 +805,16 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         }
       // Stores through a descriptor that ends with the chunk's last value: rows and
       // columns past it are dropped by the hardware, so no branch stands around them.
-      auto store = [&](auto value) __attribute__((always_inline)) {
-        using V = decltype(value);
-        if (p.out_aligned) {
-          const buf_t to = make_buf(out, ((n - 1) * o_row + p.dB) * static_cast<uint32_t>(sizeof(V)));
-          const uint32_t c = col_of(0, 4 * g4);
+      // (Buffer accesses, too, take any alignment.)
+      {
+        const buf_t to = make_buf(out, ((n - 1) * o_row + p.dB) * static_cast<uint32_t>(sizeof(V)));
+        const uint32_t c = col_of(0, 4 * g4);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const uint32_t off = c < static_cast<uint32_t>(p.dB) ? (16 * r + l16) * o_row + c : 0x3ffffff0u;
-            buf_store<V, NT>(to, off * static_cast<uint32_t>(sizeof(V)), acc[r]);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const int i = 16 * r + l16, c = col_of(t, 4 * g4);
-              if (i < n && c < p.dB)
-                store4(reinterpret_cast<V*>(out) + static_cast<uint32_t>(i) * o_row + c, acc[r][t]);
-            }
+        for (int r = 0; r < NR; ++r) {
+          const uint32_t off = c < static_cast<uint32_t>(p.dB) ? (16 * r + l16) * o_row + c : 0x3ffffff0u;
+          buf_store<V, NT>(to, off * static_cast<uint32_t>(sizeof(V)), acc[r]);
         }
-      };
-      if (p.out_f32) store(0.0f);
-      else store(T());
+      }
       if constexpr (kDot == 1) {
         if (wave == 0) {
           const int t = min(lane, C - 1), tt = t >> 4;
@@ -862,7 +856,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       }
     }
 
-    if constexpr (kOut) out += kAhead * static_cast<int64_t>(o_row) * (p.out_f32 ? 4 : int(sizeof(T)));
+    if constexpr (kOut) out += kAhead * static_cast<int64_t>(o_row);
     if constexpr (kDot == 2) {
       dotted += kAhead * static_cast<int64_t>(e_row);
       dg_at += kAhead * p.heads;
@@ -934,13 +928,34 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   if (chunks > 0) {
     const float g_first = fetch_g(0);
     g_next = fetch_g(min(1, chunks - 1));
+    // Each set's first loads are followed by as many stores as later ones (into an
+    // empty buffer, dropped): the waits in the loop then leave that many in flight,
+    // where for the sake of the first turn they would otherwise drain them.
+    auto no_stores = [&](int k) __attribute__((always_inline)) {
+      if constexpr (kOut) {
+        const buf_t none = make_buf(out, 0);
+        const f32x4 zero[NT] = {};
+#pragma unroll
+        for (int r = 0; r < NR; ++r) buf_store<V, NT>(none, 64 * (NR * k + r), zero);
+      }
+    };
     fetch(sets[0], 0);
-    if constexpr (kSets == 2) fetch(sets[1], min(1, chunks - 1));
+    no_stores(0);
+    if constexpr (kSets == 2) {
+      fetch(sets[1], min(1, chunks - 1));
+      no_stores(1);
+    }
     if (wave == 0) decays<C, kRev>(m.d[0], lane < tokens_of(0) ? g_first : 0.0f, scale, lane);
   }
-  for (int it = 0; it < chunks; it += kSets) {
-    step(it, sets[0]);
-    if (kSets == 2 && it + 1 < chunks) step(it + 1, sets[kSets - 1]);
+  int it = 0;
+  if constexpr (kSets == 2) {
+    for (; it + 1 < chunks; it += 2) {
+      step(it, sets[0]);
+      step(it + 1, sets[1]);
+    }
+    if (it < chunks) step(it, sets[0]);
+  } else {
+    for (; it < chunks; ++it) step(it, sets[0]);
   }
 
   if constexpr (kDot == 2) {

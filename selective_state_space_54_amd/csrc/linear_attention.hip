@@ -3,7 +3,6 @@
 // the sums over heads that share queries and keys, and the order of launches.
 // The matrix products are in linear_attention.h.
 #include "la_args.h"
-#include <cstdlib>
 #include "linear_attention.h"
 #include "mssm_internal.h"
 
@@ -209,8 +208,6 @@ View view_of(const void* p, int64_t row, int div) {
   return v;
 }
 
-bool word_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
-
 constexpr size_t kAlign = 256;
 size_t round_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
@@ -226,18 +223,22 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   g.seqs = s.seqs;
   g.tokens = s.tokens;
   g.L = s.packed ? 0 : (s.seqs > 0 ? s.tokens / s.seqs : 0);
-  const int64_t kBlocks = 1024, kLeast = 512, kChunk = 64;
+  // Blocks to aim for: two on each of the 256 compute units at once, once
+  // (backward) or twice over; a few blocks more than a multiple of 512 would be a
+  // round of their own (1 x 131072, 20 heads of 128: 972 us with 500 or 1000
+  // blocks, 1125 with 1040).  Segments of at least two chunks: below that the
+  // states' traffic is more than the tiles' (4 x 2048, 16 heads of 128: 82 us with
+  // 512 blocks, 89 with 256).  From 256 sequences times heads on, one segment.
+  const int64_t chunk = bf16 ? 64 : 32, target = backward ? 512 : 1024;
   const int64_t rows = s.seqs * s.heads;
-  int64_t len = s.packed ? s.tokens : g.L;      // the longest a sequence can be
+  const int64_t len = s.packed ? s.tokens : g.L;      // the longest a sequence can be
   int64_t seg = len;
-  if (rows < 512 || s.packed) {
-    seg = (s.tokens * s.heads + kBlocks - 1) / kBlocks;
-    if (seg < kLeast) seg = kLeast;
-  }
-  if (const char* ev = getenv("LA_SEGS")) { int64_t n = atoll(ev); seg = s.packed ? (s.tokens * s.heads + n - 1) / n : (len + n - 1) / n; }
+  if (s.packed) seg = (s.tokens * s.heads + 2 * target - 1) / (2 * target);
+  else if (rows < 256) seg = (len + target / rows - 1) / (target / rows);
+  if (seg < 2 * chunk) seg = 2 * chunk;
   if (seg > len) seg = len;
-  seg = (seg + kChunk - 1) / kChunk * kChunk;
-  if (seg < kChunk) seg = kChunk;
+  seg = (seg + chunk - 1) / chunk * chunk;
+  if (seg < chunk) seg = chunk;
   g.seg_len = seg;
   g.segs = s.packed ? 0 : (len + seg - 1) / seg;
   if (!s.packed && g.segs < 1) g.segs = 1;
@@ -261,7 +262,7 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
       p.rev_states = take(state * g.slots);
       p.rev_decay = take(per_slot);
     }
-    const int chunk = bf16 ? 64 : 32, every = 256 / chunk;
+    const int64_t every = 256 / chunk;
     p.chunks_per_slot = seg / chunk;
     p.dumps_per_slot = (p.chunks_per_slot + every - 1) / every;
     const size_t held = static_cast<size_t>(s.dk <= 64 ? 64 : 128) * (s.dv <= 64 ? 64 : 128) * 4;
@@ -311,7 +312,6 @@ hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStrea
   p.init = a.state;
   p.last = a.last;
   p.out = a.o;
-  p.out_aligned = word_aligned(p.out);
   return la::pass_fwd(a.dtype, p, stream);
 }
 
@@ -367,7 +367,6 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.states) : nullptr;
     p.out = rep > 1 ? at(plan.dq) : d.dq;
     p.out_f32 = rep > 1;
-    p.out_aligned = word_aligned(p.out);
     if ((err = la::pass_dq(a.dtype, p, stream)) != hipSuccess) return err;
   }
   {
@@ -379,7 +378,6 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
     p.out = rep > 1 ? at(plan.dk) : d.dk;
     p.out_f32 = rep > 1;
-    p.out_aligned = word_aligned(p.out);
     p.dg = a.per_token ? d.dg : nullptr;
     p.head_part = a.per_token ? nullptr : at(plan.head_part);
     if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;
@@ -393,7 +391,6 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
     p.last = d.dstate;
     p.out = d.dv;
-    p.out_aligned = word_aligned(p.out);
     if ((err = la::pass_dv(a.dtype, p, stream)) != hipSuccess) return err;
   }
   if (rep > 1 && s.tokens > 0) {

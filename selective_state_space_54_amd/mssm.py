@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -217,10 +218,13 @@ def tuning(scan_order=None, chunk_len=None, chains_per_lane=None):
             mssm_set_tuning(k, v)
 
 
+_HERE_STREAM = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations for a call launched on `stream` are made on that stream, so
     the caching allocator orders their reuse after the call's kernels."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _HERE_STREAM
 
 
 def mssm_supports_state_size(N: int) -> bool:
@@ -721,8 +725,9 @@ def selective_scan_bwd(x, delta, A, B, C, dout, *, Dskip=None, z=None, h0=None, 
 
 # ---- linear attention with a decay for each head ---------------------------------------------
 #
-# These calls are made once a layer and token when serving, so their checks are
-# written to cost little: one look at each tensor, the messages only where it fails.
+# These calls are made once a layer and token when serving, so their checks cost
+# little: where every tensor is dense and of the expected shape, one condition
+# says so; the checks with messages (and strided views) come where it does not.
 
 def _fits(t, dtype, shape, dev):
     """Whether t is a dense tensor of this dtype and shape on GPU number dev."""
@@ -812,8 +817,13 @@ def _la_check(q, k, v, log_decay, seq_offsets, single=False):
     lead, vt = qs[:dims], vs[dims:]
     key_heads, dk = qs[dims:]
     heads, dv = vt
-    rows = (_token_rows(q, "q", dt, qs, dev), _token_rows(k, "k", dt, qs, dev),
-            _token_rows(v, "v", dt, lead + vt, dev))
+    if (k.dtype is dt and v.dtype is dt and k.shape == qs and vs[:dims] == lead and
+            k.get_device() == dev and v.get_device() == dev and q.is_contiguous() and
+            k.is_contiguous() and v.is_contiguous()):
+        rows = (key_heads * dk, key_heads * dk, heads * dv)
+    else:
+        rows = (_token_rows(q, "q", dt, qs, dev), _token_rows(k, "k", dt, qs, dev),
+                _token_rows(v, "v", dt, lead + vt, dev))
     per_token = log_decay.dim() != 1
     _expect(log_decay, "log_decay", torch.float32, lead + vt[:1] if per_token else vt[:1], dev)
     if seq_offsets is not None:
@@ -825,6 +835,11 @@ def _la_check(q, k, v, log_decay, seq_offsets, single=False):
         seqs, L = lead[0], 1 if single else lead[1]
     decay = MSSM_DECAY_PER_TOKEN if per_token else MSSM_DECAY_PER_HEAD
     return dev, lead, (seqs, L, key_heads, heads, dk, dv), decay, rows + (_DTYPES[dt],)
+
+
+@functools.lru_cache(maxsize=1024)
+def _la_workspace(sizes, dtype, packed, backward):
+    return mssm_linear_attention_workspace_size(*sizes, dtype, packed=packed, backward=backward)
 
 
 def _workspace(nbytes, dev):
@@ -868,9 +883,9 @@ def linear_attention(q, k, v, log_decay, *, scale=None, state=None, seq_offsets=
     seqs, _, _, H, dk, dv = sizes
     if state is not None:
         _expect(state, "state", torch.float32, (seqs, H, dk, dv), dev)
-    nbytes = mssm_linear_attention_workspace_size(*sizes, q.dtype, packed=seq_offsets is not None)
+    nbytes = _la_workspace(sizes, q.dtype, seq_offsets is not None, False)
     with _on(stream):
-        o = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
         last = (torch.empty((seqs, H, dk, dv), dtype=torch.float32, device=dev)
                 if return_state else None)
         ws = _workspace(nbytes, dev)
@@ -878,28 +893,35 @@ def linear_attention(q, k, v, log_decay, *, scale=None, state=None, seq_offsets=
     return (o, last) if return_state else o
 
 
-def mssm_linear_attention_step(q, k, v, log_decay, state, o, *, scale, stream=None):
-    """One token for each sequence: state [batch, heads, dk, dv] float32 is updated in place,
-    o [batch, heads, dv] receives the output; q, k are [batch, key_heads, dk], v [batch, heads,
-    dv], log_decay [batch, heads] or [heads]."""
-    dev, lead, (seqs, _, Hk, H, dk, dv), decay, tail = _la_check(q, k, v, log_decay, None, True)
+def _step(checked, q, k, v, log_decay, state, o, scale, stream):
+    dev, _, (seqs, _, Hk, H, dk, dv), decay, tail = checked
     _expect(state, "state", torch.float32, (seqs, H, dk, dv), dev)
-    _expect(o, "o", q.dtype, (seqs, H, dv), dev)
     _call("mssm_linear_attention_step", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), state.data_ptr(), o.data_ptr(),
           dk ** -0.5 if scale is None else scale, decay, seqs, Hk, H, dk, dv, *tail)
     return o
 
 
+def mssm_linear_attention_step(q, k, v, log_decay, state, o, *, scale, stream=None):
+    """One token for each sequence: state [batch, heads, dk, dv] float32 is updated in place,
+    o [batch, heads, dv] receives the output; q, k are [batch, key_heads, dk], v [batch, heads,
+    dv], log_decay [batch, heads] or [heads]."""
+    checked = _la_check(q, k, v, log_decay, None, True)
+    dev, _, (seqs, _, _, H, _, dv), _, _ = checked
+    _expect(o, "o", q.dtype, (seqs, H, dv), dev)
+    return _step(checked, q, k, v, log_decay, state, o, scale, stream)
+
+
 def linear_attention_step(q, k, v, log_decay, state, *, scale=None, stream=None):
     """Allocate o, run mssm_linear_attention_step (state updated in place), return o.  scale
     defaults to dk ** -0.5."""
+    checked = _la_check(q, k, v, log_decay, None, True)
     if stream is None:
-        o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         with _on(stream):
-            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-    return mssm_linear_attention_step(q, k, v, log_decay, state, o, scale=scale, stream=stream)
+            o = torch.empty_like(v, memory_format=torch.contiguous_format)
+    return _step(checked, q, k, v, log_decay, state, o, scale, stream)
 
 
 def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, scale, state=None,
@@ -934,8 +956,7 @@ def linear_attention_bwd(q, k, v, log_decay, dout, *, scale=None, state=None, ds
     returns the dict of gradients (dq, dk, dv, dlog_decay, and dstate, the initial state's,
     where ``state`` is given).  ``dstate`` is the gradient of the last state, if it has one."""
     dev, _, sizes, _, _ = _la_check(q, k, v, log_decay, seq_offsets)
-    nbytes = mssm_linear_attention_workspace_size(*sizes, q.dtype, backward=True,
-                                                  packed=seq_offsets is not None)
+    nbytes = _la_workspace(sizes, q.dtype, seq_offsets is not None, True)
     with _on(stream):
         empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
         grads = {"dq": empty(q), "dk": empty(k), "dv": empty(v), "dlog_decay": empty(log_decay)}
@@ -983,16 +1004,21 @@ def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, return_stats=Fa
     float32).  With ``residual``, x + residual is normalised and returned too (rounded to x's
     type).  ``return_stats``: also the rows' mean and rstd, for layer_norm_bwd.  Returns y, or
     (y[, total][, mean, rstd])."""
-    dev = x.device
+    dev, rows, D = _norm_rows(x, weight)
+    dt, shape = x.dtype, x.shape
+    _expect_optional(bias, "bias", torch.float32, (D,), dev)
+    _expect_optional(residual, "residual", dt, shape, dev)
+    total = mean = rstd = None
     with _on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        total = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
-        mean = rstd = None
+        y = torch.empty_like(x)
+        if residual is not None:
+            total = torch.empty_like(x)
         if return_stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    mssm_layer_norm_fwd(x, weight, bias, y, residual=residual, total=total, mean=mean, rstd=rstd,
-                        eps=eps, stream=stream)
+            mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            rstd = torch.empty_like(mean)
+    _call("mssm_layer_norm_fwd", dev, stream, x.data_ptr(), _address(residual), weight.data_ptr(),
+          _address(bias), y.data_ptr(), _address(total), _address(mean), _address(rstd), eps, rows,
+          D, _DTYPES[dt])
     if total is None and not return_stats:
         return y
     return (y,) + ((total,) if total is not None else ()) + ((mean, rstd) if return_stats else ())
