@@ -30,6 +30,7 @@ struct PassArgs {
   const float* g = nullptr;          // log decays
   int64_t g_row = 0;                 // heads, or 0: one for each head
   int heads = 0;
+  bool paired = false;               // two heads a block: they share x and y, dB <= 64
   int dA = 0, dB = 0;                // sizes of x, y and of z, out
   float scale = 1.0f;
   // states, element (a, b) at a * sA + b * sB of a head's dA * dB

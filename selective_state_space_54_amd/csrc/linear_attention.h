@@ -326,7 +326,10 @@ __device__ __forceinline__ uint32_t logical_block() {
 // loads, so that all are in flight at once and the wait for them counts what
 // was issued since (where branches meet, it would wait for everything).  Pieces
 // are read at any alignment.
-template <typename T, int C, int D>
+//
+// kHalves 2: the tile's columns are two heads' of D / 2 each, the second head's d
+// values following the first's.
+template <typename T, int C, int D, int kHalves = 1>
 struct Tile {
   static constexpr int kPer = 16 / sizeof(T);              // values in a 16-byte piece
   static constexpr int kRowPieces = D / kPer;
@@ -337,7 +340,9 @@ struct Tile {
 
   __device__ __forceinline__ void fetch(const T* base, uint32_t row, int n, int d) {
     const int r = threadIdx.x / kRowPieces;
-    const int c = min(static_cast<int>(threadIdx.x % kRowPieces) * kPer, d - kPer);
+    int c = static_cast<int>(threadIdx.x % kRowPieces) * kPer;
+    if constexpr (kHalves == 2) c = (c >= D / 2 ? d : 0) + min(c % (D / 2), d - kPer);
+    else c = min(c, d - kPer);
     const char* from = reinterpret_cast<const char*>(base);
     const uint32_t bytes = row * static_cast<uint32_t>(sizeof(T));   // below 2^24
 #pragma unroll
@@ -352,13 +357,13 @@ struct Tile {
     auto at = [&](int i) {
       return reinterpret_cast<uint4*>(lds + tile_at<T, D>(r + i * kRowsApart, c));
     };
-    if (n == C && d == D) {
+    if (n == C && d == D / kHalves) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) *at(i) = v[i];
     } else {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const bool in = r + i * kRowsApart < n && c < d;
+        const bool in = r + i * kRowsApart < n && c % (D / kHalves) < d;
         *at(i) = in ? v[i] : make_uint4(0u, 0u, 0u, 0u);
       }
     }
@@ -417,6 +422,23 @@ __device__ __forceinline__ void decays(Decay<C>& d, float g, float scale, int la
   }
 }
 
+// Inclusive sums over the wavefront, by the same steps as the decays'.
+__device__ __forceinline__ float scan_f32(float v) {
+#define MSSM_LA_SCAN(CTRL, ROWS) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+  MSSM_LA_SCAN(0x111, 0xF)
+  MSSM_LA_SCAN(0x112, 0xF)
+  MSSM_LA_SCAN(0x114, 0xF)
+  MSSM_LA_SCAN(0x118, 0xF)
+  MSSM_LA_SCAN(0x142, 0xA)
+  MSSM_LA_SCAN(0x143, 0xC)
+#undef MSSM_LA_SCAN
+  return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
 // Sum over the 16 lanes of a row, in every one of them (rotations by 8, 4, 2, 1).
 __device__ __forceinline__ float row16_sum(float v) {
 #define MSSM_LA_ROT(CTRL) \
@@ -437,11 +459,13 @@ __device__ __forceinline__ float wave_sum(float v) {
 // ---- the pass ----------------------------------------------------------------------------------------
 
 // V: the type the output is stored in.
+// kHeads 2: two heads that share x and y in one block, two wavefronts for each;
+// the products of x and y, and their tiles, then serve both.
 // kOut false: only the state over the segment (no x, no output).
 // kDot 0: nothing more.  1 (dq): also W and q . dqc, as one sum u for each
 // token, and the state before some of the chunks.  2 (dk): also k . dkc, and dg
 // from it, u and those states.
-template <typename T, int C, int DA, int NT, bool kOut, int kDot>
+template <typename T, int C, int DA, int NT, int kHeads, bool kOut, int kDot>
 struct Lds {
   static constexpr int TB = 64 * NT;                        // columns of z
   static constexpr int PP = C + 16 / sizeof(T);             // row pitch of p
@@ -449,8 +473,8 @@ struct Lds {
   T y[C * DA];
   T z[C * TB];
   T e[kDot == 1 ? C * TB : 8];
-  T p[kOut ? C * PP : 8];
-  Decay<C> d[2];
+  T p[kOut ? kHeads * C * PP : 8];
+  Decay<C> d[2][kHeads];
   float dot[kDot ? 4 : 1][C];
   float rows[kDot == 1 ? 2 : 1][C];
   float cols[kDot == 1 ? 4 : 1][C];
@@ -463,20 +487,23 @@ struct Lds {
 template <int C>
 constexpr int kStride = 256 / C;
 
-template <typename T, typename V, int C, int DA, int NT, bool kRev, bool kOut, int kDot>
+template <typename T, typename V, int C, int DA, int NT, int kHeads, bool kRev, bool kOut, int kDot>
 __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kStateParts = kBf16 && kDot != 0 ? 3 : 1;  // of the state as an operand
   constexpr int NR = C / 16, NK = C / 32, NM = DA / 16, TB = 64 * NT;
-  constexpr int PP = Lds<T, C, DA, NT, kOut, kDot>::PP;
-  __shared__ __align__(16) Lds<T, C, DA, NT, kOut, kDot> m;
+  constexpr int PP = Lds<T, C, DA, NT, kHeads, kOut, kDot>::PP;
+  __shared__ __align__(16) Lds<T, C, DA, NT, kHeads, kOut, kDot> m;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
 
+  static_assert(kHeads == 1 || (NT == 2 && kDot == 0), "two heads of up to 64 columns");
   const uint32_t block = logical_block();
-  const int64_t slot = block / p.heads;
-  const int h = block % p.heads;
+  const uint32_t groups = static_cast<uint32_t>(p.heads) / kHeads;
+  const int64_t slot = block / groups;
+  const int h = static_cast<int>(block % groups) * kHeads;
+  const int hw = kHeads == 2 ? wave >> 1 : 0;              // this wavefront's head is h + hw
   const Place at = place_of(p.grid, slot);
   if (!at.ok) {
     if constexpr (kDot == 2) {
@@ -492,10 +519,11 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   // both are the eight consecutive columns 8 g4 + 4 t + r (16-byte stores)
   constexpr int kStep = NT == 2 ? 8 : 4;
   const int c_wave = 16 * NT * wave;
-  auto col_of = [&](int t, int c) { return c_wave + kStep * (c >> 2) + 4 * t + (c & 3); };
+  const int c_head = c_wave - 64 * hw;                     // of its head's columns
+  auto col_of = [&](int t, int c) { return c_head + kStep * (c >> 2) + 4 * t + (c & 3); };
 
-  const int64_t sh = (at.seq * p.heads + h) * (int64_t(p.dA) * p.dB);        // per sequence
-  const int64_t wh = (slot * p.heads + h) * (int64_t(p.dA) * p.dB);          // per segment
+  const int64_t sh = (at.seq * p.heads + h + hw) * (int64_t(p.dA) * p.dB);        // per sequence
+  const int64_t wh = (slot * p.heads + h + hw) * (int64_t(p.dA) * p.dB);          // per segment
 
   // the state: rows 16 mt + 4 g4 + r of dA, column col_of(t, l16)
   auto row_of = [&](int mt, int r) { return 16 * mt + 4 * g4 + r; };
@@ -526,7 +554,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   // worked on.
   struct Stage {
     Tile<T, C, DA> x, y;
-    Tile<T, C, TB> z, e;
+    Tile<T, C, TB, kHeads> z;
+    Tile<T, C, TB> e;
   };
   constexpr int kStage = (kOut ? Tile<T, C, DA>::kPieces : 0) * 4 + Tile<T, C, DA>::kPieces * 4 +
                          Tile<T, C, TB>::kPieces * 4 * (kDot == 1 ? 2 : 1);
@@ -545,7 +574,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   const T* Y = begin(p.y, p.dA);
   const T* Z = begin(p.z, p.dB);
   const T* E = kDot == 1 ? begin(p.e, p.dB) : nullptr;
-  const float* G = p.g + (p.g_row ? first * p.g_row : 0) + h;
+  // (the wavefronts that make the decays load them: one for each head)
+  const float* G = p.g + (p.g_row ? first * p.g_row : 0) + h + (kHeads == 2 ? wave & 1 : 0);
   constexpr int kAhead = kRev ? -C : C;                     // tokens from chunk to chunk
   const uint32_t x_row = static_cast<uint32_t>(p.x.row), y_row = static_cast<uint32_t>(p.y.row);
   const uint32_t z_row = static_cast<uint32_t>(p.z.row), e_row = static_cast<uint32_t>(p.e.row);
@@ -580,13 +610,13 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
 
   constexpr int kDumpSize = DA * TB;
-  float edge = 0.0f, head_sum = 0.0f;      // of wavefront 0
+  float edge = 0.0f, head_sum = 0.0f;      // dg's are wavefront 0's
   float g_next = 0.0f;                     // log decays of the next chunk
 
   auto step = [&](int it, Stage& f) __attribute__((always_inline)) {
     const int ck = kRev ? chunks - 1 - it : it;
     const int n = tokens_of(it);
-    const Decay<C>& d = m.d[it & 1];
+    const Decay<C>& d = m.d[it & 1][hw];
     if constexpr (kOut) f.x.stash(m.x, n, p.dA);
     f.y.stash(m.y, n, p.dA);
     f.z.stash(m.z, n, p.dB);
@@ -635,7 +665,6 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       constexpr int kWaveTiles = NR == 4 ? 4 : 1;
       const int rt = NR == 4 ? wave : wave >> 1;
       const int i = 16 * rt + l16;
-      const float gi = d.hi[i], gil = d.lo[i];
       float row_sum = 0.0f;
       // All of a row tile's products are formed, also those that the mask then
       // drops: without branches between them the loads and products of one hide
@@ -668,49 +697,55 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         }
       }
 #pragma unroll
-      for (int u = 0; u < kWaveTiles; ++u) {
-        const int ct = NR == 4 ? u : wave & 1;
-        const bool live = kRev ? ct >= rt : ct <= rt;
-        const int j0 = 16 * ct + 4 * g4;
-        if (live) {
-          f32x4 a = as[u], b = bs[kDot == 1 ? u : 0];
-          if (ct == rt) {
-            const f32x4 gj = *reinterpret_cast<const f32x4*>(&d.hi[j0]);
-            const f32x4 gjl = *reinterpret_cast<const f32x4*>(&d.lo[j0]);
+      for (int hh = 0; hh < kHeads; ++hh) {
+        const Decay<C>& dh = m.d[it & 1][hh];
+        T* const ph = m.p + hh * C * PP;
+        const float gi = dh.hi[i], gil = dh.lo[i];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const bool in = kRev ? j0 + r >= i : j0 + r <= i;
-              const float diff = (gi - gj[r]) + (gil - gjl[r]);
-              a[r] = in ? a[r] * (scale * fast_exp2(kRev ? -diff : diff)) : 0.0f;
-              if constexpr (kDot == 1) b[r] = j0 + r != i ? a[r] * b[r] : 0.0f;
+        for (int u = 0; u < kWaveTiles; ++u) {
+          const int ct = NR == 4 ? u : wave & 1;
+          const bool live = kRev ? ct >= rt : ct <= rt;
+          const int j0 = 16 * ct + 4 * g4;
+          if (live) {
+            f32x4 a = as[u], b = bs[kDot == 1 ? u : 0];
+            if (ct == rt) {
+              const f32x4 gj = *reinterpret_cast<const f32x4*>(&dh.hi[j0]);
+              const f32x4 gjl = *reinterpret_cast<const f32x4*>(&dh.lo[j0]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const bool in = kRev ? j0 + r >= i : j0 + r <= i;
+                const float diff = (gi - gj[r]) + (gil - gjl[r]);
+                a[r] = in ? a[r] * (scale * fast_exp2(kRev ? -diff : diff)) : 0.0f;
+                if constexpr (kDot == 1) b[r] = j0 + r != i ? a[r] * b[r] : 0.0f;
+              }
+            } else {
+              // through the boundary between the 16 tokens and what is nearer to i
+              const int edge16 = kRev ? 16 * ct - 1 : 16 * ct + 15;
+              const float diff = (gi - dh.hi[edge16]) + (gil - dh.lo[edge16]);
+              const float fi = scale * fast_exp2(kRev ? -diff : diff);
+              const f32x4 fj = *reinterpret_cast<const f32x4*>(&dh.fac[j0]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                a[r] *= fi * fj[r];
+                if constexpr (kDot == 1) b[r] *= a[r];
+              }
             }
-          } else {
-            // through the boundary between the 16 tokens and what is nearer to i
-            const int edge16 = kRev ? 16 * ct - 1 : 16 * ct + 15;
-            const float diff = (gi - d.hi[edge16]) + (gil - d.lo[edge16]);
-            const float fi = scale * fast_exp2(kRev ? -diff : diff);
-            const f32x4 fj = *reinterpret_cast<const f32x4*>(&d.fac[j0]);
+            lds_store4(ph + i * PP + j0, a);
+            if constexpr (kDot == 1) {
+              row_sum += (b[0] + b[1]) + (b[2] + b[3]);
+              // sums over this wavefront's 16 rows i, for each of the four j
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              a[r] *= fi * fj[r];
-              if constexpr (kDot == 1) b[r] *= a[r];
+              for (int r = 0; r < 4; ++r) b[r] = row16_sum(b[r]);
+              if (l16 == 0) *reinterpret_cast<f32x4*>(&m.cols[rt][j0]) = b;
             }
+          } else if ((ct ^ rt) == 1) {
+            lds_store4(ph + i * PP + j0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});   // read with its neighbour
           }
-          lds_store4(m.p + i * PP + j0, a);
-          if constexpr (kDot == 1) {
-            row_sum += (b[0] + b[1]) + (b[2] + b[3]);
-            // sums over this wavefront's 16 rows i, for each of the four j
-#pragma unroll
-            for (int r = 0; r < 4; ++r) b[r] = row16_sum(b[r]);
-            if (l16 == 0) *reinterpret_cast<f32x4*>(&m.cols[rt][j0]) = b;
-          }
-        } else if ((ct ^ rt) == 1) {
-          lds_store4(m.p + i * PP + j0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});   // read with its neighbour
         }
       }
-      // the wavefront with the fewest scores prepares the next chunk's decays
-      if (wave == (kRev ? 3 : 0) && it + 1 < chunks)
-        decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
+      // the wavefronts with the fewest scores prepare the next chunk's decays
+      if ((kRev ? wave > 3 - kHeads : wave < kHeads) && it + 1 < chunks)
+        decays<C, kRev>(m.d[(it + 1) & 1][wave & (kHeads - 1)], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
       if constexpr (kDot == 1) {
         row_sum += __shfl_xor(row_sum, 16, 64);
         row_sum += __shfl_xor(row_sum, 32, 64);
@@ -799,7 +834,7 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (kRev ? k < r / 2 : k > r / 2) continue;
-          const Frag<T> pf = frag_at(m.p + (16 * r + l16) * PP + 32 * k + 4 * g4);
+          const Frag<T> pf = frag_at(m.p + (hw * C + 16 * r + l16) * PP + 32 * k + 4 * g4);
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
         }
@@ -807,11 +842,11 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       // columns past it are dropped by the hardware, so no branch stands around them.
       // (Buffer accesses, too, take any alignment.)
       {
-        const buf_t to = make_buf(out, ((n - 1) * o_row + p.dB) * static_cast<uint32_t>(sizeof(V)));
+        const buf_t to = make_buf(out, ((n - 1) * o_row + kHeads * p.dB) * static_cast<uint32_t>(sizeof(V)));
         const uint32_t c = col_of(0, 4 * g4);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const uint32_t off = c < static_cast<uint32_t>(p.dB) ? (16 * r + l16) * o_row + c : 0x3ffffff0u;
+          const uint32_t off = c < static_cast<uint32_t>(p.dB) ? (16 * r + l16) * o_row + hw * p.dB + c : 0x3ffffff0u;
           buf_store<V, NT>(to, off * static_cast<uint32_t>(sizeof(V)), acc[r]);
         }
       }
@@ -835,18 +870,13 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
           const bool in = lane < n;
           const int t = min(lane, C - 1);
           const float kd = in ? (m.dot[0][t] + m.dot[1][t]) + (m.dot[2][t] + m.dot[3][t]) : 0.0f;
-          float before = kd, after = in ? uv : 0.0f;     // inclusive sums up to, and from, this token
-#pragma unroll
-          for (int o = 1; o < 64; o <<= 1) {
-            const float a = __shfl_up(before, o, 64), b = __shfl_down(after, o, 64);
-            if (lane >= o) before += a;
-            if (lane + o < 64) after += b;
-          }
+          const float u = in ? uv : 0.0f;
+          const float before = scan_f32(kd), u_before = scan_f32(u);     // up to this token
+          const float after = u + (lane_value(u_before, 63) - u_before); // from it on
           // what passes through the whole chunk
           const float through = dump ? d.all * ((m.edge[0] + m.edge[1]) + (m.edge[2] + m.edge[3]))
-                                     : edge - __shfl(before, 63, 64);
-          const float prior = __shfl_up(before, 1, 64);
-          const float dg = after + (lane > 0 ? prior : 0.0f) + through;
+                                     : edge - lane_value(before, 63);
+          const float dg = after + (before - kd) + through;
           edge = through + qs;
           if (in) {
             if (p.dg) dg_at[static_cast<uint32_t>(lane * p.heads)] = dg;
@@ -918,10 +948,10 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       }
     }
     if constexpr (!kOut) {
-      if (tid == 0) head_sum += d.hi[C - 1];     // the segment's log decay
+      head_sum += d.hi[C - 1];                   // the segment's log decay
     }
-    if (!kOut && wave == 0 && it + 1 < chunks)
-      decays<C, kRev>(m.d[(it + 1) & 1], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
+    if (!kOut && wave < kHeads && it + 1 < chunks)
+      decays<C, kRev>(m.d[(it + 1) & 1][wave & (kHeads - 1)], lane < tokens_of(it + 1) ? g_next : 0.0f, scale, lane);
     g_next = g_after;
     block_sync();
   };
@@ -945,7 +975,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       fetch(sets[1], min(1, chunks - 1));
       no_stores(1);
     }
-    if (wave == 0) decays<C, kRev>(m.d[0], lane < tokens_of(0) ? g_first : 0.0f, scale, lane);
+    if (wave < kHeads)
+      decays<C, kRev>(m.d[0][wave & (kHeads - 1)], lane < tokens_of(0) ? g_first : 0.0f, scale, lane);
   }
   int it = 0;
   if constexpr (kSets == 2) {
@@ -969,7 +1000,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
     if (last_seg && p.last) dst = p.last + sh;
   } else {
     dst = p.seg_out + wh;
-    if (tid == 0) p.seg_decay[slot * p.heads + h] = fast_exp2(head_sum);
+    if (lane == 0 && wave % (4 / kHeads) == 0)
+      p.seg_decay[slot * p.heads + h + hw] = fast_exp2(head_sum);
   }
   if (!dst) return;
 #pragma unroll

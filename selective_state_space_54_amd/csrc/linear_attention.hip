@@ -226,15 +226,24 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   // Blocks to aim for: two on each of the 256 compute units at once, once
   // (backward) or twice over; a few blocks more than a multiple of 512 would be a
   // round of their own (1 x 131072, 20 heads of 128: 972 us with 500 or 1000
-  // blocks, 1125 with 1040).  Segments of at least two chunks: below that the
-  // states' traffic is more than the tiles' (4 x 2048, 16 heads of 128: 82 us with
-  // 512 blocks, 89 with 256).  From 256 sequences times heads on, one segment.
+  // blocks, 1125 with 1040).  A segment costs its state four times through memory,
+  // as much as the tiles of max(dk, dv) or so tokens: below twice that only to
+  // reach 256 blocks, and never below two chunks (4 x 2048, 16 heads of 128: 82 us
+  // in segments of 256 tokens, 89 of 512, 107 of 128; 3 x 333 float32 backward, 6
+  // heads: 81 us in segments of 64, 121 of 128).  From 256 sequences times heads
+  // on, one segment each.
   const int64_t chunk = bf16 ? 64 : 32, target = backward ? 512 : 1024;
-  const int64_t rows = s.seqs * s.heads;
+  p.paired = s.dv <= 64 && s.heads / s.key_heads % 2 == 0;
+  const int64_t units = p.paired && !backward ? s.heads / 2 : s.heads;
+  const int64_t rows = s.seqs * units;
   const int64_t len = s.packed ? s.tokens : g.L;      // the longest a sequence can be
-  int64_t seg = len;
-  if (s.packed) seg = (s.tokens * s.heads + 2 * target - 1) / (2 * target);
-  else if (rows < 256) seg = (len + target / rows - 1) / (target / rows);
+  auto cut = [&](int64_t blocks) {                    // tokens of a segment for so many blocks
+    if (s.packed) return (s.tokens * units + blocks - 1) / blocks;
+    return rows >= 256 ? len : (len + blocks / rows - 1) / (blocks / rows);
+  };
+  const int64_t least = 2 * (s.dk > s.dv ? s.dk : s.dv);
+  int64_t seg = cut(target);
+  if (seg < least) seg = cut(256) < least ? cut(256) : least;
   if (seg < 2 * chunk) seg = 2 * chunk;
   if (seg > len) seg = len;
   seg = (seg + chunk - 1) / chunk * chunk;
@@ -295,6 +304,7 @@ hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStrea
   p.dA = static_cast<int>(s.dk);
   p.dB = static_cast<int>(s.dv);
   p.scale = a.scale;
+  p.paired = plan.paired;
   p.sA = s.dv;
   p.sB = 1;
   hipError_t err;
@@ -339,6 +349,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.y = k, p.z = v;
     p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
     p.sA = s.dv, p.sB = 1;
+    p.paired = plan.paired;
     p.seg_out = at(plan.states);
     p.seg_decay = at(plan.decay);
     if ((err = la::pass_state(a.dtype, p, stream)) != hipSuccess) return err;
@@ -389,6 +400,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.sA = s.dv, p.sB = 1;
     p.init = d.dlast;
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
+    p.paired = plan.paired;
     p.last = d.dstate;
     p.out = d.dv;
     if ((err = la::pass_dv(a.dtype, p, stream)) != hipSuccess) return err;

@@ -442,6 +442,7 @@ struct LaGrads {
 struct LaPlan {
   la::Grid grid;
   bool cut = false;
+  bool paired = false;            // heads that share keys, two a block
   size_t states = 0, decay = 0, rev_states = 0, rev_decay = 0, u = 0, q_sums = 0, dumps = 0;
   size_t head_part = 0, dq = 0, dk = 0;
   int64_t chunks_per_slot = 0, dumps_per_slot = 0;
