@@ -31,6 +31,9 @@ Modules:
     block      -- the Mamba block around the scan: causal depthwise conv1d,
                   SiLU, projections, gate (eq. (9))
     backward   -- gradients of the scan (adjoint recurrence, float64)
+    linear_attention -- the matrix-state recurrence with a decay for each head
+                  and its gradients
+    layer_norm -- layer norm and its gradients
 Parity status of each function is stated in its docstring; every function is
 pinned by a ``-m "not gpu"`` test unless it says "parity unpinned".
 """
@@ -39,3 +42,5 @@ from .selection import softplus, silu, selective_ssm_fused, round_to_bf16  # noq
 from . import forms  # noqa: F401
 from . import block  # noqa: F401
 from . import backward  # noqa: F401
+from . import linear_attention  # noqa: F401
+from . import layer_norm  # noqa: F401

@@ -49,7 +49,10 @@
 //
 // Rounding.  Products of bfloat16 inputs accumulate in float32.  The decayed
 // scores and the state are rounded to bfloat16 where they are operands of the
-// output's products (the output is rounded to bfloat16 itself); where float32
+// output's products (the output is rounded to bfloat16 itself), except the
+// scores of the 16 x 16 tiles on the diagonal, which keep 16 bits: where decays
+// are strong, or a sequence begins, a token's output is little more than its own
+// term, and that rounding would not average out.  Where float32
 // results depend on them (the state's own update, dg) the operand is split in
 // three bfloat16 parts, 24 bits.  Decays, their sums (float64 inside a chunk,
 // kept as a float32 pair) and the state are 32 bits or more.
@@ -246,6 +249,21 @@ __device__ __forceinline__ void lds_store4(uint16_t* p, f32x4 v) {
 }
 __device__ __forceinline__ void lds_store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 
+// What rounding to bfloat16 leaves of four values, itself rounded.
+__device__ __forceinline__ void lds_store4_rest(uint16_t* p, f32x4 v) {
+  uint32_t u0 = pack2(v[0], v[1]), u1 = pack2(v[2], v[3]);
+  asm("" : "+v"(u0), "+v"(u1));
+  *reinterpret_cast<uint2*>(p) = uint2{pack2(v[0] - low_half(u0), v[1] - high_half(u0)),
+                                       pack2(v[2] - low_half(u1), v[3] - high_half(u1))};
+}
+// A fragment with 16 terms in half h and none in the other.  (Products of 16 terms,
+// v_mfma_f32_16x16x16_bf16, would do half the work, but where one followed a product
+// of 32 into the same registers its results were wrong now and then.)
+__device__ __forceinline__ Frag<uint16_t> half_frag(uint2 u, int h) {
+  const uint2 none = make_uint2(0, 0);
+  return h ? frag_of(none, u) : frag_of(u, none);
+}
+
 // NT consecutive fours at byte offset `off`, rounded to V, as 8- or 16-byte stores.
 template <typename V, int NT>
 __device__ __forceinline__ void buf_store(buf_t to, uint32_t off, const f32x4 (&v)[NT]) {
@@ -422,8 +440,16 @@ __device__ __forceinline__ void decays(Decay<C>& d, float g, float scale, int la
   }
 }
 
+// Two wait states before a value is read through DPP, wherever a branch may have
+// led here from (inside a block the compiler sees to them).
+__device__ __forceinline__ float before_dpp(float v) {
+  asm volatile("s_nop 1" : "+v"(v));
+  return v;
+}
+
 // Inclusive sums over the wavefront, by the same steps as the decays'.
 __device__ __forceinline__ float scan_f32(float v) {
+  v = before_dpp(v);
 #define MSSM_LA_SCAN(CTRL, ROWS) \
   v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
   MSSM_LA_SCAN(0x111, 0xF)
@@ -441,6 +467,7 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 
 // Sum over the 16 lanes of a row, in every one of them (rotations by 8, 4, 2, 1).
 __device__ __forceinline__ float row16_sum(float v) {
+  v = before_dpp(v);
 #define MSSM_LA_ROT(CTRL) \
   v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
   MSSM_LA_ROT(0x128)
@@ -610,6 +637,11 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
   float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
 
   constexpr int kDumpSize = DA * TB;
+  // The second parts of the diagonal's scores lie in tiles of p that no product reads:
+  // (0 and 1, 2 and 3), in reverse (2 and 3, 0 and 1).
+  auto rest_at = [&](int rt) {
+    return (16 * ((kRev ? 2 : 0) + (rt & 1)) + l16) * PP + 16 * ((kRev ? 0 : 2) + (rt >> 1)) + 4 * g4;
+  };
   float edge = 0.0f, head_sum = 0.0f;      // dg's are wavefront 0's
   float g_next = 0.0f;                     // log decays of the next chunk
 
@@ -731,6 +763,9 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
               }
             }
             lds_store4(ph + i * PP + j0, a);
+            if constexpr (kBf16) {
+              if (ct == rt) lds_store4_rest(ph + rest_at(rt), a);
+            }
             if constexpr (kDot == 1) {
               row_sum += (b[0] + b[1]) + (b[2] + b[3]);
               // sums over this wavefront's 16 rows i, for each of the four j
@@ -838,6 +873,15 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
         }
+      if constexpr (kBf16) {
+        static_assert(NR == 4, "tiles for the diagonal's second parts");
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const Frag<T> rest = half_frag(lds_read8(m.p + hw * C * PP + rest_at(r)), r & 1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[r / 2][t], rest);
+        }
+      }
       // Stores through a descriptor that ends with the chunk's last value: rows and
       // columns past it are dropped by the hardware, so no branch stands around them.
       // (Buffer accesses, too, take any alignment.)

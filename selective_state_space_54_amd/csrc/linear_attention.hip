@@ -154,7 +154,7 @@ struct StepLaunch {
 template <typename T>
 __global__ __launch_bounds__(256) void la_step(StepLaunch p) {
   using la::f32x4;
-  __shared__ float red[64 * 16 * 4];                   // rows in flight * dv <= 1024 values
+  __shared__ float red[1024];                          // rows in flight * dv values
   __shared__ float sk[128], sq[128];
   const int64_t b = blockIdx.x / p.heads;
   const int h = blockIdx.x % p.heads;
