@@ -492,3 +492,49 @@ def test_refusals():
         mssm.mssm_linear_attention_fwd(long, long, long, z(1, 4000, 1, dt=torch.float32),
                                        torch.empty_like(long), None, scale=1.0)
     torch.cuda.synchronize()
+
+
+def _long_case(seed, L, H, kinds):
+    """One sequence of dk = dv = 16 whose heads have the given log decays."""
+    c = make(seed, [L], H, H, 16, 16, "fp32")
+    c["log_decay"] = torch.stack([torch.from_numpy(k).float() for k in kinds], -1)[None]
+    return c
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["prompt", "gradient"])
+def test_tokens_out_of_reach_of_a_segments_state(backward):
+    """Segments long enough that the state pass looks for the tokens that can reach a
+    segment's state at all: memories of a few tokens, of about half a segment, longer than
+    a segment and endless; resets at, before and after a segment's ends; log decays above
+    zero before the state all but vanishes (the tokens before them count no more)."""
+    L, H = 17000, 32
+    seg = 544                                        # tokens a segment, by the size query's rule
+    rng = np.random.default_rng(60)
+    t = np.arange(L)
+    pulse = np.where(t % seg == 400, 60.0, np.where(t % seg == 401, -300.0, -0.01))
+    kinds = [np.full(L, -3.0), np.full(L, -0.5), np.full(L, -0.05), np.full(L, -1e-4),
+             np.where(t % seg == seg - 1, -np.inf, -0.02), np.where(t % seg == 0, -np.inf, -0.02),
+             np.where(t % seg == 1, -1e30, -0.02), np.where(t % 700 == 0, -250.0, -0.002), pulse,
+             -rng.exponential(0.4, L)] + [np.full(L, -0.3)] * (H - 10)
+    c = _long_case(61, L, H, kinds)
+    q, k, v, g, dout, state, dlast = on_gpu(c, "q", "k", "v", "log_decay", "dout", "state", "dlast")
+    heads = range(10)
+    part = lambda a, ax: np.take(a, heads, axis=ax)
+    Q, K, V, G, _ = oracle_inputs(c)
+    args = (part(Q, 1), part(K, 1), part(V, 1), part(G, 1), c["offsets"])
+    s0 = part(host64(c["state"]), 1)
+    if not backward:
+        o, last = mssm.linear_attention(q, k, v, g, scale=0.25, state=state, return_state=True)
+        torch.cuda.synchronize()
+        want_o, want_s = la.linear_attention(*args, scale=0.25, state=s0)
+        check("o", part(host64(o)[0], 1), want_o, "fp32")
+        check("last state", part(host64(last), 1), want_s, "fp32", 1)
+        return
+    got = mssm.linear_attention_bwd(q, k, v, g, dout, scale=0.25, state=state, dstate=dlast)
+    torch.cuda.synchronize()
+    want = la.linear_attention_backward(*args, part(host64(c["dout"])[0], 1), scale=0.25, state=s0,
+                                        dlast=part(host64(c["dlast"]), 1))
+    for n in ("dq", "dk", "dv"):
+        check(n, part(host64(got[n])[0], 1), want[n], "fp32")
+    check("dlog_decay", part(host64(got["dlog_decay"])[0], 1), want["dlog_decay"], "decay", -1)
+    check("dstate", part(host64(got["dstate"]), 1), want["dstate"], "fp32", 1)
