@@ -46,7 +46,7 @@ struct PassArgs {
   bool out_f32 = false;              // dq, dk: float32 instead
   // gradient of the log decays: written by dq, read by dk
   float* u = nullptr;                // [tokens, heads]
-  float* q_sums = nullptr;           // [slots, chunks_per_slot, heads]
+  float* q_sums = nullptr;           // [slots, chunks_per_slot, heads, 4]: a wavefront's part each
   float* dumps = nullptr;            // [slots, dumps_per_slot, heads, ..]: states as dq holds them
   int64_t chunks_per_slot = 0, dumps_per_slot = 0;
   // written by dk

@@ -742,6 +742,16 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         dump = p.dumps + ((slot * p.dumps_per_slot + (chunks - 1 - ck) / kStride<C>) * p.heads + h) *
                              int64_t(kDumpSize) + tid * 4;
     }
+    // (dk: the first half of the state that dq left there, loaded before the products
+    // that stand between, into the registers of the tiles now in LDS)
+    constexpr int kHalf = kDot == 2 ? NM * NT / 2 : 1;
+    f32x4 left[kHalf];
+    if constexpr (kDot == 2) {
+      if (dump) {
+#pragma unroll
+        for (int u = 0; u < kHalf; ++u) left[u] = *reinterpret_cast<const f32x4*>(dump + u * (kThreads * 4));
+      }
+    }
     if constexpr (kDot == 1) {
       if (dump) {
 #pragma unroll
@@ -766,7 +776,8 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
           for (int q = 0; q < 4; ++q) ev[r][t][q] = to_float(raw[q]);
         }
       uv = u_at[static_cast<uint32_t>(min(lane, n - 1) * p.heads)];
-      qs = p.q_sums[(slot * p.chunks_per_slot + ck) * p.heads + h];
+      const f32x4 q = *reinterpret_cast<const f32x4*>(p.q_sums + ((slot * p.chunks_per_slot + ck) * p.heads + h) * 4);
+      qs = (q[0] + q[1]) + (q[2] + q[3]);
     }
 
     f32x4 acc[NR][NT];
@@ -917,15 +928,17 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
       }
       if constexpr (kDot == 2) {
         if (dump) {
+          f32x4 right[kHalf];
+#pragma unroll
+          for (int u = 0; u < kHalf; ++u)
+            right[u] = *reinterpret_cast<const f32x4*>(dump + (kHalf + u) * (kThreads * 4));
           float part = 0.0f;
 #pragma unroll
-          for (int mt = 0; mt < NM; ++mt)
+          for (int u = 0; u < NM * NT; ++u) {
+            const f32x4 q = u < kHalf ? left[u % kHalf] : right[u % kHalf];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const f32x4 q = *reinterpret_cast<const f32x4*>(dump + (mt * NT + t) * (kThreads * 4));
-#pragma unroll
-              for (int r = 0; r < 4; ++r) part = __builtin_fmaf(q[r], s[mt][t][r], part);
-            }
+            for (int r = 0; r < 4; ++r) part = __builtin_fmaf(q[r], s[u / NT][u % NT][r], part);
+          }
           part = wave_sum(part);
           if (lane == 0) m.edge[wave] = part;
         }
@@ -974,19 +987,25 @@ __global__ __launch_bounds__(kThreads, 2) void la_pass(PassArgs p) {
         }
       }
       if constexpr (kDot == 1) {
-        if (wave == 0) {
-          const int t = min(lane, C - 1), tt = t >> 4;
-          const float qd = (m.dot[0][t] + m.dot[1][t]) + (m.dot[2][t] + m.dot[3][t]);
-          float rows = m.rows[0][t], cols = 0.0f;
-          if (NR == 2 && tt == 1) rows += m.rows[1][t];
-#pragma unroll
-          for (int q = 0; q < NR; ++q)          // row tiles from this one on
-            if (q >= tt) cols += m.cols[q][t];
-          const bool in = lane < n;
-          if (in) u_at[static_cast<uint32_t>(lane * p.heads)] = qd + (rows - cols);
-          const float sum = wave_sum(in ? qd : 0.0f);
-          if (lane == 0) p.q_sums[(slot * p.chunks_per_slot + ck) * p.heads + h] = sum;
-        }
+        // Each wavefront finishes 16 tokens, lane group g4 with its part of the sums,
+        // and without branches, beside the products.
+        const int w = NR == 4 ? wave : wave & 1, i2 = 16 * w + l16;
+        float qd = m.dot[g4][i2];
+        const float rows = m.rows[NR == 4 ? 0 : g4 & 1][i2], cols = m.cols[NR == 4 ? g4 : g4 & 1][i2];
+        float u = (g4 < (NR == 4 ? 1 : w + 1) ? rows : 0.0f) - (g4 >= w && g4 < NR ? cols : 0.0f);
+        qd += __shfl_xor(qd, 16, 64);
+        u += __shfl_xor(u, 16, 64);
+        qd += __shfl_xor(qd, 32, 64);
+        u += __shfl_xor(u, 32, 64);
+        const bool mine = wave < NR;
+        const uint32_t heads = static_cast<uint32_t>(p.heads);
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __float_as_uint(qd + u), make_buf(u_at, ((n - 1) * heads + 1) * 4),
+            g4 == 0 && mine ? static_cast<int>(i2 * heads * 4) : 0x3ffffff0, 0, 0);
+        const float sum = row16_sum(mine && i2 < n ? qd : 0.0f);
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __float_as_uint(sum), make_buf(p.q_sums + ((slot * p.chunks_per_slot + ck) * p.heads + h) * 4, 16),
+            lane == 0 ? wave * 4 : 0x3ffffff0, 0, 0);
       }
       if constexpr (kDot == 2) {
         if (wave == 0) {

@@ -280,7 +280,7 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
     p.dumps_per_slot = (p.chunks_per_slot + every - 1) / every;
     const size_t held = static_cast<size_t>(s.dk <= 64 ? 64 : 128) * (s.dv <= 64 ? 64 : 128) * 4;
     p.dumps = take(held * s.heads * p.dumps_per_slot * g.slots);
-    p.q_sums = take(static_cast<size_t>(p.chunks_per_slot) * g.slots * s.heads * 4);
+    p.q_sums = take(static_cast<size_t>(p.chunks_per_slot) * g.slots * s.heads * 16);
     p.u = take(static_cast<size_t>(s.tokens) * s.heads * 4);
     p.head_part = take(per_slot);
     if (s.heads != s.key_heads) {
