@@ -55,7 +55,8 @@ mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm_dtype dtype,
   *plan = mssm::plan_la(s, backward, dtype == MSSM_BFLOAT16);
   int64_t n;
   if (!product({plan->grid.slots, s.heads, 128 * 128, 4 * 4, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
-  if (!product({plan->grid.slots, s.heads}, &n) || n > kMaxBlocks) return MSSM_ERROR_NOT_SUPPORTED;
+  if (!product({plan->grid.slots, s.heads}, &n) || n > kMaxBlocks / (backward ? 2 : 1))
+    return MSSM_ERROR_NOT_SUPPORTED;
   if (backward && s.heads != s.key_heads &&
       (!product({s.tokens, s.key_heads, s.dk}, &n) || n / 1024 > kMaxBlocks - 1))
     return MSSM_ERROR_NOT_SUPPORTED;

@@ -1,0 +1,11 @@
+// Linear attention, float32: dq with the queries' part of dg, and dv.
+#include "la_pass_launch.h"
+#include "linear_attention.h"
+
+namespace mssm {
+namespace la {
+hipError_t pass_dq_dv_fp32(const PassArgs& dq, const PassArgs& dv, hipStream_t stream) {
+  return launch_dq_dv<float, float>(dq, dv, stream);
+}
+}  // namespace la
+}  // namespace mssm

@@ -38,5 +38,46 @@ hipError_t launch_pass(const PassArgs& p, hipStream_t stream) {
   return launch_pass_to<T, T, kRev, kOut, kDot>(p, stream);
 }
 
+template <typename T, int DA, int NT, int kHeads>
+hipError_t launch_states_as(const PassArgs& fwd, const PassArgs& rev, hipStream_t stream) {
+  const int64_t blocks = fwd.grid.slots * (fwd.heads / kHeads);
+  hipLaunchKernelGGL((la_states<T, sizeof(T) == 2 ? 64 : 32, DA, NT, kHeads>),
+                     dim3(static_cast<uint32_t>(blocks), 2), dim3(kThreads), 0, stream, fwd, rev);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_states(const PassArgs& fwd, const PassArgs& rev, hipStream_t stream) {
+  if (fwd.paired)
+    return fwd.dA <= 64 ? launch_states_as<T, 64, 2, 2>(fwd, rev, stream)
+                        : launch_states_as<T, 128, 2, 2>(fwd, rev, stream);
+  if (fwd.dA <= 64)
+    return fwd.dB <= 64 ? launch_states_as<T, 64, 1, 1>(fwd, rev, stream)
+                        : launch_states_as<T, 64, 2, 1>(fwd, rev, stream);
+  return fwd.dB <= 64 ? launch_states_as<T, 128, 1, 1>(fwd, rev, stream)
+                      : launch_states_as<T, 128, 2, 1>(fwd, rev, stream);
+}
+
+template <typename T, typename V, int DK, int DV, int kHeads>
+hipError_t launch_dq_dv_as(const PassArgs& dq, const PassArgs& dv, hipStream_t stream) {
+  const int64_t n = dq.grid.slots * dq.heads;
+  hipLaunchKernelGGL((la_dq_dv<T, V, sizeof(T) == 2 ? 64 : 32, DK, DV, kHeads>),
+                     dim3(static_cast<uint32_t>(n + n / kHeads)), dim3(kThreads), 0, stream, dq, dv,
+                     static_cast<uint32_t>(n));
+  return hipGetLastError();
+}
+
+template <typename T, typename V>
+hipError_t launch_dq_dv(const PassArgs& dq, const PassArgs& dv, hipStream_t stream) {
+  if (dv.paired)
+    return dv.dA <= 64 ? launch_dq_dv_as<T, V, 64, 64, 2>(dq, dv, stream)
+                       : launch_dq_dv_as<T, V, 128, 64, 2>(dq, dv, stream);
+  if (dv.dA <= 64)
+    return dv.dB <= 64 ? launch_dq_dv_as<T, V, 64, 64, 1>(dq, dv, stream)
+                       : launch_dq_dv_as<T, V, 64, 128, 1>(dq, dv, stream);
+  return dv.dB <= 64 ? launch_dq_dv_as<T, V, 128, 64, 1>(dq, dv, stream)
+                     : launch_dq_dv_as<T, V, 128, 128, 1>(dq, dv, stream);
+}
+
 }  // namespace la
 }  // namespace mssm

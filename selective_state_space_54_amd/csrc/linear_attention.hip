@@ -17,11 +17,15 @@ namespace la {
   }
 MSSM_LA_PASS(fwd)
 MSSM_LA_PASS(state)
-MSSM_LA_PASS(state_rev)
 MSSM_LA_PASS(dq)
 MSSM_LA_PASS(dk)
 MSSM_LA_PASS(dv)
 #undef MSSM_LA_PASS
+hipError_t pass_states_bf16(const PassArgs& fwd, const PassArgs& rev, hipStream_t stream);
+hipError_t pass_states_fp32(const PassArgs& fwd, const PassArgs& rev, hipStream_t stream);
+hipError_t pass_dq_dv_bf16(const PassArgs& dq, const PassArgs& dv, hipStream_t stream);
+hipError_t pass_dq_dv_bf16_f32(const PassArgs& dq, const PassArgs& dv, hipStream_t stream);
+hipError_t pass_dq_dv_fp32(const PassArgs& dq, const PassArgs& dv, hipStream_t stream);
 }  // namespace la
 
 namespace {
@@ -32,16 +36,22 @@ using la::View;
 
 // ---- the state before each segment ---------------------------------------------------------------
 
-// Runs over a sequence's segments in order (kRev: from the last): `st` holds
+// Runs over a sequence's segments in order (rev: from the last): `st` holds
 // each segment's own state on entry and the state the segment starts from on
 // return.  A thread owns four values of one
 // head's state; the segments' loads do not depend on each other and run kAhead
-// ahead of the chain of multiply-adds.
-template <bool kRev>
-__global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t size,
-                                                const float* __restrict__ init,
-                                                const float* __restrict__ decay,
-                                                float* __restrict__ st) {
+// ahead of the chain of multiply-adds.  A gradient's two directions are one launch.
+struct Carry {
+  const float* init;
+  const float* decay;
+  float* st;
+};
+__global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t size, Carry fwd,
+                                                Carry back) {
+  const bool rev = blockIdx.z != 0;
+  const float* __restrict__ init = rev ? back.init : fwd.init;
+  const float* __restrict__ decay = rev ? back.decay : fwd.decay;
+  float* __restrict__ st = rev ? back.st : fwd.st;
   using la::f32x4;
   constexpr int kAhead = 8;
   const int64_t i = 4 * (int64_t(blockIdx.y) * 256 + threadIdx.x);
@@ -71,7 +81,7 @@ __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t si
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int64_t c = c0 + k;
-      const int64_t slot = first + (kRev ? count - 1 - c : c);
+      const int64_t slot = first + (rev ? count - 1 - c : c);
       u[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       e[k] = 1.0f;
       if (c < own) {
@@ -83,7 +93,7 @@ __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t si
     for (int k = 0; k < kAhead; ++k) {
       const int64_t c = c0 + k;
       if (c >= count) break;
-      const int64_t slot = first + (kRev ? count - 1 - c : c);
+      const int64_t slot = first + (rev ? count - 1 - c : c);
       *reinterpret_cast<f32x4*>(st + (slot * heads + h) * size + i) = s;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r] = __builtin_fmaf(e[k], s[r], u[k][r]);
@@ -91,25 +101,24 @@ __global__ __launch_bounds__(256) void la_carry(Grid grid, int heads, int64_t si
   }
 }
 
-hipError_t launch_carry_states(bool rev, const Grid& grid, int heads, int64_t size,
-                               const float* init, const float* decay, float* st,
-                               hipStream_t stream) {
+hipError_t launch_carry(const Grid& grid, int heads, int64_t size, const Carry& fwd,
+                        const Carry* back, hipStream_t stream) {
   const dim3 g(static_cast<uint32_t>(grid.seqs * heads),
-               static_cast<uint32_t>((size / 4 + 255) / 256));
-  if (rev)
-    hipLaunchKernelGGL(la_carry<true>, g, dim3(256), 0, stream, grid, heads, size, init, decay, st);
-  else
-    hipLaunchKernelGGL(la_carry<false>, g, dim3(256), 0, stream, grid, heads, size, init, decay,
-                       st);
+               static_cast<uint32_t>((size / 4 + 255) / 256), back ? 2 : 1);
+  hipLaunchKernelGGL(la_carry, g, dim3(256), 0, stream, grid, heads, size, fwd, back ? *back : fwd);
   return hipGetLastError();
 }
 
 // ---- sums --------------------------------------------------------------------------------------------
 
-// out[t, hk, :] = the sum over the `rep` heads that share key head hk, in their order.
+// out[t, hk, :] = the sum over the `rep` heads that share key head hk, in their order;
+// for dq and dk.
 template <typename T>
-__global__ __launch_bounds__(256) void la_sum_heads(const float* __restrict__ part, T* out,
-                                                    int64_t quads, int d, int rep) {
+__global__ __launch_bounds__(256) void la_sum_heads(const float* part_q, const float* part_k,
+                                                    T* out_q, T* out_k, int64_t quads, int d,
+                                                    int rep) {
+  const float* __restrict__ part = blockIdx.y ? part_k : part_q;
+  T* out = blockIdx.y ? out_k : out_q;
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= quads) return;
   const int per = d / 4;                               // quads of a head
@@ -319,7 +328,7 @@ hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStrea
     q.seg_out = st;
     q.seg_decay = dec;
     if ((err = la::pass_state(a.dtype, q, stream)) != hipSuccess) return err;
-    if ((err = launch_carry_states(false, p.grid, p.heads, s.dk * s.dv, a.state, dec, st, stream)) != hipSuccess)
+    if ((err = launch_carry(p.grid, p.heads, s.dk * s.dv, {a.state, dec, st}, nullptr, stream)) != hipSuccess)
       return err;
     p.seg_states = st;
   }
@@ -356,16 +365,15 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.paired = plan.paired;
     p.seg_out = at(plan.states);
     p.seg_decay = at(plan.decay);
-    if ((err = la::pass_state(a.dtype, p, stream)) != hipSuccess) return err;
-    if ((err = launch_carry_states(false, c.grid, c.heads, size, a.state, at(plan.decay),
-                                   at(plan.states), stream)) != hipSuccess)
-      return err;
-    p.y = q, p.z = g;
-    p.seg_out = at(plan.rev_states);
-    p.seg_decay = at(plan.rev_decay);
-    if ((err = la::pass_state_rev(a.dtype, p, stream)) != hipSuccess) return err;
-    if ((err = launch_carry_states(true, c.grid, c.heads, size, d.dlast, at(plan.rev_decay),
-                                   at(plan.rev_states), stream)) != hipSuccess)
+    PassArgs r = p;
+    r.y = q, r.z = g;
+    r.seg_out = at(plan.rev_states);
+    r.seg_decay = at(plan.rev_decay);
+    err = bf16 ? la::pass_states_bf16(p, r, stream) : la::pass_states_fp32(p, r, stream);
+    if (err != hipSuccess) return err;
+    const Carry back = {d.dlast, at(plan.rev_decay), at(plan.rev_states)};
+    if ((err = launch_carry(c.grid, c.heads, size, {a.state, at(plan.decay), at(plan.states)}, &back,
+                            stream)) != hipSuccess)
       return err;
   }
   c.u = at(plan.u);
@@ -382,7 +390,26 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.seg_states = plan.cut ? at(plan.states) : nullptr;
     p.out = rep > 1 ? at(plan.dq) : d.dq;
     p.out_f32 = rep > 1;
-    if ((err = la::pass_dq(a.dtype, p, stream)) != hipSuccess) return err;
+    PassArgs r = c;
+    r.x = k, r.y = q, r.z = g;
+    r.dA = static_cast<int>(s.dk), r.dB = static_cast<int>(s.dv);
+    r.sA = s.dv, r.sB = 1;
+    r.init = d.dlast;
+    r.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
+    r.paired = plan.paired;
+    r.last = d.dstate;
+    r.out = d.dv;
+    // One launch where both fit on the chip at once (3 x 333 float32, 6 heads: the call
+    // 60 us, 85 with two); larger ones are faster apart (4 x 8192, 16 heads of 128: 367
+    // and 390 us), each with its own registers.
+    if (plan.grid.slots * s.heads <= 256) {
+      err = !bf16 ? la::pass_dq_dv_fp32(p, r, stream)
+            : p.out_f32 ? la::pass_dq_dv_bf16_f32(p, r, stream)
+                        : la::pass_dq_dv_bf16(p, r, stream);
+    } else if ((err = la::pass_dq(a.dtype, p, stream)) == hipSuccess) {
+      err = la::pass_dv(a.dtype, r, stream);
+    }
+    if (err != hipSuccess) return err;
   }
   {
     PassArgs p = c;
@@ -397,33 +424,17 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.head_part = a.per_token ? nullptr : at(plan.head_part);
     if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;
   }
-  {
-    PassArgs p = c;
-    p.x = k, p.y = q, p.z = g;
-    p.dA = static_cast<int>(s.dk), p.dB = static_cast<int>(s.dv);
-    p.sA = s.dv, p.sB = 1;
-    p.init = d.dlast;
-    p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
-    p.paired = plan.paired;
-    p.last = d.dstate;
-    p.out = d.dv;
-    if ((err = la::pass_dv(a.dtype, p, stream)) != hipSuccess) return err;
-  }
   if (rep > 1 && s.tokens > 0) {
     const int64_t quads = s.tokens * s.key_heads * s.dk / 4;
-    const dim3 grid(static_cast<uint32_t>((quads + 255) / 256));
+    const dim3 grid(static_cast<uint32_t>((quads + 255) / 256), 2);
     const int dk = static_cast<int>(s.dk);
-    for (int i = 0; i < 2; ++i) {
-      const float* part = at(i ? plan.dk : plan.dq);
-      void* out = i ? d.dk : d.dq;
-      if (bf16)
-        hipLaunchKernelGGL(la_sum_heads<uint16_t>, grid, dim3(256), 0, stream, part,
-                           static_cast<uint16_t*>(out), quads, dk, rep);
-      else
-        hipLaunchKernelGGL(la_sum_heads<float>, grid, dim3(256), 0, stream, part,
-                           static_cast<float*>(out), quads, dk, rep);
-      if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
+    if (bf16)
+      hipLaunchKernelGGL(la_sum_heads<uint16_t>, grid, dim3(256), 0, stream, at(plan.dq), at(plan.dk),
+                         static_cast<uint16_t*>(d.dq), static_cast<uint16_t*>(d.dk), quads, dk, rep);
+    else
+      hipLaunchKernelGGL(la_sum_heads<float>, grid, dim3(256), 0, stream, at(plan.dq), at(plan.dk),
+                         static_cast<float*>(d.dq), static_cast<float*>(d.dk), quads, dk, rep);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   if (!a.per_token) {
     hipLaunchKernelGGL(la_sum_slots, dim3(static_cast<uint32_t>(s.heads)), dim3(256), 0, stream,
