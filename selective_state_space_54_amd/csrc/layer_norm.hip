@@ -23,6 +23,11 @@
 // The gradients of w and b: a block runs over many rows and keeps its columns'
 // sums in registers; at the end it writes one row of partial sums, and a second
 // kernel adds the blocks' rows, all in a fixed order.
+//
+// Measured: 32768 x 2560 bf16 with the residual 135 us (671 MB, 5.0 TB/s; a large
+// copy runs at 5.1 to 5.4), its gradient 146 + 6 us (4.6 TB/s); 16384 x 1536 float32
+// gradient 63 us with the sums (4.8 TB/s); 8 rows of 2560: 6 us, a launch and two
+// trips to memory, less than the host takes for the call.
 #include "mssm_internal.h"
 #include "scan_device.h"
 

