@@ -238,15 +238,15 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   g.L = s.packed ? 0 : (s.seqs > 0 ? s.tokens / s.seqs : 0);
   // Blocks to aim for: two on each of the 256 compute units at once, once
   // (backward) or twice over; a few blocks more than a multiple of 512 would be a
-  // round of their own (1 x 131072, 20 heads of 128: 1125 us with 1040 blocks, 972
-  // with 500 or 1000).  Twice over is better for short segments (packed prompts of
+  // round of their own (1 x 131072, 20 heads of 128: 1040 blocks take 16 %
+  // longer than 500 or 1000).  Twice over is better for short segments (packed prompts of
   // 32768 tokens, 32 heads of 128 x 64: 289 us, once over 322), once for those of
   // 4096 tokens and more, whose states mostly depend on a part of them (1 x 131072:
   // 903 and 946 us).  A segment costs its state four times through memory,
   // as much as the tiles of max(dk, dv) or so tokens: below twice that only to
   // reach 256 blocks, and never below two chunks (4 x 2048, 16 heads of 128: 82 us
   // in segments of 256 tokens, 89 of 512, 107 of 128; 3 x 333 float32 backward, 6
-  // heads: 81 us in segments of 64, 121 of 128).  From 256 sequences times heads
+  // heads: half as long again in segments of 128 as of 64).  From 256 sequences times heads
   // on, one segment each.
   const int64_t chunk = bf16 ? 64 : 32;
   p.paired = s.dv <= 64 && s.heads / s.key_heads % 2 == 0;
