@@ -282,3 +282,22 @@ def test_refusals():
             call()
             pytest.fail("accepted")
     torch.cuda.synchronize()
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 values: the last rows, forward and backward."""
+    D = 4096
+    rows = 2 ** 31 // D + 70
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, dy = (torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+             for _ in range(2))
+    w = torch.empty(D, device="cuda").uniform_(0.5, 1.5, generator=gen)
+    y, mean, rstd = mssm.layer_norm(x, w, return_stats=True)
+    gr = mssm.layer_norm_bwd(dy, x, w, mean, rstd)
+    torch.cuda.synchronize()
+    x64, dy64, w64 = host64(x[-64:]), host64(dy[-64:]), host64(w)
+    want, m64, r64 = ln.layer_norm(x64, w64, eps=1e-5)
+    check("mean", mean[-64:], m64, "fp32", np.ones(64))
+    check("y", y[-64:], want, "bf16", np.abs(want) + w64)
+    dx = ln.layer_norm_backward(dy64, x64, w64, m64, r64)[0]
+    check("dx", gr["dx"][-64:], dx, "bf16", np.full_like(dx, 2 * np.abs(dx).max()))

@@ -538,3 +538,52 @@ def test_tokens_out_of_reach_of_a_segments_state(backward):
         check(n, part(host64(got[n])[0], 1), want[n], "fp32")
     check("dlog_decay", part(host64(got["dlog_decay"])[0], 1), want["dlog_decay"], "decay", -1)
     check("dstate", part(host64(got["dstate"]), 1), want["dstate"], "fp32", 1)
+
+
+def test_offsets_past_32_bits():
+    """A packed sequence that begins past 2^31 values, after one whose end is past them."""
+    H, d, n = 16, 128, 150
+    T1 = 2 ** 31 // (H * d) + 1000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, dout = (torch.empty(T1 + n, H, d, dtype=torch.bfloat16, device="cuda").normal_(
+        generator=gen) for _ in range(4))
+    g = torch.empty(T1 + n, H, device="cuda").uniform_(-0.6, -0.4, generator=gen)
+    off = torch.tensor([0, T1, T1 + n], device="cuda")
+    o, last = mssm.linear_attention(q, k, v, g, seq_offsets=off, return_state=True)
+    gr = mssm.linear_attention_bwd(q, k, v, g, dout, seq_offsets=off)
+    torch.cuda.synchronize()
+    host = lambda t, a, b: host64(t[a:b])
+    # the first sequence's end: decays of exp(-80) and less make 200 tokens before it enough
+    a, b = T1 - 250, T1
+    want_o, want_s = la.linear_attention(*(host(t, a, b) for t in (q, k, v, g)),
+                                         np.array([0, 250]), scale=d ** -0.5)
+    check("o", host(o, b - 50, b), want_o[200:], "bf16")
+    check("last state", host64(last[:1]), want_s, "fp32", 1)
+    # the second sequence
+    a, b = T1, T1 + n
+    args = [host(t, a, b) for t in (q, k, v, g)] + [np.array([0, n])]
+    want_o, want_s = la.linear_attention(*args, scale=d ** -0.5)
+    check("o", host(o, a, b), want_o, "bf16")
+    check("last state", host64(last[1:]), want_s, "fp32", 1)
+    want = la.linear_attention_backward(*args, host(dout, a, b), scale=d ** -0.5)
+    for name in ("dq", "dk", "dv"):
+        check(name, host(gr[name], a, b), want[name], "bf16")
+    check("dlog_decay", host(gr["dlog_decay"], a, b), want["dlog_decay"], "decay", -1)
+
+
+def test_step_with_states_past_32_bits():
+    """More than 2^31 state values; the last sequences against the oracle."""
+    H, d = 16, 128
+    B = 2 ** 31 // (H * d * d) + 2
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.empty(B, H, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+               for _ in range(3))
+    g = torch.empty(H, device="cuda").uniform_(-1.0, 0.0, generator=gen)
+    state = torch.empty(B, H, d, d, device="cuda").normal_(generator=gen)
+    before = host64(state[-2:])
+    o = mssm.linear_attention_step(q, k, v, g, state)
+    torch.cuda.synchronize()
+    want_o, want_s = la.linear_attention(host64(q[-2:]), host64(k[-2:]), host64(v[-2:]), host64(g),
+                                         np.arange(3), scale=d ** -0.5, state=before)
+    check("o", host64(o[-2:]), want_o, "bf16")
+    check("state", host64(state[-2:]), want_s, "fp32", 1)
