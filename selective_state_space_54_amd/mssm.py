@@ -809,30 +809,34 @@ def _la_check(q, k, v, log_decay, seq_offsets, single=False):
     sizes (seqs, L, key_heads, heads, dk, dv) and what the C call takes after them."""
     dev = _gpu_of(q, "q")
     dt = q.dtype
-    dims = 1 if single or seq_offsets is not None else 2
+    packed = seq_offsets is not None
     qs, vs = q.shape, v.shape
+    dims = 1 if single or packed else 2
     if len(qs) != dims + 2 or len(vs) != dims + 2:
         lead = "[tokens" if dims == 1 else "[batch, L"
         raise ValueError(f"q, k and v must be {lead}, heads, head size]")
-    lead, vt = qs[:dims], vs[dims:]
-    key_heads, dk = qs[dims:]
-    heads, dv = vt
-    if (k.dtype is dt and v.dtype is dt and k.shape == qs and vs[:dims] == lead and
+    if dims == 1:
+        seqs, key_heads, dk = qs
+        lead, L = (seqs,), 1
+    else:
+        seqs, L, key_heads, dk = qs
+        lead = (seqs, L)
+    heads, dv = vs[-2], vs[-1]
+    shape = lead + (heads, dv)
+    if (k.dtype is dt and v.dtype is dt and k.shape == qs and vs == shape and
             k.get_device() == dev and v.get_device() == dev and q.is_contiguous() and
             k.is_contiguous() and v.is_contiguous()):
         rows = (key_heads * dk, key_heads * dk, heads * dv)
     else:
         rows = (_token_rows(q, "q", dt, qs, dev), _token_rows(k, "k", dt, qs, dev),
-                _token_rows(v, "v", dt, lead + vt, dev))
+                _token_rows(v, "v", dt, shape, dev))
     per_token = log_decay.dim() != 1
-    _expect(log_decay, "log_decay", torch.float32, lead + vt[:1] if per_token else vt[:1], dev)
-    if seq_offsets is not None:
+    _expect(log_decay, "log_decay", torch.float32, lead + (heads,) if per_token else (heads,), dev)
+    if packed:
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
             raise ValueError("seq_offsets must be [sequences + 1]")
         _expect(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
-        seqs, L = seq_offsets.shape[0] - 1, lead[0]
-    else:
-        seqs, L = lead[0], 1 if single else lead[1]
+        seqs, L = seq_offsets.shape[0] - 1, seqs
     decay = MSSM_DECAY_PER_TOKEN if per_token else MSSM_DECAY_PER_HEAD
     return dev, lead, (seqs, L, key_heads, heads, dk, dv), decay, rows + (_DTYPES[dt],)
 
