@@ -3,7 +3,7 @@ against the float64 formulas on the same inputs.
 
 Tolerances, |err| <= a |ref| + b s: s is the size of the values that meet in one
 result (for dweight, dbias the square root of the sum of squares over the rows).
-  bfloat16 results: a = 2^-8 (one rounding is 2^-9 |ref|), b = 1e-5.
+  bfloat16 results: a = 2^-8 (one rounding is at most that), b = 1e-5.
   float32 results, statistics and parameter gradients: a = b = 1e-5; sums of up to
     16384 values in a tree of at most 64 x 20 steps err by far less than
     100 * 2^-24 = 6e-6 of their values' size.

@@ -3,10 +3,11 @@ tokens, gradient) against the float64 recurrence on the same inputs.
 
 Tolerances, |err| <= a |ref| + b rms, rms the root mean square of the reference
 over a head's tokens:
-  bfloat16 results: 2^-8 |ref| + 2^-6 rms.  The output's rounding is at most 2^-9
-    of it.  The rounded operands (decayed scores, state) err by at most 2^-9 each,
-    independently, so a sum of such products errs by about 2^-10 rms; six of those
-    deviations for the largest of many, times two for two roundings, is 2^-6.4 rms.
+  bfloat16 results: 2^-8 |ref| + 2^-6 rms.  The output's rounding is at most 2^-8
+    of it.  The rounded operands (decayed scores between runs of 16 tokens, state)
+    err by at most 2^-8 each, independently, with a deviation of some 2^-9.5, so a
+    sum of such products errs by about 2^-9.5 rms; five of those deviations for the
+    largest of many, times sqrt(2) for two roundings, is 2^-6.7 rms.
   float32 results: 2e-5 (|ref| + rms): sums of up to a few hundred products at
     2^-24 each, in any order, stay under 300 * 2^-24 = 1.8e-5 of their sizes.
   states and their gradients (float32 from either type): the same 2e-5.
