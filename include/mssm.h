@@ -489,10 +489,8 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
  * inputs are multiplied on the bf16 matrix cores with float32 sums; states are
  * float32 and accurate to about 1e-6, outputs are rounded to bfloat16 once and
  * their operands (the state, and decayed scores but for those inside a run of 16
- * tokens) once before: about 0.2 % of the outputs' norm in all.  Whether the
- * last state is asked for decides how exactly the last segment's state is kept
- * on the way, so a call with it and one without may differ in an output's last
- * bit.  A sequence is worked on in chunks of 64 (float32: 32) tokens: infinities
+ * tokens) once before: about 0.2 % of the outputs' norm in all.  They do not
+ * depend on whether the last state is asked for.  A sequence is worked on in chunks of 64 (float32: 32) tokens: infinities
  * or NaN in a token's q, k, v can reach every output of its chunk and what
  * follows, never another sequence.
  *
