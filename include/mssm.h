@@ -487,12 +487,11 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
  *
  * Precision: float32 inputs are multiplied and summed in float32.  bfloat16
  * inputs are multiplied on the bf16 matrix cores with float32 sums; states are
- * float32 and accurate to about 1e-6, outputs are rounded to bfloat16 once and
- * their operands (the state, and decayed scores but for those inside a run of 16
- * tokens) once before: about 0.2 % of the outputs' norm in all.  They do not
- * depend on whether the last state is asked for.  A sequence is worked on in chunks of 64 (float32: 32) tokens: infinities
- * or NaN in a token's q, k, v can reach every output of its chunk and what
- * follows, never another sequence.
+ * float32 and accurate to about 1e-6; outputs and gradients of q, k, v are rounded
+ * to bfloat16 once (what they are made of keeps 16 bits or more).  Outputs do not
+ * depend on whether the last state is asked for.  A sequence is worked on in
+ * chunks of 64 (float32: 32) tokens: infinities or NaN in a token's q, k, v can
+ * reach every output of its chunk and what follows, as NaN, never another sequence.
  *
  * Supported: dk and dv multiples of 16 from 16 to 128
  * (mssm_linear_attention_supports); heads a multiple of key_heads.

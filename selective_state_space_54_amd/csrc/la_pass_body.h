@@ -4,10 +4,11 @@
 // tokens of 20 heads of 128: 890 us and 867.)  In scope: p, m, and the number of
 // blocks and this block's index, `blocks` and `index`.
   constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int kStateParts = kBf16 && kDot != 0 ? 3 : 1;  // of the state as an operand
+  constexpr int kStateParts = !kBf16 ? 1 : kDot != 0 ? 3 : 2;  // of the state as an operand
   constexpr bool kExact = !kBf16 || kDot != 0;             // float32 results depend on the scores
   constexpr int NR = C / 16, NK = C / 32, NM = DA / 16, TB = 64 * NT;
-  constexpr int PP = Lds<T, C, DA, NT, kHeads, kOut, kDot>::PP;
+  using Shared = Lds<T, C, DA, NT, kHeads, kOut, kDot>;
+  constexpr int PP = Shared::PP, kHeadP = Shared::PR * PP;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -140,10 +141,10 @@
   float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
 
   constexpr int kDumpSize = DA * TB;
-  // The second parts of the diagonal's scores lie in tiles of p that no product reads:
-  // (0 and 1, 2 and 3), in reverse (2 and 3, 0 and 1).
-  auto rest_at = [&](int rt) {
-    return (16 * ((kRev ? 2 : 0) + (rt & 1)) + l16) * PP + 16 * ((kRev ? 0 : 2) + (rt >> 1)) + 4 * g4;
+  // The scores' second parts: those of tile (rt, ct) lie in tile (ct, rt) of p, which the
+  // mask leaves empty, those of the diagonal below the rest.
+  auto rest_at = [&](int rt, int ct) {
+    return ((ct == rt ? C : 16 * ct) + l16) * PP + 16 * rt + 4 * g4;
   };
   float edge = 0.0f, head_sum = 0.0f;      // dg's are wavefront 0's
   double decay_sum = 0.0;
@@ -246,7 +247,7 @@
 #pragma unroll
       for (int hh = 0; hh < kHeads; ++hh) {
         const Decay<C>& dh = m.d[it & 1][hh];
-        T* const ph = m.p + hh * C * PP;
+        T* const ph = m.p + hh * kHeadP;
         const float gi = dh.hi[i], gil = dh.lo[i];
 #pragma unroll
         for (int u = 0; u < kWaveTiles; ++u) {
@@ -278,17 +279,15 @@
               }
             }
             lds_store4(ph + i * PP + j0, a);
-            if constexpr (kBf16) {
-              if (ct == rt) lds_store4_rest(ph + rest_at(rt), a);
-            }
+            if constexpr (kBf16) lds_store4_rest(ph + rest_at(rt, ct), a);
             if constexpr (kDot == 1) {
               row_sum += (b[0] + b[1]) + (b[2] + b[3]);
               // sums over this wavefront's 16 rows i, for each of the four j
 #pragma unroll
               for (int r = 0; r < 4; ++r) b[r] = row16_sum(b[r]);
-              if (l16 == 0) *reinterpret_cast<f32x4*>(&m.cols[rt][j0]) = b;
+              if (l16 == 0) *reinterpret_cast<f32x4*>(&m.cols[8 * rt * (rt + 1) + j0]) = b;
             }
-          } else if ((ct ^ rt) == 1) {
+          } else if (!kBf16 && (ct ^ rt) == 1) {
             lds_store4(ph + i * PP + j0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});   // read with its neighbour
           }
         }
@@ -381,23 +380,36 @@
         zf[k][t] = frag_col<TB, kStep>(m.z, 32 * k, c_wave + 4 * t, lane);
 
     if constexpr (kOut) {
+      // whether both of row tile r's tiles 2 k and 2 k + 1 hold scores, or the diagonal's only
+      auto both = [](int k, int r) { return kRev ? 2 * k >= r : 2 * k + 1 <= r; };
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (kRev ? k < r / 2 : k > r / 2) continue;
-          const Frag<T> pf = frag_at(m.p + (hw * C + 16 * r + l16) * PP + 32 * k + 4 * g4);
+          const T* at_p = m.p + hw * kHeadP + (16 * r + l16) * PP + 32 * k + 4 * g4;
+          Frag<T> pf;
+          if constexpr (kBf16) {
+            pf = both(k, r) ? frag_at(at_p) : half_frag(lds_read8(at_p + 16 * kRev), kRev);
+          } else {
+            pf = frag_at(at_p);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
         }
       if constexpr (kBf16) {
-        static_assert(NR == 4, "tiles for the diagonal's second parts");
+        const T* rest = m.p + hw * kHeadP;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const Frag<T> rest = half_frag(lds_read8(m.p + hw * C * PP + rest_at(r)), r & 1);
+        for (int k = 0; k < NK; ++k)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[r / 2][t], rest);
-        }
+          for (int r = 0; r < NR; ++r) {
+            if (kRev ? k < r / 2 : k > r / 2) continue;
+            const Frag<T> pf = both(k, r) ? frag_of(lds_read8(rest + rest_at(r, 2 * k)),
+                                                    lds_read8(rest + rest_at(r, 2 * k + 1)))
+                                          : half_frag(lds_read8(rest + rest_at(r, r)), kRev);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma(acc[r][t], zf[k][t], pf);
+          }
       }
       // Stores through a descriptor that ends with the chunk's last value: rows and
       // columns past it are dropped by the hardware, so no branch stands around them.
@@ -415,8 +427,9 @@
         // Each wavefront finishes 16 tokens, lane group g4 with its part of the sums,
         // and without branches, beside the products.
         const int w = NR == 4 ? wave : wave & 1, i2 = 16 * w + l16;
+        const int tile = NR == 4 ? g4 : g4 & 1;
         float qd = m.dot[g4][i2];
-        const float rows = m.rows[NR == 4 ? 0 : g4 & 1][i2], cols = m.cols[NR == 4 ? g4 : g4 & 1][i2];
+        const float rows = m.rows[NR == 4 ? 0 : g4 & 1][i2], cols = m.cols[8 * tile * (tile + 1) + i2];
         float u = (g4 < (NR == 4 ? 1 : w + 1) ? rows : 0.0f) - (g4 >= w && g4 < NR ? cols : 0.0f);
         qd += __shfl_xor(qd, 16, 64);
         u += __shfl_xor(u, 16, 64);

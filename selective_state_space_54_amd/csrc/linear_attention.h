@@ -47,15 +47,19 @@
 // per lane and a product eight v_mfma_f32_16x16x4_f32, whose four sums per
 // instruction take the fragments' values in the same order on both sides.
 //
-// Rounding.  Products of bfloat16 inputs accumulate in float32.  The decayed
-// scores and the state are rounded to bfloat16 where they are operands of the
-// output's products (the output is rounded to bfloat16 itself), except the
-// scores of the 16 x 16 tiles on the diagonal, which keep 16 bits: where decays
-// are strong, or a sequence begins, a token's output is little more than its own
-// term, and that rounding would not average out.  Where float32
-// results depend on them (the state's own update, dg) the operand is split in
-// three bfloat16 parts, 24 bits.  Decays, their sums (float64 inside a chunk,
-// kept as a float32 pair) and the state are 32 bits or more.
+// Rounding.  Products of bfloat16 inputs accumulate in float32.  Float32 operands
+// go through the bfloat16 products in parts, each the rounding of what the parts
+// before it leave.  The decayed scores, and the state where it is an operand of
+// an output that is rounded to bfloat16 itself, have two (16 bits, 2^-17.5 of
+// them on average): an output then differs from the float32 formula rounded once
+// by 1e-4 of the norm, a last place where the rounding is all but a tie.  (One part,
+// but for the scores of the 16 x 16 tiles on the diagonal: 1.8e-3.  The second
+// costs 1 x 131072 tokens of 20 heads of 128 930 us, not 874; packed prompts of
+// 32768 tokens, 32 heads of 128 x 64 304, not 284; a gradient over 4 x 8192, 16
+// heads of 128 756, not 748.)  Where float32 results depend on them (the state's
+// own update, dg) the operand has three parts, 24 bits.  Decays, their sums (float64
+// inside a chunk, kept as a float32 pair) and the state are 32 bits or more.
+//
 // What bounds it.  On long prompts memory, then what a wavefront issues between a
 // chunk's barriers: 1 x 131072 tokens of 20 heads of 128, bf16, moves 2.7 GB in
 // 660 us (4.1 TB/s; 256-byte rows reach 4.1 to 4.9 when only copied) with the
@@ -564,16 +568,17 @@ template <typename T, int C, int DA, int NT, int kHeads, bool kOut, int kDot>
 struct Lds {
   static constexpr int TB = 64 * NT;                        // columns of z
   static constexpr int PP = C + 16 / sizeof(T);             // row pitch of p
+  static constexpr int PR = C + (sizeof(T) == 2 ? 16 : 0);  // rows of p: a head's
   T x[kOut ? C * DA : 8];
   T y[C * DA];
   T z[C * TB];
   T e[kDot == 1 ? C * TB : 8];
-  T p[kOut ? kHeads * C * PP : 8];
+  T p[kOut ? kHeads * PR * PP : 8];
   Decay<C> d[2][kHeads];
   float dot[kDot ? 4 : 1][C];
-  float rows[kDot == 1 ? 2 : 1][C];
-  float cols[kDot == 1 ? 4 : 1][C];
-  float edge[4];
+  float rows[kDot == 1 && C == 32 ? 2 : 1][kDot == 1 ? C : 4];
+  float cols[kDot == 1 ? C / 32 * (C + 16) : 4];            // row tile rt's first 16 (rt + 1), on end
+  float edge[kDot == 2 ? 4 : 1];
 };
 
 // Of the chunks of a segment, those whose carried-through part of dg is computed
