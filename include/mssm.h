@@ -514,7 +514,7 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
  *   dv_out      : [tokens, heads, dv] of `dtype`, dense
  *   dlog_decay  : float32, as log_decay
  *   dstate      : gradient of the initial state [seqs, heads, dk, dv] float32,
- *                 or NULL
+ *                 or NULL; may be dlast or state itself
  *   Every gradient is overwritten.  The states are recomputed.  Sums over
  *   tokens, heads and segments run in a fixed order: results are deterministic.
  */

@@ -575,9 +575,13 @@
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int c = col_of(t, l16);
+      if constexpr (kDot != 0) {                           // (rows consecutive in memory)
+        if (row_of(mt, 0) < p.dA && c < p.dB) store4(dst + row_of(mt, 0) + c * p.sB, s[mt][t]);
+      } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int a = row_of(mt, r);
-        if (a < p.dA && c < p.dB) dst[a * p.sA + c * p.sB] = s[mt][t][r];
+        for (int r = 0; r < 4; ++r) {
+          const int a = row_of(mt, r);
+          if (a < p.dA && c < p.dB) dst[a * p.sA + c * p.sB] = s[mt][t][r];
+        }
       }
     }

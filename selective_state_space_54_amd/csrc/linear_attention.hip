@@ -401,7 +401,6 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     r.init = d.dlast;
     r.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
     r.paired = plan.paired;
-    r.last = d.dstate;
     r.out = d.dv;
     // One launch where both fit on the chip at once (3 x 333 float32, 6 heads: the call
     // 60 us, 85 with two); larger ones are faster apart (4 x 8192, 16 heads of 128: 367
@@ -422,6 +421,10 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     p.sA = 1, p.sB = s.dv;
     p.init = d.dlast;
     p.seg_states = plan.cut ? at(plan.rev_states) : nullptr;
+    // dstate is written here, where the adjoint is walked for the last time and the
+    // states are no longer read: it may then be dlast (each block has read its own part)
+    // or the state.
+    p.last = d.dstate;
     p.out = rep > 1 ? at(plan.dk) : d.dk;
     p.out_f32 = rep > 1;
     p.dg = a.per_token ? d.dg : nullptr;

@@ -932,7 +932,7 @@ def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, sca
                               dstate=None, seq_offsets=None, stream=None):
     """Gradients of sum(dout * o) + sum(dstate * last state) of linear_attention.  ``grads``
     maps dq, dk, dv (of the inputs' dtype), dlog_decay (float32) and, for the initial state's,
-    dstate to dense tensors that are overwritten."""
+    dstate to dense tensors that are overwritten; grads["dstate"] may be dstate or state."""
     dev, lead, sizes, decay, tail = _la_check(q, k, v, log_decay, seq_offsets)
     seqs, _, _, H, dk, dv = sizes
     states = (seqs, H, dk, dv)
