@@ -53,8 +53,8 @@ mssm_status shape_of(int64_t seqs, int64_t L, int64_t key_heads, int64_t heads, 
 mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm_dtype dtype,
                     mssm::LaPlan* plan) {
   *plan = mssm::plan_la(s, backward, dtype == MSSM_BFLOAT16);
+  if (plan->overflow) return MSSM_ERROR_SIZE_OVERFLOW;
   int64_t n;
-  if (!product({plan->grid.slots, s.heads, 128 * 128, 4 * 4, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (!product({plan->grid.slots, s.heads}, &n) || n > kMaxBlocks / (backward ? 2 : 1))
     return MSSM_ERROR_NOT_SUPPORTED;
   if (backward && s.heads != s.key_heads &&

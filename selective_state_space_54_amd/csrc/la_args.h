@@ -46,9 +46,12 @@ struct PassArgs {
   bool out_f32 = false;              // dq, dk: float32 instead
   // gradient of the log decays: written by dq, read by dk
   float* u = nullptr;                // [tokens, heads]
-  float* q_sums = nullptr;           // [slots, chunks_per_slot, heads, 4]: a wavefront's part each
-  float* dumps = nullptr;            // [slots, dumps_per_slot, heads, ..]: states as dq holds them
+  float* q_sums = nullptr;           // [a segment's chunks, heads, 4]: a wavefront's part each
+  float* dumps = nullptr;            // [a segment's dumps, heads, ..]: states as dq holds them
+  // A segment's chunks and dumps (one for every 256 tokens begun) lie from slot times
+  // these on, with by_token also its first token / C (/ 256) further.
   int64_t chunks_per_slot = 0, dumps_per_slot = 0;
+  bool by_token = false;
   // written by dk
   float* dg = nullptr;               // [tokens, heads], or null
   float* head_part = nullptr;        // [slots, heads]: sums of dg, or null

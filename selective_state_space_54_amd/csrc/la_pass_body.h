@@ -141,6 +141,8 @@
   float* dg_at = kDot == 2 && p.dg ? p.dg + first * p.heads + h : nullptr;
 
   constexpr int kDumpSize = DA * TB;
+  const int64_t chunk0 = slot * p.chunks_per_slot + (p.by_token ? at.start / C : 0);
+  const int64_t dump0 = slot * p.dumps_per_slot + (p.by_token ? at.start / (C * kStride<C>) : 0);
   // The scores' second parts: those of tile (rt, ct) lie in tile (ct, rt) of p, which the
   // mask leaves empty, those of the diagonal below the rest.
   auto rest_at = [&](int rt, int ct) {
@@ -165,8 +167,8 @@
     float* dump = nullptr;
     if constexpr (kDot != 0) {
       if (back == 0)
-        dump = p.dumps + ((slot * p.dumps_per_slot + (chunks - 1 - ck) / kStride<C>) * p.heads + h) *
-                             int64_t(kDumpSize) + tid * 4;
+        dump = p.dumps + ((dump0 + (chunks - 1 - ck) / kStride<C>) * p.heads + h) * int64_t(kDumpSize) +
+               tid * 4;
     }
     // (dk: the first half of the state that dq left there, loaded before the products
     // that stand between, into the registers of the tiles now in LDS)
@@ -202,7 +204,7 @@
           for (int q = 0; q < 4; ++q) ev[r][t][q] = to_float(raw[q]);
         }
       uv = u_at[static_cast<uint32_t>(min(lane, n - 1) * p.heads)];
-      const f32x4 q = *reinterpret_cast<const f32x4*>(p.q_sums + ((slot * p.chunks_per_slot + ck) * p.heads + h) * 4);
+      const f32x4 q = *reinterpret_cast<const f32x4*>(p.q_sums + ((chunk0 + ck) * p.heads + h) * 4);
       qs = (q[0] + q[1]) + (q[2] + q[3]);
     }
 
@@ -442,7 +444,7 @@
             g4 == 0 && mine ? static_cast<int>(i2 * heads * 4) : 0x3ffffff0, 0, 0);
         const float sum = row16_sum(mine && i2 < n ? qd : 0.0f);
         __builtin_amdgcn_raw_buffer_store_b32(
-            __float_as_uint(sum), make_buf(p.q_sums + ((slot * p.chunks_per_slot + ck) * p.heads + h) * 4, 16),
+            __float_as_uint(sum), make_buf(p.q_sums + ((chunk0 + ck) * p.heads + h) * 4, 16),
             lane == 0 ? wave * 4 : 0x3ffffff0, 0, 0);
       }
       if constexpr (kDot == 2) {

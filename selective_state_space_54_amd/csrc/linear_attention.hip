@@ -2,6 +2,10 @@
 // segments, the pass that joins the segments' states, the single-token step,
 // the sums over heads that share queries and keys, and the order of launches.
 // The matrix products are in linear_attention.h.
+#include <stdint.h>
+
+#include <initializer_list>
+
 #include "la_args.h"
 #include "linear_attention.h"
 #include "mssm_internal.h"
@@ -271,34 +275,51 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   g.slots = s.packed ? s.tokens / seg + s.seqs : s.seqs * g.segs;
   p.cut = len > seg;
 
-  const size_t state = static_cast<size_t>(s.dk) * s.dv * s.heads * 4;
-  const size_t per_slot = round_up(static_cast<size_t>(g.slots) * s.heads * 4);
+  // as many values of four bytes as the factors' product, at an aligned place
   size_t at = 0;
-  auto take = [&](size_t bytes) {
+  auto take = [&](std::initializer_list<int64_t> factors) {
     const size_t o = at;
-    at += round_up(bytes);
+    size_t n = 4;
+    for (int64_t f : factors) p.overflow |= __builtin_mul_overflow(n, static_cast<size_t>(f), &n);
+    p.overflow |= n > SIZE_MAX / 2 || __builtin_add_overflow(at, round_up(n), &at);
     return o;
   };
   if (p.cut) {
-    p.states = take(state * g.slots);
-    p.decay = take(per_slot);
+    p.states = take({g.slots, s.heads, s.dk, s.dv});
+    p.decay = take({g.slots, s.heads});
   }
   if (backward) {
     if (p.cut) {
-      p.rev_states = take(state * g.slots);
-      p.rev_decay = take(per_slot);
+      p.rev_states = take({g.slots, s.heads, s.dk, s.dv});
+      p.rev_decay = take({g.slots, s.heads});
     }
+    // Room for a whole segment's chunks and kept states in every slot, or, where packed
+    // sequences are many and a segment long, for what the tokens can fill: a segment of n
+    // tokens from token a on writes ceil(n / 256) states, no more than lie between
+    // a / 256 + slot and the next segment's (a + n) / 256 + slot + 1.  (512 sequences of
+    // 131072 tokens, 20 heads of 128: 2.8 GB, 15.5 by slots.)
     const int64_t every = 256 / chunk;
     p.chunks_per_slot = seg / chunk;
     p.dumps_per_slot = (p.chunks_per_slot + every - 1) / every;
-    const size_t held = static_cast<size_t>(s.dk <= 64 ? 64 : 128) * (s.dv <= 64 ? 64 : 128) * 4;
-    p.dumps = take(held * s.heads * p.dumps_per_slot * g.slots);
-    p.q_sums = take(static_cast<size_t>(p.chunks_per_slot) * g.slots * s.heads * 16);
-    p.u = take(static_cast<size_t>(s.tokens) * s.heads * 4);
-    p.head_part = take(per_slot);
+    int64_t chunks = p.chunks_per_slot, dumps = p.dumps_per_slot;
+    const bool chunks_fit = !__builtin_mul_overflow(chunks, g.slots, &chunks);
+    const bool dumps_fit = !__builtin_mul_overflow(dumps, g.slots, &dumps);
+    const bool fit = chunks_fit && dumps_fit;
+    p.by_token = s.packed && (!fit || s.tokens / 256 + g.slots < dumps);
+    if (p.by_token) {
+      p.chunks_per_slot = p.dumps_per_slot = 1;
+      chunks = s.tokens / chunk + g.slots;
+      dumps = s.tokens / 256 + g.slots;
+    } else {
+      p.overflow |= !fit;
+    }
+    p.dumps = take({dumps, s.heads, s.dk <= 64 ? 64 : 128, s.dv <= 64 ? 64 : 128});
+    p.q_sums = take({chunks, s.heads, 4});
+    p.u = take({s.tokens, s.heads});
+    p.head_part = take({g.slots, s.heads});
     if (s.heads != s.key_heads) {
-      p.dq = take(static_cast<size_t>(s.tokens) * s.heads * s.dk * 4);
-      p.dk = take(static_cast<size_t>(s.tokens) * s.heads * s.dk * 4);
+      p.dq = take({s.tokens, s.heads, s.dk});
+      p.dk = take({s.tokens, s.heads, s.dk});
     }
   }
   p.bytes = at;
@@ -385,6 +406,7 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
   c.dumps = at(plan.dumps);
   c.chunks_per_slot = plan.chunks_per_slot;
   c.dumps_per_slot = plan.dumps_per_slot;
+  c.by_token = plan.by_token;
   {
     PassArgs p = c;
     p.x = g, p.y = v, p.z = k, p.e = q;

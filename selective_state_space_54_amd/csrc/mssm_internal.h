@@ -446,7 +446,9 @@ struct LaPlan {
   size_t states = 0, decay = 0, rev_states = 0, rev_decay = 0, u = 0, q_sums = 0, dumps = 0;
   size_t head_part = 0, dq = 0, dk = 0;
   int64_t chunks_per_slot = 0, dumps_per_slot = 0;
+  bool by_token = false;
   size_t bytes = 0;
+  bool overflow = false;          // bytes does not fit
 };
 LaPlan plan_la(const LaShape& s, bool backward, bool bf16);
 hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream);

@@ -1,5 +1,6 @@
 """Linear attention and layer norm on the GPU: buffers that a caller passes twice, and
 arguments at the ends of what the calls take."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -8,8 +9,10 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
+from gpu_support import host64  # noqa: E402
+from oracle import linear_attention as la  # noqa: E402
 from selective_state_space_54_amd import mssm  # noqa: E402
-from test_linear_attention_gpu import DT, make, offsets_kw, on_gpu  # noqa: E402
+from test_linear_attention_gpu import DT, check, make, offsets_kw, on_gpu  # noqa: E402
 
 
 # sequences of one segment and of several; few and many blocks (dq beside dv, and apart)
@@ -31,3 +34,37 @@ def test_the_states_gradient_may_be_written_over_what_it_comes_from(dtype, batch
     torch.cuda.synchronize()
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("per_head", [False, True], ids=["token", "head"])
+def test_gradient_of_many_short_sequences_and_some_long_ones(dtype, per_head):
+    """Segments of 1024 tokens for sequences of 0 to 3000, so that what a segment keeps lies
+    by its first token: four heads against the oracle."""
+    rng = np.random.default_rng(81)
+    lengths = [3000, 0, 1] + [int(n) for n in rng.integers(0, 40, 250)] + [1100, 257, 256, 255]
+    lengths += [16384 - sum(lengths), 0]
+    H, heads = 32, (0, 13, 14, 31)
+    c = make(82, lengths, H, H, 16, 16, dtype, per_head=per_head, packed=True, decay=(1e-4, 0.1))
+    per_slot = mssm.mssm_linear_attention_workspace_size(1, 16384, H, H, 16, 16, DT[dtype],
+                                                         packed=True, backward=True)
+    many = mssm.mssm_linear_attention_workspace_size(len(lengths), 16384, H, H, 16, 16, DT[dtype],
+                                                     packed=True, backward=True)
+    assert many - per_slot < 4 * len(lengths) * H * 64 * 64 * 4       # not four states a slot
+    q, k, v, g, dout, state, dlast = on_gpu(c, "q", "k", "v", "log_decay", "dout", "state", "dlast")
+    o, last = mssm.linear_attention(q, k, v, g, state=state, return_state=True, **offsets_kw(c))
+    got = mssm.linear_attention_bwd(q, k, v, g, dout, state=state, dstate=dlast, **offsets_kw(c))
+    torch.cuda.synchronize()
+    part = lambda t, axis: np.take(host64(t), heads, axis=axis)
+    args = (part(c["q"], 1), part(c["k"], 1), part(c["v"], 1), part(c["log_decay"], -1),
+            c["offsets"])
+    s0, d1 = part(c["state"], 1), part(c["dlast"], 1)
+    want_o, want_s = la.linear_attention(*args, scale=0.25, state=s0)
+    check("o", part(o, 1), want_o, dtype)
+    check("last state", part(last, 1), want_s, "fp32", 1)
+    want = la.linear_attention_backward(*args, part(c["dout"], 1), scale=0.25, state=s0, dlast=d1)
+    for n in ("dq", "dk", "dv"):
+        check(n, part(got[n], 1), want[n], dtype)
+    check("dlog_decay", part(got["dlog_decay"], -1), want["dlog_decay"], "decay",
+          0 if per_head else -1)
+    check("dstate", part(got["dstate"], 1), want["dstate"], "fp32", 1)
