@@ -574,7 +574,7 @@ mssm_status mssm_linear_attention_bwd(const void *q, const void *k, const void *
  *   weight, bias  : [D] float32; bias may be NULL
  *   mean, rstd    : [rows] float32, given together (for the backward pass) or
  *                   both NULL
- * D up to 16384 (MSSM_ERROR_NOT_SUPPORTED above).  eps >= 0.
+ * D up to 16384 and rows below 2^32 (MSSM_ERROR_NOT_SUPPORTED above).  eps >= 0.
  *
  * mssm_layer_norm_bwd: gradients of sum(dy * y) (+ sum(dsum * t)) from what was
  * normalised (x of this call: t of the forward pass) and its mean and rstd.

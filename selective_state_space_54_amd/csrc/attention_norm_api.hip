@@ -221,8 +221,7 @@ mssm_status check_norm(int64_t rows, int64_t D, mssm_dtype dtype) {
   if (!mssm::norm_size_supported(D)) return MSSM_ERROR_NOT_SUPPORTED;
   int64_t n;
   if (!product({rows, D, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
-  // one block of 1024 threads per row at most
-  if (rows > kMaxBlocks / 4) return MSSM_ERROR_NOT_SUPPORTED;
+  if (rows >> 32 != 0) return MSSM_ERROR_NOT_SUPPORTED;
   return MSSM_SUCCESS;
 }
 

@@ -526,12 +526,34 @@ struct RunNorm {
     // (32768 x 2560 with a residual: 134 to 140 us from 256 to 4096 blocks; 60000 x
     // 333 float32: 65 us with 256, 34 from 768 on).
     int64_t blocks = (a.rows + per - 1) / per;
-    if (TPR <= 64 && blocks > 2048) blocks = 2048;
+    if (TPR <= 64) return launch<TPR, VPT>(a, blocks > 2048 ? 2048 : blocks);
+    // A block that holds one row takes one; the rows past what a grid can be get a
+    // launch of their own.
+    constexpr int64_t most = (int64_t(1) << 32) / kBlock - 1;
+    for (int64_t r = 0; r < a.rows; r += most) {
+      NormArgs p = a;
+      p.rows = a.rows - r < most ? a.rows - r : most;
+      const int64_t n = r * a.D;
+      p.x = static_cast<const T*>(a.x) + n;
+      p.y = static_cast<T*>(a.y) + n;
+      if (a.residual) {
+        p.residual = static_cast<const T*>(a.residual) + n;
+        p.sum = static_cast<T*>(a.sum) + n;
+      }
+      if (a.mean) p.mean += r, p.rstd += r;
+      const hipError_t e = launch<TPR, VPT>(p, p.rows);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  template <int TPR, int VPT>
+  hipError_t launch(const NormArgs& p, int64_t blocks) const {
+    constexpr int kBlock = TPR > 256 ? TPR : 256;
     const dim3 grid(static_cast<uint32_t>(blocks));
-    if (a.residual)
-      hipLaunchKernelGGL((layer_norm_kernel<T, TPR, VPT, true>), grid, dim3(kBlock), 0, stream, a);
+    if (p.residual)
+      hipLaunchKernelGGL((layer_norm_kernel<T, TPR, VPT, true>), grid, dim3(kBlock), 0, stream, p);
     else
-      hipLaunchKernelGGL((layer_norm_kernel<T, TPR, VPT, false>), grid, dim3(kBlock), 0, stream, a);
+      hipLaunchKernelGGL((layer_norm_kernel<T, TPR, VPT, false>), grid, dim3(kBlock), 0, stream, p);
     return hipGetLastError();
   }
 };
