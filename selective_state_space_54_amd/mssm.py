@@ -749,10 +749,14 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _gpu_of(t, name):
-    """The number of the GPU that t is on."""
+def _expect_tensor(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _gpu_of(t, name):
+    """The number of the GPU that t is on."""
+    _expect_tensor(t, name)
     _dtype_code(t.dtype)
     dev = t.get_device()
     if dev < 0:
@@ -788,8 +792,6 @@ def mssm_linear_attention_workspace_size(seqs, L, key_heads, heads, dk, dv, dtyp
 def _token_rows(t, name, dtype, shape, dev):
     """Checks a [tokens.., heads, d] tensor whose tokens are evenly spaced (a view into a
     wider projection's output is one) and returns the elements between tokens."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         _dense(t, name, dtype, shape, torch.device("cuda", dev))
     dense = shape[-2] * shape[-1]
@@ -808,6 +810,11 @@ def _la_check(q, k, v, log_decay, seq_offsets, single=False):
     """Checks a linear attention call's inputs.  Returns the GPU, the token dimensions, the
     sizes (seqs, L, key_heads, heads, dk, dv) and what the C call takes after them."""
     dev = _gpu_of(q, "q")
+    Tensor = torch.Tensor
+    if not (isinstance(k, Tensor) and isinstance(v, Tensor) and isinstance(log_decay, Tensor)):
+        _expect_tensor(k, "k")
+        _expect_tensor(v, "v")
+        _expect_tensor(log_decay, "log_decay")
     dt = q.dtype
     packed = seq_offsets is not None
     qs, vs = q.shape, v.shape
@@ -833,6 +840,7 @@ def _la_check(q, k, v, log_decay, seq_offsets, single=False):
     per_token = log_decay.dim() != 1
     _expect(log_decay, "log_decay", torch.float32, lead + (heads,) if per_token else (heads,), dev)
     if packed:
+        _expect_tensor(seq_offsets, "seq_offsets")
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
             raise ValueError("seq_offsets must be [sequences + 1]")
         _expect(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
@@ -960,6 +968,8 @@ def linear_attention_bwd(q, k, v, log_decay, dout, *, scale=None, state=None, ds
     returns the dict of gradients (dq, dk, dv, dlog_decay, and dstate, the initial state's,
     where ``state`` is given).  ``dstate`` is the gradient of the last state, if it has one."""
     dev, _, sizes, _, _ = _la_check(q, k, v, log_decay, seq_offsets)
+    if state is not None:
+        _expect_tensor(state, "state")
     nbytes = _la_workspace(sizes, q.dtype, seq_offsets is not None, True)
     with _on(stream):
         empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)

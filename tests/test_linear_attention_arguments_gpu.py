@@ -68,3 +68,22 @@ def test_gradient_of_many_short_sequences_and_some_long_ones(dtype, per_head):
     check("dlog_decay", part(got["dlog_decay"], -1), want["dlog_decay"], "decay",
           0 if per_head else -1)
     check("dstate", part(got["dstate"], 1), want["dstate"], "fp32", 1)
+
+
+@pytest.mark.parametrize("missing", ["q", "k", "v", "log_decay", "seq_offsets", "state", "dout"])
+def test_what_is_no_tensor_is_refused_by_name(missing):
+    """As the scan's calls do: a TypeError that names the argument."""
+    c = make(83, [5, 3], 1, 2, 16, 16, "bf16", packed=True)
+    a = dict(zip(("q", "k", "v", "log_decay", "state", "dout"),
+                 on_gpu(c, "q", "k", "v", "log_decay", "state", "dout")), **offsets_kw(c))
+    a[missing] = [1.0] if missing in ("seq_offsets", "state") else None
+    kw = {"seq_offsets": a["seq_offsets"], "state": a["state"]}
+    inputs = (a["q"], a["k"], a["v"], a["log_decay"])
+    calls = [lambda: mssm.linear_attention_bwd(*inputs, a["dout"], **kw)]
+    if missing != "dout":
+        calls.append(lambda: mssm.linear_attention(*inputs, **kw))
+    if missing not in ("dout", "seq_offsets"):
+        calls.append(lambda: mssm.linear_attention_step(*inputs, a["state"]))
+    for call in calls:
+        with pytest.raises(TypeError, match=f"^{missing} must be a torch.Tensor"):
+            call()
