@@ -173,6 +173,18 @@ def _dense(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace_args(workspace, device):
+    """Address and bytes of a caller's workspace tensor, None and 0 without one."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    nbytes = workspace.numel() * workspace.element_size()
+    return (workspace.data_ptr() if nbytes else None), nbytes
+
+
 def _dtype_code(dtype) -> int:
     if dtype not in _DTYPES:
         raise TypeError(f"dtype {dtype} not supported (float32 or bfloat16)")
@@ -290,8 +302,7 @@ def mssm_selective_scan_fwd_noalloc(x, delta, A, B, C, y, *, stream=None):
 def mssm_selective_scan_fwd_ws(x, delta, A, B, C, y, workspace, *, stream=None):
     """y <- selective scan with a caller-provided uint8 device workspace tensor."""
     batch, L, D, N = _check_scan_args(x, delta, A, B, C, y)
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     _check(load().mssm_selective_scan_fwd_ws(
         _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(y), ws_ptr, ws_bytes,
         batch, L, D, N, _DTYPES[x.dtype], _stream_handle(stream)), "mssm_selective_scan_fwd_ws")
@@ -318,8 +329,7 @@ class PreparedCall:
 def prepare_selective_scan_fwd_ws(x, delta, A, B, C, y, workspace, *, stream=None):
     """mssm_selective_scan_fwd_ws as a PreparedCall."""
     batch, L, D, N = _check_scan_args(x, delta, A, B, C, y)
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     args = (_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(y), ws_ptr, ws_bytes,
             batch, L, D, N, _DTYPES[x.dtype], _stream_handle(stream))
     return PreparedCall(load().mssm_selective_scan_fwd_ws, args, "mssm_selective_scan_fwd_ws",
@@ -358,8 +368,7 @@ def mssm_selective_scan_fwd_ex(x, delta, A, B, C, y, workspace, *, Dskip=None, z
     _check_optional(z, "z", x.dtype, (batch, L, D), dev)
     _check_optional(h0, "h0", torch.float32, (batch, D, N), dev)
     _check_optional(h_last, "h_last", torch.float32, (batch, D, N), dev)
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     _check(load().mssm_selective_scan_fwd_ex(
         _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(h0), _ptr(y),
         _ptr(h_last), _bbar_code(bbar), ws_ptr, ws_bytes, batch, L, D, N, _DTYPES[x.dtype],
@@ -457,8 +466,7 @@ def mssm_selective_ssm_fused_fwd(x, W_x, W_dt, dt_bias, A, y, workspace, *, stre
     """y <- scan(x, softplus(x_proj(x)[:R] @ W_dt + dt_bias), A, B, C) with B, C the
     remaining x_proj outputs; workspace is a uint8 device tensor."""
     batch, L, D, N, R = _check_fused_args(x, W_x, W_dt, dt_bias, A, y)
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     _check(load().mssm_selective_ssm_fused_fwd(
         _ptr(x), _ptr(W_x), _ptr(W_dt), _ptr(dt_bias), _ptr(A), _ptr(y), ws_ptr, ws_bytes,
         batch, L, D, N, R, _dtype_code(x.dtype), _stream_handle(stream)),
@@ -546,8 +554,7 @@ def mssm_mamba_block_fwd(u0, W_in, conv_w, conv_b, W_x, W_dt, dt_bias, A, Dskip,
     _check_optional(Dskip, "Dskip", torch.float32, (Di,), dev)
     _dense(W_out, "W_out", dt, (Di, Dm), dev)
     _dense(out, "out", torch.float32, (batch, L, Dm), dev)
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_ptr, ws_bytes = _workspace_args(workspace, u0.device)
     _check(load().mssm_mamba_block_fwd(
         _ptr(u0), _ptr(W_in), _ptr(conv_w), _ptr(conv_b), _ptr(W_x), _ptr(W_dt), _ptr(dt_bias),
         _ptr(A), _ptr(Dskip), _ptr(W_out), _ptr(out), ws_ptr, ws_bytes, batch, L, Dm, Di, N, R,
@@ -613,11 +620,11 @@ def mssm_selective_scan_bwd(x, delta, A, B, C, dout, grads, workspace, *, Dskip=
     dz, dh0 for the parts given) to float32 tensors that are overwritten."""
     batch, L, D, N = _check_bwd_args(x, delta, A, B, C, dout, grads, Dskip, z, h0)
     g = lambda k: _ptr(grads.get(k))
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     _check(load().mssm_selective_scan_bwd(
         _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(h0),
         _ptr(dout), g("dx"), g("ddelta"), g("dA"), g("dB"), g("dC"), g("dD"), g("dz"), g("dh0"),
-        ws_ptr, _bytes_of(workspace), batch, L, D, N, _DTYPES[x.dtype], _stream_handle(stream)),
+        ws_ptr, ws_bytes, batch, L, D, N, _DTYPES[x.dtype], _stream_handle(stream)),
         "mssm_selective_scan_bwd")
     return grads
 
@@ -659,11 +666,11 @@ def mssm_selective_scan_bwd_saved(x, delta, A, B, C, saved, dout, grads, workspa
     if saved is not None and (saved.device != x.device or not saved.is_contiguous()):
         raise ValueError("saved must be a contiguous tensor on the inputs' device")
     g = lambda k: _ptr(grads.get(k))
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() > 0 else None
+    ws_ptr, ws_bytes = _workspace_args(workspace, x.device)
     _check(load().mssm_selective_scan_bwd_saved(
         _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(h0),
         _ptr(saved), _bytes_of(saved), _ptr(dout), g("dx"), g("ddelta"), g("dA"), g("dB"),
-        g("dC"), g("dD"), g("dz"), g("dh0"), ws_ptr, _bytes_of(workspace), batch, L, D, N,
+        g("dC"), g("dD"), g("dz"), g("dh0"), ws_ptr, ws_bytes, batch, L, D, N,
         _DTYPES[x.dtype], _stream_handle(stream)), "mssm_selective_scan_bwd_saved")
     return grads
 
@@ -863,7 +870,7 @@ def _fwd(checked, q, k, v, log_decay, seq_offsets, state, o, last_state, scale, 
     _call("mssm_linear_attention_fwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), _address(seq_offsets), _address(state), o.data_ptr(),
           _address(last_state), sizes[4] ** -0.5 if scale is None else scale, decay,
-          _address(workspace), _bytes_of(workspace), *sizes, *tail)
+          *_workspace_args(workspace, q.device), *sizes, *tail)
 
 
 def mssm_linear_attention_fwd(q, k, v, log_decay, o, workspace, *, scale, state=None,
@@ -957,8 +964,8 @@ def mssm_linear_attention_bwd(q, k, v, log_decay, dout, grads, workspace, *, sca
     _call("mssm_linear_attention_bwd", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_decay.data_ptr(), _address(seq_offsets), _address(state), dout.data_ptr(),
           _address(dstate), g("dq"), g("dk"), g("dv"), g("dlog_decay"), g("dstate"),
-          dk ** -0.5 if scale is None else scale, decay, _address(workspace),
-          _bytes_of(workspace), *sizes, *tail)
+          dk ** -0.5 if scale is None else scale, decay,
+          *_workspace_args(workspace, q.device), *sizes, *tail)
     return grads
 
 
@@ -1062,7 +1069,7 @@ def mssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace
     _expect_optional(dbias, "dbias", torch.float32, (D,), dev)
     _call("mssm_layer_norm_bwd", dev, stream, dy.data_ptr(), _address(dsum), x.data_ptr(),
           weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
-          _address(dbias), _address(workspace), _bytes_of(workspace), rows, D, _DTYPES[dt])
+          _address(dbias), *_workspace_args(workspace, x.device), rows, D, _DTYPES[dt])
     return dx
 
 
