@@ -181,7 +181,16 @@ mssm_status mssm_linear_attention_bwd(const void* q, const void* k, const void* 
   if (st != MSSM_SUCCESS) return st;
   if (decay != MSSM_DECAY_PER_HEAD && decay != MSSM_DECAY_PER_TOKEN)
     return MSSM_ERROR_INVALID_VALUE;
-  if (heads == 0) return MSSM_SUCCESS;
+  if (heads == 0) {
+    // no head reads the queries and keys there may be: their gradients are zero
+    int64_t n;
+    if (!product({a.shape.tokens, key_heads, dk, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
+    if (n == 0) return MSSM_SUCCESS;
+    if (!dq || !dk_out) return MSSM_ERROR_INVALID_VALUE;
+    if (n / 8 / 1024 > kMaxBlocks - 1) return MSSM_ERROR_NOT_SUPPORTED;
+    return done(mssm::launch_la_no_heads(a.shape, dq, dk_out, dtype, static_cast<hipStream_t>(stream)),
+                "linear attention backward launch");
+  }
   const bool per_token = decay == MSSM_DECAY_PER_TOKEN;
   a.q_row = q_row, a.k_row = k_row, a.v_row = v_row;
   if (a.shape.tokens > 0 && seqs > 0) {

@@ -136,6 +136,20 @@ __global__ __launch_bounds__(256) void la_sum_heads(const float* part_q, const f
   la::store4(out + head * d + c, s);
 }
 
+hipError_t launch_sum_heads(const LaShape& s, const float* part_q, const float* part_k, void* dq,
+                            void* dk, int rep, mssm_dtype dtype, hipStream_t stream) {
+  const int64_t quads = s.tokens * s.key_heads * s.dk / 4;
+  const dim3 grid(static_cast<uint32_t>((quads + 255) / 256), 2);
+  const int d = static_cast<int>(s.dk);
+  if (dtype == MSSM_BFLOAT16)
+    hipLaunchKernelGGL(la_sum_heads<uint16_t>, grid, dim3(256), 0, stream, part_q, part_k,
+                       static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk), quads, d, rep);
+  else
+    hipLaunchKernelGGL(la_sum_heads<float>, grid, dim3(256), 0, stream, part_q, part_k,
+                       static_cast<float*>(dq), static_cast<float*>(dk), quads, d, rep);
+  return hipGetLastError();
+}
+
 // out[h] = sum over slots of part[slot, h]; one block per head.
 __global__ __launch_bounds__(256) void la_sum_slots(const float* __restrict__ part, float* out,
                                                     int64_t slots, int heads) {
@@ -454,16 +468,8 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     if ((err = la::pass_dk(a.dtype, p, stream)) != hipSuccess) return err;
   }
   if (rep > 1 && s.tokens > 0) {
-    const int64_t quads = s.tokens * s.key_heads * s.dk / 4;
-    const dim3 grid(static_cast<uint32_t>((quads + 255) / 256), 2);
-    const int dk = static_cast<int>(s.dk);
-    if (bf16)
-      hipLaunchKernelGGL(la_sum_heads<uint16_t>, grid, dim3(256), 0, stream, at(plan.dq), at(plan.dk),
-                         static_cast<uint16_t*>(d.dq), static_cast<uint16_t*>(d.dk), quads, dk, rep);
-    else
-      hipLaunchKernelGGL(la_sum_heads<float>, grid, dim3(256), 0, stream, at(plan.dq), at(plan.dk),
-                         static_cast<float*>(d.dq), static_cast<float*>(d.dk), quads, dk, rep);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
+    err = launch_sum_heads(s, at(plan.dq), at(plan.dk), d.dq, d.dk, rep, a.dtype, stream);
+    if (err != hipSuccess) return err;
   }
   if (!a.per_token) {
     hipLaunchKernelGGL(la_sum_slots, dim3(static_cast<uint32_t>(s.heads)), dim3(256), 0, stream,
@@ -471,6 +477,11 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   return hipSuccess;
+}
+
+hipError_t launch_la_no_heads(const LaShape& s, void* dq, void* dk, mssm_dtype dtype,
+                              hipStream_t stream) {
+  return launch_sum_heads(s, nullptr, nullptr, dq, dk, 0, dtype, stream);   // sums over none
 }
 
 hipError_t launch_la_step(const LaArgs& a, float* state, hipStream_t stream) {

@@ -454,6 +454,9 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16);
 hipError_t launch_la_fwd(const LaArgs& a, const LaPlan& plan, void* ws, hipStream_t stream);
 hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, void* ws,
                          hipStream_t stream);
+// Zero gradients of the queries and keys that no head reads.
+hipError_t launch_la_no_heads(const LaShape& s, void* dq, void* dk, mssm_dtype dtype,
+                              hipStream_t stream);
 // One token for each sequence (shape.tokens == shape.seqs), the state in place.
 hipError_t launch_la_step(const LaArgs& a, float* state, hipStream_t stream);
 

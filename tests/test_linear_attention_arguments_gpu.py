@@ -87,3 +87,17 @@ def test_what_is_no_tensor_is_refused_by_name(missing):
     for call in calls:
         with pytest.raises(TypeError, match=f"^{missing} must be a torch.Tensor"):
             call()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_without_heads_are_zero(dtype):
+    """Every gradient is overwritten, also that of queries and keys that no head reads."""
+    e = lambda *s: torch.full(s, float("nan"), dtype=DT[dtype], device="cuda")
+    q, v = e(2, 75, 3, 48), e(2, 75, 0, 32)
+    grads = {"dq": e(2, 75, 3, 48), "dk": e(2, 75, 3, 48), "dv": e(2, 75, 0, 32),
+             "dlog_decay": torch.zeros(2, 75, 0, device="cuda")}
+    mssm.mssm_linear_attention_bwd(q, q, v, torch.zeros(2, 75, 0, device="cuda"), v, grads, None,
+                                   scale=1.0)
+    torch.cuda.synchronize()
+    for n in ("dq", "dk"):
+        assert torch.equal(grads[n], torch.zeros_like(q)), n
