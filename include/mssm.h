@@ -496,7 +496,8 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
  * Supported: dk and dv multiples of 16 from 16 to 128
  * (mssm_linear_attention_supports); heads a multiple of key_heads.
  * Any element-aligned address; 16-byte aligned tensors and rows are faster.
- * q_row, k_row, v_row, heads * dk and heads * dv are below 2^22.
+ * heads * dk and heads * dv are below 2^22; so are q_row, k_row and v_row but
+ * in mssm_linear_attention_step.
  * The workspace (256-byte aligned, at least the size the query gives, which
  * may be 0) holds the states of the segments that long sequences are cut into.
  * tokens, seqs or heads equal to zero are valid: last states are still set.

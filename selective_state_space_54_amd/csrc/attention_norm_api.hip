@@ -1,5 +1,6 @@
 // C-ABI front end of linear attention and layer norm: argument checks, which
 // all run before the first HIP call, and dispatch.
+#include <initializer_list>
 #include <limits>
 
 #include "mssm_internal.h"
@@ -63,12 +64,17 @@ mssm_status plan_of(const mssm::LaShape& s, bool backward, mssm_dtype dtype,
   return MSSM_SUCCESS;
 }
 
-// Rows hold their heads.
-mssm_status check_rows(const mssm::LaArgs& a) {
+// Rows hold their heads.  (A single token's are reached in 64 bits, whatever lies
+// between them.)
+mssm_status check_rows(const mssm::LaArgs& a, bool single) {
   const mssm::LaShape& s = a.shape;
   if (a.q_row < s.key_heads * s.dk || a.k_row < s.key_heads * s.dk || a.v_row < s.heads * s.dv)
     return MSSM_ERROR_INVALID_VALUE;
-  if (a.q_row >= kMaxRow || a.k_row >= kMaxRow || a.v_row >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
+  for (int64_t row : {a.q_row, a.k_row, a.v_row}) {
+    int64_t n;
+    if (!single && row >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
+    if (!product({s.tokens, row, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
+  }
   return MSSM_SUCCESS;
 }
 
@@ -125,7 +131,7 @@ mssm_status mssm_linear_attention_fwd(const void* q, const void* k, const void* 
   a.q_row = q_row, a.k_row = k_row, a.v_row = v_row;
   if (a.shape.tokens > 0) {
     if (!q || !k || !v || !log_decay || !o) return MSSM_ERROR_INVALID_VALUE;
-    if ((st = check_rows(a)) != MSSM_SUCCESS) return st;
+    if ((st = check_rows(a, false)) != MSSM_SUCCESS) return st;
   } else if (!last_state) {
     return MSSM_SUCCESS;
   }
@@ -154,7 +160,7 @@ mssm_status mssm_linear_attention_step(const void* q, const void* k, const void*
   if (seqs == 0 || heads == 0) return MSSM_SUCCESS;
   if (!q || !k || !v || !log_decay || !state || !o) return MSSM_ERROR_INVALID_VALUE;
   a.q_row = q_row, a.k_row = k_row, a.v_row = v_row;
-  if ((st = check_rows(a)) != MSSM_SUCCESS) return st;
+  if ((st = check_rows(a, true)) != MSSM_SUCCESS) return st;
   int64_t blocks;
   if (!product({seqs, heads}, &blocks)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (blocks > kMaxBlocks) return MSSM_ERROR_NOT_SUPPORTED;
@@ -196,7 +202,7 @@ mssm_status mssm_linear_attention_bwd(const void* q, const void* k, const void* 
   if (a.shape.tokens > 0 && seqs > 0) {
     if (!q || !k || !v || !log_decay || !dout || !dq || !dk_out || !dv_out || !dlog_decay)
       return MSSM_ERROR_INVALID_VALUE;
-    if ((st = check_rows(a)) != MSSM_SUCCESS) return st;
+    if ((st = check_rows(a, false)) != MSSM_SUCCESS) return st;
   } else {
     // nothing to differentiate but the decays (zero) and the states that pass through
     if (!per_token && !dlog_decay) return MSSM_ERROR_INVALID_VALUE;

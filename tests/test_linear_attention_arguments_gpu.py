@@ -101,3 +101,21 @@ def test_gradients_without_heads_are_zero(dtype):
     torch.cuda.synchronize()
     for n in ("dq", "dk"):
         assert torch.equal(grads[n], torch.zeros_like(q)), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_step_on_a_token_of_a_long_prompt_s_projection(dtype):
+    """Tokens of [batch, L, width] with more than 2^22 values from sequence to sequence."""
+    B, L, Hk, H, d = 3, 6000, 1, 2, 64
+    u = torch.zeros(B, L, 1024, dtype=DT[dtype], device="cuda")
+    u[:, 4321] = torch.randn(B, 1024, device="cuda").to(DT[dtype])
+    token = u[:, 4321]
+    q, k = (token[:, i * d:(i + 1) * d].unflatten(-1, (Hk, d)) for i in range(2))
+    v = token[:, 2 * d:4 * d].unflatten(-1, (H, d))
+    assert q.stride(0) >= 2 ** 22
+    g = -torch.rand(B, H, device="cuda")
+    states = [torch.ones(B, H, d, d, device="cuda") for _ in range(2)]
+    o = mssm.linear_attention_step(q, k, v, g, states[0])
+    want = mssm.linear_attention_step(q.contiguous(), k.contiguous(), v.contiguous(), g, states[1])
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(*states)
