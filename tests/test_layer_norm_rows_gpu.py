@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
 from gpu_support import host64  # noqa: E402
 from oracle import layer_norm as ln  # noqa: E402
 from selective_state_space_54_amd import mssm  # noqa: E402
-from test_layer_norm_gpu import check  # noqa: E402
+from test_layer_norm_gpu import check, check_norm, make  # noqa: E402
 
 
 def _spot_check(rows, D, picks):
@@ -47,3 +47,10 @@ def test_more_rows_than_a_grid_of_wide_blocks():
         pytest.skip("needs 170 GB of memory")
     _spot_check(rows, D, [slice(0, 8), slice((1 << 22) - 2, 1 << 22), slice(rows - 8, rows)])
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [1000, 2560, 2600, 5000, 8200, 16384])
+def test_parameter_gradients_over_more_rows_than_blocks(dtype, D):
+    """A block then sums several rows: also those that a whole block holds."""
+    check_norm(make(D, 700, D, dtype), dtype, residual=D != 5000, bias=True)
