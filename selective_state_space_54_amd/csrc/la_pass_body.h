@@ -14,6 +14,10 @@
   const int l16 = lane & 15, g4 = lane >> 4;
 
   static_assert(kHeads == 1 || (NT == 2 && kDot == 0), "two heads of up to 64 columns");
+  static_assert(sizeof(Decay<C>) % sizeof(f32x4) == 0 && offsetof(Shared, d) % sizeof(f32x4) == 0 &&
+                    offsetof(Shared, p) % sizeof(f32x4) == 0 &&
+                    (kDot != 1 || offsetof(Shared, cols) % sizeof(f32x4) == 0),
+                "four values are read and written at once");
   const uint32_t block = logical_block(blocks, index);
   const uint32_t groups = static_cast<uint32_t>(p.heads) / kHeads;
   const int64_t slot = block / groups;

@@ -71,6 +71,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -401,7 +402,7 @@ struct Tile {
 
 // Decays of one chunk, in LDS.  Log decays are in powers of two.
 template <int C>
-struct Decay {
+struct alignas(16) Decay {
   float hi[C], lo[C];      // G, inclusive, as a float32 pair
   float ein[C];            // factor of the carried state at each token
   float w[C];              // factor of each token in the state's update
@@ -577,7 +578,7 @@ struct Lds {
   Decay<C> d[2][kHeads];
   float dot[kDot ? 4 : 1][C];
   float rows[kDot == 1 && C == 32 ? 2 : 1][kDot == 1 ? C : 4];
-  float cols[kDot == 1 ? C / 32 * (C + 16) : 4];            // row tile rt's first 16 (rt + 1), on end
+  alignas(16) float cols[kDot == 1 ? C / 32 * (C + 16) : 4];   // row tile rt's first 16 (rt + 1), on end
   float edge[kDot == 2 ? 4 : 1];
 };
 
