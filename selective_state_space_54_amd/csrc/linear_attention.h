@@ -270,8 +270,10 @@ __device__ __forceinline__ void lds_store4_rest(uint16_t* p, f32x4 v) {
                                        pack2(v[2] - low_half(u1), v[3] - high_half(u1))};
 }
 // A fragment with 16 terms in half h and none in the other.  (Products of 16 terms,
-// v_mfma_f32_16x16x16_bf16, would do half the work, but where one followed a product
-// of 32 into the same registers its results were wrong now and then.)
+// v_mfma_f32_16x16x16_bf16, would do half the work.  But in a variant where one followed
+// a product of 32 into the same registers, results were wrong now and then; why was not
+// found.  So no kernel has matrix products of two kinds:
+// tests/test_linear_attention_isa_cpu.py looks for them in the compiled code.)
 __device__ __forceinline__ Frag<uint16_t> half_frag(uint2 u, int h) {
   const uint2 none = make_uint2(0, 0);
   return h ? frag_of(none, u) : frag_of(u, none);
