@@ -483,7 +483,7 @@ mssm_status mssm_selective_scan_bwd_saved(const void *x, const void *delta, cons
  * at 0, does not decrease and ends at L) L is the number of tokens in all and
  * sequence i has tokens seq_offsets[i] .. seq_offsets[i + 1] - 1; a sequence
  * may be empty (its last state is its first).  Offsets outside 0 .. L are taken
- * as 0 or L; tokens that no sequence holds get no output.
+ * as 0 or L; outputs and gradients of tokens that no sequence holds are undefined.
  *
  * Precision: float32 inputs are multiplied and summed in float32.  bfloat16
  * inputs are multiplied on the bf16 matrix cores with float32 sums; states are

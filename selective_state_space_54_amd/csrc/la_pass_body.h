@@ -1,7 +1,8 @@
 // The pass of linear_attention.h: the body of la_pass, and of the function that the
 // kernels of two passes call.  (Included twice instead of called by both: through
-// the function, the compiler's registers for la_pass come out 2 % slower, 1 x 131072
-// tokens of 20 heads of 128: 890 us and 867.)  In scope: p, m, and the number of
+// the function, the compiler's registers for la_pass come out up to 2.5 % slower: a
+// gradient over 4 x 8192, 16 heads of 128, 768 us and 755, over 4 x 2048 in float32 575
+// and 560; prompts the same.)  In scope: p, m, and the number of
 // blocks and this block's index, `blocks` and `index`.
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kStateParts = !kBf16 ? 1 : kDot != 0 ? 3 : 2;  // of the state as an operand
@@ -481,9 +482,8 @@
 
     // The state after the chunk, from three parts of the weighted z (24 bits): the same
     // state whether it is a result or only on its way to the outputs, so that these do not
-    // depend on what else the caller asks for.  (Two parts where only outputs rounded to
-    // bfloat16 depend on it: packed prompts 281 us instead of 289, the long prompt 868 and
-    // 873, 4 x 2048 with 16 heads of 128 82 and 81.)
+    // depend on what else the caller asks for.  (Two parts: packed prompts 298 us instead of
+    // 309, the long prompt 895 and 927, but the last state errs by 2e-6 of its norm, not 1e-7.)
     if (it + 1 < chunks || !kOut || (last_seg && p.last)) {
       constexpr int kParts = kBf16 ? 3 : 1;
       const float all = d.all;

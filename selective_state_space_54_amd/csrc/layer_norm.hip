@@ -27,7 +27,14 @@
 // Measured: 32768 x 2560 bf16 with the residual 135 us (671 MB, 5.0 TB/s; a large
 // copy runs at 5.1 to 5.4), its gradient 146 + 6 us (4.6 TB/s); 16384 x 1536 float32
 // gradient 63 us with the sums (4.8 TB/s); 8 rows of 2560: 6 us, a launch and two
-// trips to memory, less than the host takes for the call.
+// trips to memory, less than the host takes for the call.  The forward pass is near the
+// copy's rate up to 4096 values a row (8192 x 4096 bf16 with the residual: 51 us, 5.2
+// TB/s; 60000 x 333 float32: 34 us, 4.7) and falls off where a block holds a row and loads
+// nothing ahead (4096 x 8192 bf16: 39 us, 3.4; 2048 x 16384 float32: 68 us, 4.0).  The
+// gradient is far from it away from the widths above: rows of 64 have too few blocks and
+// 16 bytes a lane in flight (65536 x 64 bf16: 24 us, 1.0 TB/s); rows of a whole block
+// load nothing ahead (8192 x 4096 bf16: 67 us, 3.0; 4096 x 8192: 79 us, 2.5); float32
+// rows of 1793 to 2048 spill (16384 x 2048 with the stream's gradient: 219 us, 2.5).
 #include "mssm_internal.h"
 #include "scan_device.h"
 

@@ -61,13 +61,16 @@
 // inside a chunk, kept as a float32 pair) and the state are 32 bits or more.
 //
 // What bounds it.  On long prompts memory, then what a wavefront issues between a
-// chunk's barriers: 1 x 131072 tokens of 20 heads of 128, bf16, moves 2.7 GB in
-// 660 us (4.1 TB/s; 256-byte rows reach 4.1 to 4.9 when only copied) with the
-// matrix cores busy 28 % of the cycles.  dq and dk also split the state in three
-// parts: 4 x 8192, 16 heads of 128: 225 and 235 us at 2.4 TB/s, matrix cores 27 %,
+// chunk's barriers: 1 x 131072 tokens of 20 heads of 128, bf16, moves 2.75 GB in
+// 715 us (3.9 TB/s; 256-byte rows reach 4.1 to 4.9 when only copied) with the
+// matrix cores busy 37 % of the cycles.  dq and dk split the state in three
+// parts: 4 x 8192, 16 heads of 128: 229 and 232 us at 3.8 TB/s, matrix cores 27 %,
 // vector instructions as long again, two blocks a compute unit for 256 registers
-// each.  float32: the 16x16x4 products, 8 x 2048, 24 heads of 64: 128 us, 55 % of
-// the matrix cores' cycles.
+// each, some spilled (20 and 28 bytes a lane).  float32: the 16x16x4 products and
+// the LDS reads between them, 40 % of whose cycles meet bank conflicts (the
+// swizzle of the tiles is made for values of two bytes): 8 x 2048, 24 heads of 64:
+// 131 us, 56 % of the matrix cores' cycles.  Its gradient passes for heads of 128
+// spill 160 to 250 bytes a lane: 4 x 2048, 16 heads: 177, 126 and 155 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -525,7 +528,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // thread sums a run of log decays, the runs are scanned, and the answer is rounded
 // up to whole runs.  (1 x 131072, 20 heads of 128, log decays of -0.02 times 1 to
 // 16 on average: the state pass reads about a third of the tokens of segments of
-// 5248 and takes 220 us; it took 326 over all of them in segments of 2624.)
+// 5248 and takes 245 us; it took 326 over all of them in segments of 2624.)
 constexpr int kReachFrom = 512;            // shorter segments are not looked over
 struct Reach {
   float sum[4];

@@ -45,7 +45,7 @@ using la::View;
 // return.  A thread owns four values of one
 // head's state; the segments' loads do not depend on each other and run kAhead
 // ahead of the chain of multiply-adds.  A gradient's two directions are one launch.
-// Bound by memory (25 segments of 20 heads of 128 x 128: 64 MB in 16 us, 4.0 TB/s).
+// Bound by memory (25 segments of 20 heads of 128 x 128: 65 MB in 15 us, 4.3 TB/s).
 struct Carry {
   const float* init;
   const float* decay;
@@ -256,15 +256,17 @@ LaPlan plan_la(const LaShape& s, bool backward, bool bf16) {
   g.L = s.packed ? 0 : (s.seqs > 0 ? s.tokens / s.seqs : 0);
   // Blocks to aim for: two on each of the 256 compute units at once, once
   // (backward) or twice over; a few blocks more than a multiple of 512 would be a
-  // round of their own (1 x 131072, 20 heads of 128: 1040 blocks take 16 %
-  // longer than 500 or 1000).  Twice over is better for short segments (packed prompts of
-  // 32768 tokens, 32 heads of 128 x 64: 289 us, once over 322), once for those of
+  // round of their own (1 x 131072, 20 heads of 128: 1040 blocks take 12 %
+  // longer than 1000).  Twice over is better for short segments (packed prompts of
+  // 32768 tokens, 32 heads of 128 x 64: 302 us, once over 342), once for those of
   // 4096 tokens and more, whose states mostly depend on a part of them (1 x 131072:
-  // 903 and 946 us).  A segment costs its state four times through memory,
+  // 940 us, twice over 1004; where they depend on all of them, log decays of -1e-4, 1061
+  // and 1079).
+  // A segment costs its state four times through memory,
   // as much as the tiles of max(dk, dv) or so tokens: below twice that only to
-  // reach 256 blocks, and never below two chunks (4 x 2048, 16 heads of 128: 82 us
-  // in segments of 256 tokens, 89 of 512, 107 of 128; 3 x 333 float32 backward, 6
-  // heads: half as long again in segments of 128 as of 64).  From 256 sequences times heads
+  // reach 256 blocks, and never below two chunks (4 x 2048, 16 heads of 128: 87 us
+  // in segments of 256 tokens, 92 of 512, 111 of 128; 3 x 333 float32 backward, 6
+  // heads: 79 us in segments of 128, 55 of 64).  From 256 sequences times heads
   // on, one segment each.
   const int64_t chunk = bf16 ? 64 : 32;
   p.paired = s.dv <= 64 && s.heads / s.key_heads % 2 == 0;
@@ -439,8 +441,8 @@ hipError_t launch_la_bwd(const LaArgs& a, const LaGrads& d, const LaPlan& plan, 
     r.paired = plan.paired;
     r.out = d.dv;
     // One launch where both fit on the chip at once (3 x 333 float32, 6 heads: the call
-    // 60 us, 85 with two); larger ones are faster apart (4 x 8192, 16 heads of 128: 367
-    // and 390 us), each with its own registers.
+    // 56 us, 65 with two); larger ones are faster apart (4 x 8192, 16 heads of 128: 738
+    // and 746 us), each with its own registers.
     if (plan.grid.slots * s.heads <= 256) {
       err = !bf16 ? la::pass_dq_dv_fp32(p, r, stream)
             : p.out_f32 ? la::pass_dq_dv_bf16_f32(p, r, stream)
