@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define MSSM_ABI_VERSION 7
+#define MSSM_ABI_VERSION 8
 
 typedef enum {
     MSSM_SUCCESS = 0,
@@ -599,6 +599,178 @@ mssm_status mssm_layer_norm_bwd(const void *dy, const void *dsum, const void *x,
                                 void *dx, float *dweight, float *dbias, void *workspace,
                                 size_t workspace_bytes, int64_t rows, int64_t D,
                                 mssm_dtype dtype, void *stream);
+
+/*
+ * ---- a gated recurrent layer: shared notions -----------------------------------------------------
+ *
+ * The three operators below make up a gated recurrent layer with its projections: the causal
+ * convolution before the recurrence, the recurrence, and the norms, gate and residual add around
+ * the block.  Tokens of all sequences lie in one row, [tokens, D] of `dtype`, sequence after
+ * sequence.  Inputs may be views into a wider projection's output: consecutive tokens are *_row
+ * elements apart (D when dense).  Outputs and gradients are dense.
+ * Sequences: with seq_offsets NULL, `seqs` sequences of `L` tokens each.  With seq_offsets (a
+ * device array of seqs + 1 int64 that does not decrease) L is the number of tokens in all and
+ * sequence i has tokens seq_offsets[i] .. seq_offsets[i + 1] - 1; it may be empty (its last state is
+ * its first).  Offsets outside 0 .. L are taken as 0 or L; tokens before the first and behind the
+ * last sequence may hold anything, and their outputs and gradients are left as they were.
+ * What is not finite in a sequence stays in that sequence and channel.  Any element-aligned
+ * address.  D below 2^28.  Sums over tokens or rows run in a fixed order, so results are
+ * deterministic.  tokens, seqs or D equal to zero are valid: last states and the parameters'
+ * gradients are still set.
+ */
+typedef enum {
+    MSSM_ACT_NONE = 0,
+    MSSM_ACT_SILU = 1
+} mssm_activation;
+
+/*
+ * ---- causal convolution with sequence states -----------------------------------------------------
+ *
+ * Depthwise, over a sequence's own tokens and the k - 1 places before its first, its state:
+ *     c_t = bias + sum_i weight[:, i] u_{t - (k - 1) + i}      y_t = SiLU(c_t), or c_t
+ * (mssm_causal_conv1d_silu is the Mamba block's prologue: the same convolution over dense batches
+ * from zero, with a float32 result.)
+ *   weight, bias      : [D, k] float32, tap k - 1 weighs the current token; [D] float32 or NULL
+ *   state, last_state : [seqs, k - 1, D] of `dtype`, the inputs at the k - 1 places before the
+ *                       sequence and at its end, oldest first; NULL: zero, not wanted.
+ *                       last_state is not state.
+ * k is 1 to 8 (MSSM_ERROR_NOT_SUPPORTED above).  Sums in float32, y rounded once.
+ *
+ * mssm_causal_conv1d_step: one token for each of `seqs` sequences, u and y [seqs, D]; the state is
+ *   read and moved on by one place.
+ * mssm_causal_conv1d_bwd: gradients of sum(dy * y) + sum(dlast * last_state).
+ *   dy, du      : [tokens, D] of `dtype`
+ *   dlast       : [seqs, k - 1, D] of `dtype`, or NULL
+ *   dweight     : [D, k] float32; dbias: [D] float32 or NULL
+ *   dstate      : gradient of the state, of `dtype`, or NULL; neither state nor dlast
+ *   The workspace (256-byte aligned) holds the blocks' partial sums.
+ */
+mssm_status mssm_causal_conv1d_fwd(const void *u, const float *weight, const float *bias,
+                                   const int64_t *seq_offsets, const void *state, void *y,
+                                   void *last_state, mssm_activation act, int64_t seqs,
+                                   int64_t L, int64_t D, int64_t k, int64_t u_row,
+                                   mssm_dtype dtype, void *stream);
+
+mssm_status mssm_causal_conv1d_step(const void *u, const float *weight, const float *bias,
+                                    void *state, void *y, mssm_activation act, int64_t seqs,
+                                    int64_t D, int64_t k, int64_t u_row, mssm_dtype dtype,
+                                    void *stream);
+
+/* `packed`: whether seq_offsets are given (then L is the number of tokens in all). */
+mssm_status mssm_causal_conv1d_bwd_workspace_size(int64_t seqs, int64_t L, int64_t D, int64_t k,
+                                                  int packed, mssm_dtype dtype, size_t *bytes);
+
+mssm_status mssm_causal_conv1d_bwd(const void *u, const float *weight, const float *bias,
+                                   const int64_t *seq_offsets, const void *state, const void *dy,
+                                   const void *dlast, void *du, float *dweight, float *dbias,
+                                   void *dstate, mssm_activation act, void *workspace,
+                                   size_t workspace_bytes, int64_t seqs, int64_t L, int64_t D,
+                                   int64_t k, int64_t u_row, mssm_dtype dtype, void *stream);
+
+/*
+ * ---- gated linear recurrence ----------------------------------------------------------------------
+ *
+ * The diagonal recurrence with one state for each channel and both of its terms gated:
+ *     a_t = exp(A sigmoid(r_t))
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+ * with the input gate i and the decay gate r before their sigmoids.
+ *   x, input_gate, decay_gate : [tokens, D] of `dtype`, rows x_row, i_row, r_row elements apart
+ *   A                 : [D] float32, <= 0 (positive rates give NaN)
+ *   h                 : [tokens, D] of `dtype`, rounded once from the float32 state
+ *   state, last_state : [seqs, D] float32, or NULL (zero, not wanted); last_state is not state
+ *   saved             : NULL, or mssm_gated_recurrence_saved_size bytes (256-byte aligned) that
+ *                       receive states for the backward call, about one in every 64 tokens'
+ * Where A sigmoid(r) > -1/4, 1 - a^2 and a keep their last place.  A decay that comes to zero in
+ * float32 over a few dozen tokens forgets the state completely.
+ *
+ * mssm_gated_recurrence_step: one token for each of `seqs` sequences, the state [seqs, D] read and
+ *   overwritten; x, gates, h [seqs, D].  No workspace.
+ * mssm_gated_recurrence_bwd: gradients of sum(dh * h) + sum(dlast * last_state), from the float32
+ *   states, which are recomputed (with `saved` as the forward call wrote it for the same inputs: from
+ *   there; NULL: from the start).
+ *   dh                             : [tokens, D] of `dtype`
+ *   dx, dinput_gate, ddecay_gate   : [tokens, D] of `dtype`
+ *   dA                             : [D] float32
+ *   dlast, dstate                  : [seqs, D] float32 or NULL; dstate is neither dlast nor state
+ *   Where a_t = 1 (A sigmoid(r) = 0) the gradient of sqrt(1 - a_t^2) is taken as zero.
+ * The workspace is 256-byte aligned and at least the size the query gives, which may be 0.
+ */
+mssm_status mssm_gated_recurrence_saved_size(int64_t seqs, int64_t L, int64_t D, int packed,
+                                             mssm_dtype dtype, size_t *bytes);
+
+/* `saved`: whether the call gets (backward) or writes (forward) saved states. */
+mssm_status mssm_gated_recurrence_workspace_size(int64_t seqs, int64_t L, int64_t D, int packed,
+                                                 int backward, int saved, mssm_dtype dtype,
+                                                 size_t *bytes);
+
+mssm_status mssm_gated_recurrence_fwd(const void *x, const void *input_gate,
+                                      const void *decay_gate, const float *A,
+                                      const int64_t *seq_offsets, const float *state, void *h,
+                                      float *last_state, float *saved, size_t saved_bytes,
+                                      void *workspace, size_t workspace_bytes, int64_t seqs,
+                                      int64_t L, int64_t D, int64_t x_row, int64_t i_row,
+                                      int64_t r_row, mssm_dtype dtype, void *stream);
+
+mssm_status mssm_gated_recurrence_step(const void *x, const void *input_gate,
+                                       const void *decay_gate, const float *A, float *state,
+                                       void *h, int64_t seqs, int64_t D, int64_t x_row,
+                                       int64_t i_row, int64_t r_row, mssm_dtype dtype,
+                                       void *stream);
+
+mssm_status mssm_gated_recurrence_bwd(const void *x, const void *input_gate,
+                                      const void *decay_gate, const float *A,
+                                      const int64_t *seq_offsets, const float *state,
+                                      const float *saved, size_t saved_bytes, const void *dh,
+                                      const float *dlast, void *dx, void *dinput_gate,
+                                      void *ddecay_gate, float *dA, float *dstate,
+                                      void *workspace, size_t workspace_bytes, int64_t seqs,
+                                      int64_t L, int64_t D, int64_t x_row, int64_t i_row,
+                                      int64_t r_row, mssm_dtype dtype, void *stream);
+
+/*
+ * ---- residual norm ----------------------------------------------------------------------------------
+ *
+ * What stands between two blocks ("Understanding Mamba", section 8.2): the norm of a block's output
+ * y, its gate, the residual scale and the residual add, and the next block's norm.  Per row of D
+ * values, with rms(v) = v / sqrt(mean(v^2) + eps):
+ *     t   = residual + scale * act(gate) * rms(y) * post_weight       rounded to `dtype`
+ *     out = rms(t) * weight
+ *   y, residual, out, total : [rows, D] of `dtype`; total receives t and may be residual or y
+ *   weight            : [D] float32
+ *   post_weight       : [D] float32, or NULL: y itself takes rms(y) * post_weight's place
+ *   gate              : [rows / gate_rows, D] of `dtype`: row r reads gate row r / gate_rows; or NULL.
+ *                       gate_rows divides rows.  gate_form MSSM_ACT_NONE: as it is.
+ *   scale             : [D] float32, or NULL
+ *   rstd, post_rstd   : [rows] float32, for the backward pass (post_rstd only with post_weight and
+ *                       rstd), or NULL
+ * D up to 16384 and rows below 2^32 (MSSM_ERROR_NOT_SUPPORTED above).  eps >= 0.
+ *
+ * mssm_residual_norm_bwd: gradients of sum(dout * out) (+ sum(dtotal * t)) from y, total (t), gate and
+ * the statistics of the forward call.
+ *   dtotal            : gradient that reaches t itself, or NULL
+ *   dy, dresidual     : [rows, D] of `dtype` (dresidual is the gradient of t)
+ *   dgate             : as gate, summed over the rows that share one; given with gate
+ *   dweight, dpost_weight, dscale : [D] float32; the latter two given with post_weight, scale
+ * The workspace holds the blocks' partial sums (256-byte aligned).
+ */
+mssm_status mssm_residual_norm_fwd(const void *y, const void *residual, const float *weight,
+                                   const float *post_weight, const void *gate, const float *scale,
+                                   void *out, void *total, float *rstd, float *post_rstd,
+                                   mssm_activation gate_form, int64_t gate_rows, float eps,
+                                   int64_t rows, int64_t D, mssm_dtype dtype, void *stream);
+
+/* gate_rows: 1 without a gate. */
+mssm_status mssm_residual_norm_bwd_workspace_size(int64_t rows, int64_t D, int64_t gate_rows,
+                                                  mssm_dtype dtype, size_t *bytes);
+
+mssm_status mssm_residual_norm_bwd(const void *dout, const void *dtotal, const void *y,
+                                   const void *total, const float *weight,
+                                   const float *post_weight, const void *gate, const float *scale,
+                                   const float *rstd, const float *post_rstd, void *dy,
+                                   void *dresidual, void *dgate, float *dweight,
+                                   float *dpost_weight, float *dscale, mssm_activation gate_form,
+                                   int64_t gate_rows, void *workspace, size_t workspace_bytes,
+                                   int64_t rows, int64_t D, mssm_dtype dtype, void *stream);
 
 #ifdef __cplusplus
 }

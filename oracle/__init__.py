@@ -34,6 +34,9 @@ Modules:
     linear_attention -- the matrix-state recurrence with a decay for each head
                   and its gradients
     layer_norm -- layer norm and its gradients
+    gated_recurrence -- the gated linear recurrence and its gradients
+    causal_conv -- the causal convolution with sequence states and its gradients
+    residual_norm -- the norms, gate and residual add around a block and their gradients
 Parity status of each function is stated in its docstring; every function is
 pinned by a ``-m "not gpu"`` test unless it says "parity unpinned".
 """
@@ -44,3 +47,6 @@ from . import block  # noqa: F401
 from . import backward  # noqa: F401
 from . import linear_attention  # noqa: F401
 from . import layer_norm  # noqa: F401
+from . import gated_recurrence  # noqa: F401
+from . import causal_conv  # noqa: F401
+from . import residual_norm  # noqa: F401

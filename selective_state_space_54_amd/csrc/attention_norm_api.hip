@@ -1,31 +1,18 @@
 // C-ABI front end of linear attention and layer norm: argument checks, which
 // all run before the first HIP call, and dispatch.
-#include <initializer_list>
-#include <limits>
-
-#include "mssm_internal.h"
+#include "api_checks.h"
 
 namespace {
+
+using mssm::bad_dtype;
+using mssm::check_workspace;
+using mssm::done;
+using mssm::kMaxBlocks;
+using mssm::product;
 
 // A token's values in any tensor: its bytes fit 24 bits, a chunk's 32, which is
 // how the kernels reach them.
 constexpr int64_t kMaxRow = int64_t(1) << 22;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;   // blocks of 256 threads
-
-bool product(std::initializer_list<int64_t> f, int64_t* out) {
-  int64_t n = 1;
-  for (int64_t v : f) {
-    if (v == 0) { *out = 0; return true; }
-  }
-  for (int64_t v : f) {
-    if (n > std::numeric_limits<int64_t>::max() / v) return false;
-    n *= v;
-  }
-  *out = n;
-  return true;
-}
-
-bool bad_dtype(mssm_dtype t) { return t != MSSM_FLOAT32 && t != MSSM_BFLOAT16; }
 
 mssm_status shape_of(int64_t seqs, int64_t L, int64_t key_heads, int64_t heads, int64_t dk,
                      int64_t dv, bool packed, mssm_dtype dtype, mssm::LaShape* s) {
@@ -76,18 +63,6 @@ mssm_status check_rows(const mssm::LaArgs& a, bool single) {
     if (!product({s.tokens, row, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   }
   return MSSM_SUCCESS;
-}
-
-mssm_status check_workspace(const void* ws, size_t have, size_t need) {
-  if (need == 0) return MSSM_SUCCESS;
-  if (!ws || have < need || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MSSM_ERROR_WORKSPACE;
-  return MSSM_SUCCESS;
-}
-
-mssm_status done(hipError_t e, const char* where) {
-  if (e == hipSuccess) return MSSM_SUCCESS;
-  mssm::set_hip_error(e, where);
-  return MSSM_ERROR_HIP;
 }
 
 }  // namespace

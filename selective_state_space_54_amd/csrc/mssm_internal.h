@@ -10,6 +10,7 @@
 
 #include "la_args.h"
 #include "mssm.h"
+#include "sequences.h"
 
 namespace mssm {
 
@@ -492,5 +493,111 @@ bool norm_size_supported(int64_t D);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_workspace(int64_t rows, int64_t D, mssm_dtype dtype);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, void* ws, hipStream_t stream);
+
+// ---- gated linear recurrence --------------------------------------------------------------------
+
+struct RecurrenceArgs {
+  Sequences seqs;
+  int64_t D = 0;
+  const void* x = nullptr;        // [tokens, D], token rows x_row elements apart
+  const void* i = nullptr;        // input gate
+  const void* r = nullptr;        // decay gate
+  int64_t x_row = 0, i_row = 0, r_row = 0;
+  const float* A = nullptr;       // [D]
+  const float* state = nullptr;   // [seqs, D] or null
+  void* h = nullptr;              // [tokens, D]
+  float* last = nullptr;          // [seqs, D] or null
+  float* saved = nullptr;         // the state before each tile [tiles, D], or null
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+struct RecurrenceGrads {
+  const void* dh = nullptr;       // [tokens, D]
+  const float* dlast = nullptr;   // [seqs, D] or null
+  void* dx = nullptr;
+  void* di = nullptr;
+  void* dr = nullptr;
+  float* dA = nullptr;            // [D]
+  float* dstate = nullptr;        // [seqs, D] or null
+};
+// Tiles of tokens by groups of channels, and the workspace.
+struct RecurrencePlan {
+  int64_t tiles = 0, groups = 0;
+  size_t agg = 0, states = 0, rcarry = 0, part = 0;
+  size_t saved_bytes = 0;
+  size_t bytes = 0;
+};
+// saved: the backward call gets the states that the forward call saved (forward: stores them).
+RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool saved,
+                               mssm_dtype dtype);
+hipError_t launch_recurrence(const RecurrenceArgs& a, const RecurrencePlan& p, void* ws,
+                             hipStream_t stream);
+hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads& d,
+                                 const RecurrencePlan& p, void* ws, hipStream_t stream);
+// One token for each sequence, the state in place.
+hipError_t launch_recurrence_step(const RecurrenceArgs& a, float* state, hipStream_t stream);
+
+// ---- causal convolution --------------------------------------------------------------------------
+
+struct ConvArgs {
+  Sequences seqs;
+  int64_t D = 0, k = 0;
+  const void* u = nullptr;        // [tokens, D], token rows u_row elements apart
+  int64_t u_row = 0;
+  const float* weight = nullptr;  // [D, k]
+  const float* bias = nullptr;    // [D] or null
+  bool silu = false;
+  const void* state = nullptr;    // [seqs, k - 1, D] or null
+  void* y = nullptr;              // [tokens, D]
+  void* last = nullptr;           // [seqs, k - 1, D] or null
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+struct ConvGrads {
+  const void* dy = nullptr;       // [tokens, D]
+  const void* dlast = nullptr;    // [seqs, k - 1, D] or null
+  void* du = nullptr;
+  float* dweight = nullptr;       // [D, k]
+  float* dbias = nullptr;         // [D] or null
+  void* dstate = nullptr;         // [seqs, k - 1, D] or null
+};
+size_t conv_bwd_workspace(int64_t tokens, int64_t D, int64_t k, mssm_dtype dtype);
+int64_t conv_blocks(int64_t tokens, int64_t D, bool backward, mssm_dtype dtype);
+hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv_bwd(const ConvArgs& a, const ConvGrads& d, void* ws, hipStream_t stream);
+hipError_t launch_conv_step(const ConvArgs& a, void* state, hipStream_t stream);
+
+// ---- residual norm --------------------------------------------------------------------------------
+
+struct ResidualNormArgs {
+  const void* y = nullptr;          // [rows, D]
+  const void* residual = nullptr;   // [rows, D]
+  const float* weight = nullptr;    // [D]
+  const float* post_weight = nullptr;  // [D] or null
+  const void* gate = nullptr;       // [rows / gate_rows, D] or null
+  int64_t gate_rows = 1;            // rows that share a gate row
+  bool silu = false;                // the gate's form
+  const float* scale = nullptr;     // [D] or null
+  void* out = nullptr;
+  void* total = nullptr;
+  float* rstd = nullptr;            // [rows] or null
+  float* post_rstd = nullptr;       // [rows] or null
+  float eps = 0.0f;
+  int64_t rows = 0, D = 0;
+  mssm_dtype dtype = MSSM_FLOAT32;
+};
+struct ResidualNormGrads {
+  const void* dout = nullptr;       // [rows, D]
+  const void* dtotal = nullptr;     // [rows, D] or null
+  void* dy = nullptr;
+  void* dresidual = nullptr;
+  void* dgate = nullptr;            // as gate
+  float* dweight = nullptr;         // [D]
+  float* dpost_weight = nullptr;    // [D], with post_weight
+  float* dscale = nullptr;          // [D], with scale
+};
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream);
+// In a backward call total, rstd and post_rstd are inputs.
+size_t residual_norm_bwd_workspace(int64_t rows, int64_t D, int64_t gate_rows, mssm_dtype dtype);
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const ResidualNormGrads& d, void* ws,
+                                    hipStream_t stream);
 
 }  // namespace mssm

@@ -31,6 +31,8 @@ MSSM_BBAR_ZOH = 1
 _BBAR = {"euler": MSSM_BBAR_EULER, "zoh": MSSM_BBAR_ZOH}
 MSSM_DECAY_PER_HEAD = 0
 MSSM_DECAY_PER_TOKEN = 1
+MSSM_ACT_NONE = 0
+MSSM_ACT_SILU = 1
 MSSM_TUNE_SCAN_ORDER = 0
 MSSM_TUNE_CHUNK_LEN = 1
 MSSM_TUNE_CHAINS_PER_LANE = 2
@@ -113,6 +115,31 @@ _SIGNATURES = {
                                                           ctypes.POINTER(ctypes.c_size_t)]),
     "mssm_layer_norm_bwd": (ctypes.c_int, [_vp] * 10 + [ctypes.c_size_t, _i64, _i64, ctypes.c_int,
                                                         _vp]),
+    "mssm_causal_conv1d_fwd": (ctypes.c_int, [_vp] * 7 + [ctypes.c_int] + [_i64] * 5 +
+                               [ctypes.c_int, _vp]),
+    "mssm_causal_conv1d_step": (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] + [_i64] * 4 +
+                                [ctypes.c_int, _vp]),
+    "mssm_causal_conv1d_bwd_workspace_size": (ctypes.c_int, [_i64] * 4 + [ctypes.c_int] * 2 +
+                                              [ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_causal_conv1d_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_int, _vp, ctypes.c_size_t] +
+                               [_i64] * 5 + [ctypes.c_int, _vp]),
+    "mssm_gated_recurrence_saved_size": (ctypes.c_int, [_i64] * 3 + [ctypes.c_int] * 2 +
+                                         [ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_gated_recurrence_workspace_size": (ctypes.c_int, [_i64] * 3 + [ctypes.c_int] * 4 +
+                                             [ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_gated_recurrence_fwd": (ctypes.c_int, [_vp] * 9 + [ctypes.c_size_t, _vp,
+                                                             ctypes.c_size_t] + [_i64] * 6 +
+                                  [ctypes.c_int, _vp]),
+    "mssm_gated_recurrence_step": (ctypes.c_int, [_vp] * 6 + [_i64] * 5 + [ctypes.c_int, _vp]),
+    "mssm_gated_recurrence_bwd": (ctypes.c_int, [_vp] * 7 + [ctypes.c_size_t] + [_vp] * 8 +
+                                  [ctypes.c_size_t] + [_i64] * 6 + [ctypes.c_int, _vp]),
+    "mssm_residual_norm_fwd": (ctypes.c_int, [_vp] * 10 + [ctypes.c_int, _i64, ctypes.c_float,
+                                                           _i64, _i64, ctypes.c_int, _vp]),
+    "mssm_residual_norm_bwd_workspace_size": (ctypes.c_int, [_i64] * 3 + [
+        ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "mssm_residual_norm_bwd": (ctypes.c_int, [_vp] * 16 + [ctypes.c_int, _i64, _vp,
+                                                           ctypes.c_size_t, _i64, _i64,
+                                                           ctypes.c_int, _vp]),
 }
 
 
@@ -1088,3 +1115,470 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, dsum=None, bias=True, stream=No
     mssm_layer_norm_bwd(dy, x, weight, mean, rstd, grads["dx"], grads["dweight"],
                         grads.get("dbias"), ws, dsum=dsum, stream=stream)
     return grads
+
+
+# ---- a gated recurrent layer: causal convolution, gated recurrence, residual norm -----------------
+
+def _channel_rows(t, name, dtype, shape, dev):
+    """Checks a [tokens.., D] tensor whose tokens are evenly spaced (a slice of a wider
+    projection's output is one) and returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _dense(t, name, dtype, shape, torch.device("cuda", dev))
+    D = shape[-1]
+    if t.is_contiguous():
+        return D
+    st = t.stride()
+    lead = [i for i in range(len(shape) - 1) if shape[i] > 1]   # strides of single entries say nothing
+    row = st[lead[-1]] if lead else D
+    even = len(lead) < 2 or st[0] == shape[1] * row
+    if (D > 1 and st[-1] != 1) or row < D or not even:
+        raise ValueError(f"{name} must hold its channels densely, at an even token stride")
+    return row
+
+
+def _sequences(t, name, seq_offsets, single=False):
+    """Of a [batch, L, D], packed [tokens, D] or (``single``) [batch, D] tensor: the GPU, and the
+    sizes seqs, L and D that the C calls take."""
+    dev = _gpu_of(t, name)
+    shape = t.shape
+    dims = 2 if single or seq_offsets is not None else 3
+    if len(shape) != dims:
+        raise ValueError(f"{name} must be [{'batch, L' if dims == 3 else 'batch' if single else 'tokens'}, D]")
+    if seq_offsets is not None:
+        _expect_tensor(seq_offsets, "seq_offsets")
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+            raise ValueError("seq_offsets must be [sequences + 1]")
+        _expect(seq_offsets, "seq_offsets", torch.int64, seq_offsets.shape, dev)
+        return dev, (seq_offsets.shape[0] - 1, shape[0], shape[1])
+    return dev, (shape[0], 1, shape[1]) if single else tuple(shape)
+
+
+def _size_query(name, *args):
+    out = ctypes.c_size_t(0)
+    _check(getattr(load(), name)(*args, ctypes.byref(out)), name)
+    return out.value
+
+
+_size_of = functools.lru_cache(maxsize=1024)(_size_query)
+
+
+def _expect_grads(grads, shapes, dev):
+    """Checks a dict of gradients; returns their addresses by name."""
+    for name, t in grads.items():
+        if name not in shapes:
+            raise ValueError(f"unknown gradient {name}")
+        _expect(t, name, *shapes[name], dev)
+    return lambda name: _address(grads.get(name))
+
+
+_ACTIVATIONS = {None: MSSM_ACT_NONE, "silu": MSSM_ACT_SILU}
+
+
+def _activation(name):
+    if name not in _ACTIVATIONS:
+        raise ValueError('activation must be "silu" or None')
+    return _ACTIVATIONS[name]
+
+
+def _conv_check(u, weight, bias, seq_offsets, single=False):
+    dev, (seqs, L, D) = _sequences(u, "u", seq_offsets, single)
+    row = _channel_rows(u, "u", u.dtype, u.shape, dev)
+    _expect_tensor(weight, "weight")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D, taps]")
+    k = weight.shape[1]
+    _expect(weight, "weight", torch.float32, (D, k), dev)
+    _expect_optional(bias, "bias", torch.float32, (D,), dev)
+    return dev, (seqs, L, D, k), row
+
+
+def mssm_causal_conv1d_fwd(u, weight, bias, y, *, activation="silu", state=None, last_state=None,
+                           seq_offsets=None, stream=None):
+    """y (and last_state) <- causal convolution (see causal_conv1d)."""
+    dev, (seqs, L, D, k), row = _conv_check(u, weight, bias, seq_offsets)
+    act = _activation(activation)
+    _expect(y, "y", u.dtype, u.shape, dev)
+    _expect_optional(state, "state", u.dtype, (seqs, k - 1, D), dev)
+    _expect_optional(last_state, "last_state", u.dtype, (seqs, k - 1, D), dev)
+    _call("mssm_causal_conv1d_fwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
+          _address(seq_offsets), _address(state), y.data_ptr(), _address(last_state), act, seqs, L,
+          D, k, row, _DTYPES[u.dtype])
+    return y
+
+
+def causal_conv1d(u, weight, bias=None, *, activation="silu", state=None, seq_offsets=None,
+                  return_state=False, stream=None):
+    """Causal depthwise convolution over whole sequences, c_t = bias + sum_i weight[:, i]
+    u_{t - (k - 1) + i}, and SiLU of it (``activation`` None: c itself).
+
+    u [batch, L, D], or with ``seq_offsets`` (int64 [sequences + 1] on the GPU) packed sequences
+    [tokens, D]; float32 or bfloat16; views whose tokens are evenly spaced are taken as they are.
+    weight [D, k] (k up to 8), bias [D] float32.  ``state`` [sequences, k - 1, D] of u's dtype holds
+    the inputs before the first token (default zero).  Tokens that no sequence holds are not
+    written.  Returns y of u's dtype, or (y, last state)."""
+    dev, (seqs, L, D, k), row = _conv_check(u, weight, bias, seq_offsets)
+    act = _activation(activation)
+    dt = u.dtype
+    _expect_optional(state, "state", dt, (seqs, k - 1, D), dev)
+    with _on(stream):
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+        last = torch.empty((seqs, k - 1, D), dtype=dt, device=dev) if return_state else None
+    _call("mssm_causal_conv1d_fwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
+          _address(seq_offsets), _address(state), y.data_ptr(), _address(last), act, seqs, L, D, k,
+          row, _DTYPES[dt])
+    return (y, last) if return_state else y
+
+
+def mssm_causal_conv1d_step(u, weight, bias, state, y, *, activation="silu", stream=None):
+    """One token for each sequence: u, y [batch, D]; state [batch, k - 1, D] moves on by one
+    place."""
+    dev, (seqs, _, D, k), row = _conv_check(u, weight, bias, None, True)
+    act = _activation(activation)
+    _expect(state, "state", u.dtype, (seqs, k - 1, D), dev)
+    _expect(y, "y", u.dtype, (seqs, D), dev)
+    _call("mssm_causal_conv1d_step", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
+          state.data_ptr(), y.data_ptr(), act, seqs, D, k, row, _DTYPES[u.dtype])
+    return y
+
+
+def causal_conv1d_step(u, weight, bias, state, *, activation="silu", stream=None):
+    """Allocate y, run mssm_causal_conv1d_step (state updated in place), return y."""
+    with _on(stream):
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+    return mssm_causal_conv1d_step(u, weight, bias, state, y, activation=activation, stream=stream)
+
+
+def mssm_causal_conv1d_bwd_workspace_size(seqs, L, D, k, dtype, *, packed=False) -> int:
+    return _size_query("mssm_causal_conv1d_bwd_workspace_size", seqs, L, D, k, int(packed),
+                       _dtype_code(dtype))
+
+
+def mssm_causal_conv1d_bwd(u, weight, bias, dy, grads, workspace, *, activation="silu", state=None,
+                           dstate=None, seq_offsets=None, stream=None):
+    """Gradients of sum(dy * y) + sum(dstate * last state) of causal_conv1d.  ``grads`` maps du,
+    dweight and, where wanted, dbias and dstate (the initial state's) to dense tensors that are
+    overwritten."""
+    dev, (seqs, L, D, k), row = _conv_check(u, weight, bias, seq_offsets)
+    act = _activation(activation)
+    states = (u.dtype, (seqs, k - 1, D))
+    _expect(dy, "dy", u.dtype, u.shape, dev)
+    _expect_optional(state, "state", *states, dev)
+    _expect_optional(dstate, "dstate", *states, dev)
+    g = _expect_grads(grads, {"du": (u.dtype, u.shape), "dweight": (torch.float32, (D, k)),
+                              "dbias": (torch.float32, (D,)), "dstate": states}, dev)
+    _call("mssm_causal_conv1d_bwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
+          _address(seq_offsets), _address(state), dy.data_ptr(), _address(dstate), g("du"),
+          g("dweight"), g("dbias"), g("dstate"), act, *_workspace_args(workspace, u.device), seqs,
+          L, D, k, row, _DTYPES[u.dtype])
+    return grads
+
+
+def causal_conv1d_bwd(u, weight, bias, dy, *, activation="silu", state=None, dstate=None,
+                      seq_offsets=None, stream=None):
+    """Allocate the gradients and the workspace with torch, then run mssm_causal_conv1d_bwd;
+    returns the dict of gradients: du, dweight, dbias where there is a bias, and dstate, the initial
+    state's, where ``state`` is given.  ``dstate`` is the gradient of the last state, if it has
+    one."""
+    dev, (seqs, L, D, k), _ = _conv_check(u, weight, bias, seq_offsets)
+    nbytes = _size_of("mssm_causal_conv1d_bwd_workspace_size", seqs, L, D, k,
+                      int(seq_offsets is not None), _DTYPES[u.dtype])
+    with _on(stream):
+        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
+        grads = {"du": empty(u), "dweight": empty(weight)}
+        if bias is not None:
+            grads["dbias"] = empty(bias)
+        if state is not None:
+            _expect_tensor(state, "state")
+            grads["dstate"] = empty(state)
+        ws = _workspace(nbytes, dev)
+    return mssm_causal_conv1d_bwd(u, weight, bias, dy, grads, ws, activation=activation,
+                                  state=state, dstate=dstate, seq_offsets=seq_offsets,
+                                  stream=stream)
+
+
+def _recurrence_check(x, input_gate, decay_gate, A, seq_offsets, single=False):
+    """The GPU, the sizes (seqs, L, D) and what the C calls take at their end."""
+    dev, sizes = _sequences(x, "x", seq_offsets, single)
+    dt, shape = x.dtype, x.shape
+    rows = (_channel_rows(x, "x", dt, shape, dev),
+            _channel_rows(input_gate, "input_gate", dt, shape, dev),
+            _channel_rows(decay_gate, "decay_gate", dt, shape, dev))
+    _expect(A, "A", torch.float32, (sizes[2],), dev)
+    return dev, sizes, rows + (_DTYPES[dt],)
+
+
+def mssm_gated_recurrence_saved_size(seqs, L, D, dtype, *, packed=False) -> int:
+    """Bytes of the states that a forward call saves for its backward call."""
+    return _size_query("mssm_gated_recurrence_saved_size", seqs, L, D, int(packed),
+                       _dtype_code(dtype))
+
+
+def mssm_gated_recurrence_workspace_size(seqs, L, D, dtype, *, packed=False, backward=False,
+                                         saved=False) -> int:
+    return _size_query("mssm_gated_recurrence_workspace_size", seqs, L, D, int(packed),
+                       int(backward), int(saved), _dtype_code(dtype))
+
+
+def _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last, saved,
+                    workspace, stream):
+    dev, sizes, tail = checked
+    _call("mssm_gated_recurrence_fwd", dev, stream, x.data_ptr(), input_gate.data_ptr(),
+          decay_gate.data_ptr(), A.data_ptr(), _address(seq_offsets), _address(state),
+          h.data_ptr(), _address(last), *_workspace_args(saved, x.device),
+          *_workspace_args(workspace, x.device), *sizes, *tail)
+
+
+def mssm_gated_recurrence_fwd(x, input_gate, decay_gate, A, h, workspace, *, state=None,
+                              last_state=None, saved=None, seq_offsets=None, stream=None):
+    """h (and last_state, saved) <- gated linear recurrence (see gated_recurrence); workspace is a
+    uint8 GPU tensor of mssm_gated_recurrence_workspace_size bytes, or None where that is 0."""
+    checked = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    dev, (seqs, _, D), _ = checked
+    _expect(h, "h", x.dtype, x.shape, dev)
+    _expect_optional(state, "state", torch.float32, (seqs, D), dev)
+    _expect_optional(last_state, "last_state", torch.float32, (seqs, D), dev)
+    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last_state, saved,
+                    workspace, stream)
+    return h
+
+
+def gated_recurrence(x, input_gate, decay_gate, A, *, state=None, seq_offsets=None,
+                     return_state=False, return_saved=False, stream=None):
+    """Gated linear recurrence over whole sequences: a_t = exp(A sigmoid(decay_gate_t)),
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t.
+
+    x and the gates (before their sigmoids) [batch, L, D], or with ``seq_offsets`` (int64
+    [sequences + 1] on the GPU) packed sequences [tokens, D]; float32 or bfloat16; views whose
+    tokens are evenly spaced (slices of a fused projection) are taken as they are.  A float32 [D],
+    at most zero.  ``state`` float32 [sequences, D] is the state before the first token (default
+    zero).  Tokens that no sequence holds are not written.  Returns h of x's dtype, or (h[, last
+    state][, saved]); ``saved`` spares gated_recurrence_bwd a pass over the inputs."""
+    checked = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    dev, sizes, tail = checked
+    seqs, _, D = sizes
+    packed = int(seq_offsets is not None)
+    _expect_optional(state, "state", torch.float32, (seqs, D), dev)
+    nbytes = _size_of("mssm_gated_recurrence_workspace_size", *sizes, packed, 0, int(return_saved),
+                      tail[3])
+    with _on(stream):
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        last = torch.empty((seqs, D), dtype=torch.float32, device=dev) if return_state else None
+        saved = None
+        if return_saved:
+            size = _size_of("mssm_gated_recurrence_saved_size", *sizes, packed, tail[3])
+            saved = torch.empty(size, dtype=torch.uint8, device=dev)
+        ws = _workspace(nbytes, dev)
+    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last, saved, ws,
+                    stream)
+    if not return_state and not return_saved:
+        return h
+    return (h,) + ((last,) if return_state else ()) + ((saved,) if return_saved else ())
+
+
+def _recurrence_step(checked, x, input_gate, decay_gate, A, state, h, stream):
+    dev, (seqs, _, D), tail = checked
+    _expect(state, "state", torch.float32, (seqs, D), dev)
+    _call("mssm_gated_recurrence_step", dev, stream, x.data_ptr(), input_gate.data_ptr(),
+          decay_gate.data_ptr(), A.data_ptr(), state.data_ptr(), h.data_ptr(), seqs, D, *tail)
+    return h
+
+
+def mssm_gated_recurrence_step(x, input_gate, decay_gate, A, state, h, *, stream=None):
+    """One token for each sequence: x, gates, h [batch, D]; state [batch, D] float32 is updated in
+    place."""
+    checked = _recurrence_check(x, input_gate, decay_gate, A, None, True)
+    _expect(h, "h", x.dtype, x.shape, checked[0])
+    return _recurrence_step(checked, x, input_gate, decay_gate, A, state, h, stream)
+
+
+def gated_recurrence_step(x, input_gate, decay_gate, A, state, *, stream=None):
+    """Allocate h, run mssm_gated_recurrence_step (state updated in place), return h."""
+    checked = _recurrence_check(x, input_gate, decay_gate, A, None, True)
+    with _on(stream):
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _recurrence_step(checked, x, input_gate, decay_gate, A, state, h, stream)
+
+
+def mssm_gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, grads, workspace, *, saved=None,
+                              state=None, dstate=None, seq_offsets=None, stream=None):
+    """Gradients of sum(dh * h) + sum(dstate * last state) of gated_recurrence.  ``grads`` maps dx,
+    dinput_gate, ddecay_gate (of x's dtype), dA (float32) and, where wanted, dstate (the initial
+    state's) to dense tensors that are overwritten.  The workspace is that of a call with or without
+    ``saved``."""
+    dev, sizes, tail = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    seqs, _, D = sizes
+    dt, shape = x.dtype, x.shape
+    states = (torch.float32, (seqs, D))
+    _expect(dh, "dh", dt, shape, dev)
+    _expect_optional(state, "state", *states, dev)
+    _expect_optional(dstate, "dstate", *states, dev)
+    g = _expect_grads(grads, {"dx": (dt, shape), "dinput_gate": (dt, shape),
+                              "ddecay_gate": (dt, shape), "dA": (torch.float32, (D,)),
+                              "dstate": states}, dev)
+    _call("mssm_gated_recurrence_bwd", dev, stream, x.data_ptr(), input_gate.data_ptr(),
+          decay_gate.data_ptr(), A.data_ptr(), _address(seq_offsets), _address(state),
+          *_workspace_args(saved, x.device), dh.data_ptr(), _address(dstate), g("dx"),
+          g("dinput_gate"), g("ddecay_gate"), g("dA"), g("dstate"),
+          *_workspace_args(workspace, x.device), *sizes, *tail)
+    return grads
+
+
+def gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, *, saved=None, state=None, dstate=None,
+                         seq_offsets=None, stream=None):
+    """Allocate the gradients and the workspace with torch, then run mssm_gated_recurrence_bwd;
+    returns the dict of gradients: dx, dinput_gate, ddecay_gate, dA, and dstate, the initial
+    state's, where ``state`` is given.  ``saved``: what gated_recurrence returned for the same
+    inputs; ``dstate``: the gradient of the last state, if it has one."""
+    dev, sizes, tail = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    nbytes = _size_of("mssm_gated_recurrence_workspace_size", *sizes, int(seq_offsets is not None),
+                      1, int(saved is not None), tail[3])
+    with _on(stream):
+        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
+        grads = {"dx": empty(x), "dinput_gate": empty(x), "ddecay_gate": empty(x), "dA": empty(A)}
+        if state is not None:
+            _expect_tensor(state, "state")
+            grads["dstate"] = empty(state)
+        ws = _workspace(nbytes, dev)
+    return mssm_gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, grads, ws, saved=saved,
+                                     state=state, dstate=dstate, seq_offsets=seq_offsets,
+                                     stream=stream)
+
+
+_GATE_FORMS = {"silu": MSSM_ACT_SILU, "linear": MSSM_ACT_NONE}
+
+
+def _gate_rows(gate, form, y, rows, dev):
+    """The C calls' gate form and the rows that share one gate row."""
+    if form not in _GATE_FORMS:
+        raise ValueError('gate_form must be "silu" or "linear"')
+    form = _GATE_FORMS[form]
+    if gate is None:
+        return form, 1
+    _expect_tensor(gate, "gate")
+    shape, D = y.shape, y.shape[-1]
+    if gate.shape == shape:
+        _expect(gate, "gate", y.dtype, shape, dev)
+        return form, 1
+    groups = gate.shape[0] if gate.dim() == 2 else -1
+    _expect(gate, "gate", y.dtype, (max(groups, 0), D), dev)
+    starts, n = [], 1                  # rows of the leading dimensions: what a gate can stand for
+    for size in shape[:-1]:
+        starts.append(n)
+        n *= size
+    if groups < 1 or (rows % groups if len(shape) == 2 else groups not in starts):
+        raise ValueError("gate must have y's shape, or be [groups, D] with as many rows as y's "
+                         "leading dimensions (a divisor of y's rows where y is [rows, D])")
+    return form, max(rows // groups, 1)
+
+
+def _residual_norm_check(y, weight, post_weight, gate, gate_form, scale):
+    dev, rows, D = _norm_rows(y, weight)
+    _expect_optional(post_weight, "post_weight", torch.float32, (D,), dev)
+    _expect_optional(scale, "scale", torch.float32, (D,), dev)
+    return dev, rows, D, *_gate_rows(gate, gate_form, y, rows, dev)
+
+
+def mssm_residual_norm_fwd(y, residual, weight, out, total, *, post_weight=None, gate=None,
+                           gate_form="silu", scale=None, rstd=None, post_rstd=None, eps=1e-5,
+                           stream=None):
+    """out, total (and rstd, post_rstd) <- residual norm (see residual_norm); total may be residual
+    or y."""
+    dev, rows, D, form, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form,
+                                                         scale)
+    dt, shape = y.dtype, y.shape
+    _expect(residual, "residual", dt, shape, dev)
+    _expect(out, "out", dt, shape, dev)
+    _expect(total, "total", dt, shape, dev)
+    _expect_optional(rstd, "rstd", torch.float32, shape[:-1], dev)
+    _expect_optional(post_rstd, "post_rstd", torch.float32, shape[:-1], dev)
+    _call("mssm_residual_norm_fwd", dev, stream, y.data_ptr(), residual.data_ptr(),
+          weight.data_ptr(), _address(post_weight), _address(gate), _address(scale),
+          out.data_ptr(), total.data_ptr(), _address(rstd), _address(post_rstd), form, gate_rows,
+          eps, rows, D, _DTYPES[dt])
+    return out
+
+
+def residual_norm(y, residual, weight, *, post_weight=None, gate=None, gate_form="silu",
+                  scale=None, eps=1e-5, return_stats=False, stream=None):
+    """What stands between two blocks, over the last dimension: total = residual + scale *
+    act(gate) * rms_norm(y) * post_weight (rounded to y's dtype), out = rms_norm(total) * weight.
+
+    y, residual [.., D] float32 or bfloat16, dense; weight, post_weight, scale float32 [D]; without
+    post_weight y is not normalised.  gate, of y's dtype and shape, or [groups, D] where rows / groups
+    rows in a row share one; ``gate_form`` "silu" or "linear" (as it is).  Returns (out, total), with
+    ``return_stats`` (out, total, rstd[, post_rstd]) for residual_norm_bwd."""
+    dev, rows, D, form, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form,
+                                                         scale)
+    dt, shape = y.dtype, y.shape
+    _expect(residual, "residual", dt, shape, dev)
+    rstd = post_rstd = None
+    with _on(stream):
+        out, total = torch.empty_like(y), torch.empty_like(y)
+        if return_stats:
+            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            post_rstd = torch.empty_like(rstd) if post_weight is not None else None
+    _call("mssm_residual_norm_fwd", dev, stream, y.data_ptr(), residual.data_ptr(),
+          weight.data_ptr(), _address(post_weight), _address(gate), _address(scale),
+          out.data_ptr(), total.data_ptr(), _address(rstd), _address(post_rstd), form, gate_rows,
+          eps, rows, D, _DTYPES[dt])
+    stats = (rstd,) + ((post_rstd,) if post_rstd is not None else ())
+    return (out, total) + (stats if return_stats else ())
+
+
+def mssm_residual_norm_bwd_workspace_size(rows, D, dtype, *, gate_rows=1) -> int:
+    return _size_query("mssm_residual_norm_bwd_workspace_size", rows, D, gate_rows,
+                       _dtype_code(dtype))
+
+
+def mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, workspace, *, dtotal=None,
+                           post_weight=None, post_rstd=None, gate=None, gate_form="silu",
+                           scale=None, stream=None):
+    """Gradients of sum(dout * out) (+ sum(dtotal * total)) of residual_norm.  ``grads`` maps dy,
+    dresidual, dweight and, with post_weight, gate and scale, dpost_weight, dgate and dscale to
+    dense tensors that are overwritten."""
+    dev, rows, D, form, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form,
+                                                         scale)
+    dt, shape = y.dtype, y.shape
+    _expect(dout, "dout", dt, shape, dev)
+    _expect(total, "total", dt, shape, dev)
+    _expect(rstd, "rstd", torch.float32, shape[:-1], dev)
+    _expect_optional(dtotal, "dtotal", dt, shape, dev)
+    if post_weight is not None:
+        _expect(post_rstd, "post_rstd", torch.float32, shape[:-1], dev)
+    shapes = {"dy": (dt, shape), "dresidual": (dt, shape), "dweight": (torch.float32, (D,))}
+    if post_weight is not None:
+        shapes["dpost_weight"] = (torch.float32, (D,))
+    if gate is not None:
+        shapes["dgate"] = (dt, gate.shape)
+    if scale is not None:
+        shapes["dscale"] = (torch.float32, (D,))
+    g = _expect_grads(grads, shapes, dev)
+    _call("mssm_residual_norm_bwd", dev, stream, dout.data_ptr(), _address(dtotal), y.data_ptr(),
+          total.data_ptr(), weight.data_ptr(), _address(post_weight), _address(gate),
+          _address(scale), rstd.data_ptr(),
+          _address(post_rstd) if post_weight is not None else None, g("dy"), g("dresidual"),
+          g("dgate"), g("dweight"), g("dpost_weight"), g("dscale"), form, gate_rows,
+          *_workspace_args(workspace, y.device), rows, D, _DTYPES[dt])
+    return grads
+
+
+def residual_norm_bwd(dout, y, total, weight, rstd, *, dtotal=None, post_weight=None,
+                      post_rstd=None, gate=None, gate_form="silu", scale=None, stream=None):
+    """Allocate the gradients and the workspace with torch, then run mssm_residual_norm_bwd; returns
+    the dict of gradients: dy, dresidual, dweight, and dpost_weight, dgate, dscale for what is
+    given.  total, rstd and post_rstd are what residual_norm returned; ``dtotal`` is the gradient
+    that reaches total itself."""
+    dev, rows, D, _, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form, scale)
+    nbytes = _size_of("mssm_residual_norm_bwd_workspace_size", rows, D, gate_rows, _DTYPES[y.dtype])
+    with _on(stream):
+        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
+        grads = {"dy": empty(y), "dresidual": empty(y), "dweight": empty(weight)}
+        for name, t in (("dpost_weight", post_weight), ("dgate", gate), ("dscale", scale)):
+            if t is not None:
+                grads[name] = empty(t)
+        ws = _workspace(nbytes, dev)
+    return mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, ws, dtotal=dtotal,
+                                  post_weight=post_weight, post_rstd=post_rstd, gate=gate,
+                                  gate_form=gate_form, scale=scale, stream=stream)
