@@ -313,6 +313,8 @@ mssm_status mssm_residual_norm_fwd(const void* y, const void* residual, const fl
   if (rows == 0 || D == 0) return MSSM_SUCCESS;
   if (!y || !residual || !weight || !out || !total) return MSSM_ERROR_INVALID_VALUE;
   if (post_rstd && (!rstd || !post_weight)) return MSSM_ERROR_INVALID_VALUE;
+  for (const void* in : {y, residual, gate})
+    if (in && (in == total || in == out)) return MSSM_ERROR_INVALID_VALUE;
   mssm::ResidualNormArgs a;
   a.y = y, a.residual = residual, a.weight = weight, a.post_weight = post_weight;
   a.gate = gate, a.gate_rows = gate ? gate_rows : 1, a.silu = gate_form == MSSM_ACT_SILU;
@@ -349,6 +351,8 @@ mssm_status mssm_residual_norm_bwd(const void* dout, const void* dtotal, const v
     if (!dout || !y || !total || !weight || !rstd || !dy || !dresidual ||
         !post_weight != !post_rstd || !gate != !dgate)
       return MSSM_ERROR_INVALID_VALUE;
+    for (const void* in : {dout, dtotal, y, total, gate})
+      if (in && (in == dy || in == dresidual || in == dgate)) return MSSM_ERROR_INVALID_VALUE;
     st = check_workspace(workspace, workspace_bytes,
                          mssm::residual_norm_bwd_workspace(rows, D, gate_rows, dtype));
     if (st != MSSM_SUCCESS) return st;

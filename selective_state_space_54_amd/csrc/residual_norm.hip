@@ -6,15 +6,24 @@
 // Backwards, the means taken over the row and q = c pw yhat:
 //   d   = dt + rstd (w dout - that mean(w dout that))          the gradient of t, and of residual
 //   dy  = post (d c pw - yhat mean(d q))
-//   dz  = d yhat pw scale act'(z),     dw = sum dout that,   dpw = sum d c yhat,
-//   dscale = sum d yhat pw act(z)      (sums over rows; dz over the rows that share a gate)
+//   dz  = d yhat pw scale act'(z),     dw = sum dout that
+//   dpw = scale S,  dscale = pw S,     S = sum d act(z) yhat
+// (sums over rows; dz over the rows that share a gate)
 // mean(d q) follows from sums that need no d: with S2 = sum (dt + rstd w dout) q and
 // S3 = sum that q it is (S2 - rstd mean(w dout that) S3) / D, so a row meets one
 // reduction.
 //
-// Bound by memory.  A thread holds 16-byte pieces of the same columns of every row it meets, and the
-// parameters and the column sums of those columns in registers.  Short rows take a part of
-// a wavefront, others as many wavefronts as they have pieces.
+// Bound by memory.  A thread holds 16-byte pieces of the same columns of every row it meets, and
+// the column sums of those columns in registers.  Short rows take a part of a wavefront, others as
+// many wavefronts as they have pieces.
+//
+// There is no branch around a load or a store (one would have every wait for a load also wait
+// for the stores before it): the last piece of a row whose end is not a piece's is the row's last
+// N values, threads past the end repeat it, and rows past the last one repeat the last one.
+// All of those compute the same values again and write them to the same place; only the sums leave
+// them out.  So outputs must not be inputs.
+#include <type_traits>
+
 #include "mssm_internal.h"
 #include "norm_device.h"
 
@@ -23,53 +32,87 @@ namespace mssm {
 namespace {
 
 constexpr int kMaxWaves = 16;
+constexpr int kMinWaves = 4;              // wavefronts a SIMD: at most 128 registers
 
-template <typename T>
-__device__ __forceinline__ uint4 load_piece(const T* row, int c, int D) {
-  constexpr int N = kPer<T>;
-  uint4 u;
-  if (D >= N) {
-    __builtin_memcpy(&u, row + (c < D - N ? c : D - N), 16);
-  } else {
-    T e[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) e[j] = row[j < D ? j : D - 1];
-    __builtin_memcpy(&u, e, 16);
+// Rows of up to 512 pieces: two fit a thread's registers.
+template <int VPT, int kThreads>
+constexpr bool kLoadsAhead = VPT == 1 && kThreads <= 512;
+
+// A thread's N = 16 / sizeof(T) columns of a row: from c on, of which lo .. are its own (none past
+// the row's end).  kShort: a row shorter than N, read and written value by value.
+template <typename T, bool kShort>
+struct Columns {
+  static constexpr int N = kPer<T>;
+  int c, lo, D;
+  __device__ __forceinline__ Columns(int piece, int D_) : D(D_) {
+    const int at = piece * N;
+    c = kShort ? 0 : at < D - N ? at : D - N;
+    lo = at - c < N ? at - c : N;
   }
-  return u;
+  __device__ __forceinline__ bool own(int j) const { return j >= lo && (!kShort || j < D); }
+  __device__ __forceinline__ uint4 load(const void* base, int64_t row) const {
+    const T* p = static_cast<const T*>(base) + row * D;
+    uint4 u;
+    if constexpr (!kShort) {
+      __builtin_memcpy(&u, p + c, 16);
+    } else {
+      T e[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) e[j] = p[j < D ? j : D - 1];
+      __builtin_memcpy(&u, e, 16);
+    }
+    return u;
+  }
+  __device__ __forceinline__ void store(void* base, int64_t row, const float (&v)[N]) const {
+    T* p = static_cast<T*>(base) + row * D;
+    if constexpr (!kShort) {
+      const uint4 u = packed(v);
+      __builtin_memcpy(p + c, &u, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j < D) p[j] = narrow(v[j], T());
+    }
+  }
+  __device__ __forceinline__ void store_sums(float* row, const float (&v)[N]) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (own(j)) row[c + j] = v[j];
+  }
+  __device__ __forceinline__ float param(const float* p, int j) const {
+    return !p || (kShort && j >= D) ? 1.0f : p[c + j];
+  }
+};
+
+// Value j of a piece.
+template <typename T>
+__device__ __forceinline__ float value(const uint4& u, int j) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+  else return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
 }
 
-// The piece that load_piece read for column c, widened; zero past the row's end.
-template <typename T>
-__device__ __forceinline__ void get_piece(uint4 u, int c, int D, float (&out)[kPer<T>]) {
-  constexpr int N = kPer<T>;
-  if (D >= N) {
-    const uint32_t s = static_cast<uint32_t>(c > D - N ? c - (D - N) : 0) * sizeof(T) * 8;
-    if (s & 64) u = make_uint4(u.z, u.w, 0u, 0u);
-    if (s & 32) u = make_uint4(u.y, u.z, u.w, 0u);
-    if (s & 16)
-      u = make_uint4(u.x >> 16 | u.y << 16, u.y >> 16 | u.z << 16, u.z >> 16 | u.w << 16,
-                     u.w >> 16);
-    if (s >= 128) u = make_uint4(0u, 0u, 0u, 0u);
-  }
-  widen(u, out);
-  if (D < N) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) out[j] = c == 0 && j < D ? out[j] : 0.0f;
-  }
+template <int kCtrl>
+__device__ __forceinline__ float plus_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true));
 }
 
-template <typename T>
-__device__ __forceinline__ void store_piece(T* row, int c, int D, const float (&v)[kPer<T>]) {
-  constexpr int N = kPer<T>;
-  if (c + N <= D) {
-    const uint4 u = packed(v);
-    __builtin_memcpy(row + c, &u, 16);
-  } else {
-#pragma unroll
-    for (int j = 0; j + 1 < N; ++j)
-      if (c + j < D) row[c + j] = narrow(v[j], T());
+// The sum over each group of W neighbouring lanes, in every one of them.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v = plus_dpp<0xB1>(v);                          // quad_perm [1, 0, 3, 2]
+  v = plus_dpp<0x4E>(v);                          // quad_perm [2, 3, 0, 1]
+  v = plus_dpp<0x141>(v);                         // row_half_mirror: the other quad of eight
+  if constexpr (W > 8) v = plus_dpp<0x140>(v);    // row_mirror: the other eight of sixteen
+  if constexpr (W > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
+  if constexpr (W > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
 }
 
 // Sums over the threads of a row (TPR lanes of a wavefront, or with TPR = 0 the whole block), in a
@@ -77,14 +120,11 @@ __device__ __forceinline__ void store_piece(T* row, int c, int D, const float (&
 template <int TPR, int K>
 __device__ __forceinline__ void sum_row(float (&v)[K], float (*red)[kMaxWaves][4], int& flip) {
 #pragma unroll
-  for (int o = (TPR ? TPR : 64) / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], o, 64);
+  for (int k = 0; k < K; ++k) v[k] = lanes_sum<TPR ? TPR : 64>(v[k]);
   if constexpr (TPR == 0) {
     const int waves = blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int k = 0; k < K; ++k) red[flip][threadIdx.x >> 6][k] = v[k];
+    for (int k = 0; k < K; ++k) red[flip][threadIdx.x >> 6][k] = v[k];    // the same from every lane
     block_sync();
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = 0.0f;
@@ -99,9 +139,10 @@ struct Slope {
   float value, slope;
 };
 __device__ __forceinline__ Slope gate_of(float z, bool silu_form) {
-  if (!silu_form) return {z, 1.0f};
   const float s = __builtin_amdgcn_rcpf(1.0f + fast_exp2(-z * kLog2e));
-  return {z * s, s * __builtin_fmaf(z, 1.0f - s, 1.0f)};
+  Slope k = {z * s, s * __builtin_fmaf(z, 1.0f - s, 1.0f)};
+  if (!silu_form) k = {z, 1.0f};
+  return k;
 }
 
 // Which rows a block meets: `per` rows at a time (one for each TPR threads), blocks side by side.
@@ -114,90 +155,126 @@ struct Rows {
     lane = TPR ? static_cast<int>(threadIdx.x) % TPR : static_cast<int>(threadIdx.x);
     slot = TPR ? static_cast<int>(threadIdx.x) / TPR : 0;
   }
+  // Row r0 + slot of `rows`, or the last one.
+  __device__ __forceinline__ int64_t at(int64_t r0, int64_t rows) const {
+    const int64_t r = r0 + slot;
+    return r < rows ? r : rows - 1;
+  }
 };
 
-template <typename T, int N>
-__device__ __forceinline__ void load_columns(const float* p, int c, int D, float other,
-                                             float (&v)[N]) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = c + j < D ? (p ? p[c + j] : other) : 0.0f;
+// Where a row's statistic goes; nowhere without p.
+__device__ __forceinline__ void store_stat(float* p, int64_t r0, int slot, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), make_buf(p + (p ? r0 : 0), p ? 4 * 64 : 0),
+                                        slot * 4, 0, 0);
 }
 
-template <typename T, int TPR, int VPT, bool kGate>
-__global__ __launch_bounds__(TPR ? 256 : 1024) void residual_norm_kernel(ResidualNormArgs a) {
+template <int VPT, bool kGate>
+struct FwdRow {
+  uint4 y[VPT], q[VPT], z[kGate ? VPT : 1];
+};
+
+template <typename T, int TPR, int VPT, int kThreads, bool kShort, bool kGate>
+__global__ __launch_bounds__(kThreads, kMinWaves) void residual_norm_kernel(ResidualNormArgs a) {
   constexpr int N = kPer<T>;
+  using Col = Columns<T, kShort>;
   __shared__ float red[2][kMaxWaves][4];
   int flip = 0;
   const Rows<TPR> at;
   const int D = static_cast<int>(a.D);
   const float inv = 1.0f / static_cast<float>(D);
-  float w[VPT][N], pw[VPT][N];                     // pw: times the scale
+  float w[VPT][N], cp[VPT][N];                     // cp: post_weight times the scale
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (at.lane + at.tpr * i) * N;
-    float sc[N];
-    load_columns<T>(a.weight, c, D, 1.0f, w[i]);
-    load_columns<T>(a.post_weight, c, D, 1.0f, pw[i]);
-    load_columns<T>(a.scale, c, D, 1.0f, sc);
+    const Col col(at.lane + at.tpr * i, D);
 #pragma unroll
-    for (int j = 0; j < N; ++j) pw[i][j] *= sc[j];
+    for (int j = 0; j < N; ++j) {
+      w[i][j] = col.param(a.weight, j);
+      cp[i][j] = col.param(a.post_weight, j) * col.param(a.scale, j);
+    }
   }
-  const int64_t stride = int64_t(gridDim.x) * at.per;
-  for (int64_t r0 = int64_t(blockIdx.x) * at.per; r0 < a.rows; r0 += stride) {
-    const bool mine = r0 + at.slot < a.rows;
-    const int64_t r = mine ? r0 + at.slot : a.rows - 1;
-    uint4 y[VPT], q[VPT], z[VPT];
+  using Row = FwdRow<VPT, kGate>;
+  auto load = [&](Row& p, int64_t r0) __attribute__((always_inline)) {
+    const int64_t r = at.at(r0, a.rows);
     const int64_t zr = a.gate_rows > 1 ? static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows)
                                        : r;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (at.lane + at.tpr * i) * N;
-      y[i] = load_piece(static_cast<const T*>(a.y) + r * D, c, D);
-      if constexpr (kGate) z[i] = load_piece(static_cast<const T*>(a.gate) + zr * D, c, D);
-      q[i] = load_piece(static_cast<const T*>(a.residual) + r * D, c, D);
+      const Col col(at.lane + at.tpr * i, D);
+      p.y[i] = col.load(a.y, r);
+      if constexpr (kGate) p.z[i] = col.load(a.gate, zr);
+      p.q[i] = col.load(a.residual, r);
     }
-    float v[VPT][N], s[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      get_piece<T>(y[i], (at.lane + at.tpr * i) * N, D, v[i]);
-#pragma unroll
-      for (int j = 0; j < N; ++j) s[0] = __builtin_fmaf(v[i][j], v[i][j], s[0]);
-    }
-    float post = 1.0f;
+  };
+  auto work = [&](const Row& p, int64_t r0) __attribute__((always_inline)) {
+    const int64_t r = at.at(r0, a.rows);
+    const int slot = r0 + at.slot < a.rows ? at.slot : 64;
+    float post = 1.0f, s[1];
     if (a.post_weight) {
+      s[0] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const Col col(at.lane + at.tpr * i, D);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float v = col.own(j) ? value<T>(p.y[i], j) : 0.0f;
+          s[0] = __builtin_fmaf(v, v, s[0]);
+        }
+      }
       sum_row<TPR>(s, red, flip);
       post = 1.0f / sqrtf(s[0] * inv + a.eps);
-      if (mine && at.lane == 0 && a.post_rstd) a.post_rstd[r] = post;
     }
+    float t[VPT][N];
     s[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (at.lane + at.tpr * i) * N;
-      float u[N], g[N];
-      get_piece<T>(q[i], c, D, u);
-      if constexpr (kGate) get_piece<T>(z[i], c, D, g);
+      const Col col(at.lane + at.tpr * i, D);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        float t = v[i][j] * post * pw[i][j];
-        if constexpr (kGate) t *= gate_of(g[j], a.silu).value;
-        v[i][j] = to_float(narrow(u[j] + t, T()));
-        s[0] = __builtin_fmaf(v[i][j], v[i][j], s[0]);
+        float v = value<T>(p.y[i], j) * post * cp[i][j];
+        if constexpr (kGate) v *= gate_of(value<T>(p.z[i], j), a.silu).value;
+        t[i][j] = to_float(narrow(value<T>(p.q[i], j) + v, T()));
+        const float u = col.own(j) ? t[i][j] : 0.0f;
+        s[0] = __builtin_fmaf(u, u, s[0]);
       }
-      if (mine) store_piece(static_cast<T*>(a.total) + r * D, c, D, v[i]);
+      col.store(a.total, r, t[i]);
     }
     sum_row<TPR>(s, red, flip);
     const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-    if (mine && at.lane == 0 && a.rstd) a.rstd[r] = rstd;
+    store_stat(a.rstd, r0, slot, rstd);
+    store_stat(a.post_rstd, r0, slot, post);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      const Col col(at.lane + at.tpr * i, D);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[i][j] = v[i][j] * rstd * w[i][j];
-      if (mine) store_piece(static_cast<T*>(a.out) + r * D, (at.lane + at.tpr * i) * N, D, v[i]);
+      for (int j = 0; j < N; ++j) t[i][j] = t[i][j] * rstd * w[i][j];
+      col.store(a.out, r, t[i]);
+    }
+  };
+  const int64_t step = int64_t(gridDim.x) * at.per;
+  int64_t r0 = int64_t(blockIdx.x) * at.per;
+  if constexpr (kLoadsAhead<VPT, kThreads>) {
+    // two rows' registers in turn: the next row is on its way while one is worked on
+    Row p[2];
+    load(p[0], r0);
+    while (r0 < a.rows) {
+      load(p[1], r0 + step);
+      work(p[0], r0);
+      r0 += step;
+      if (r0 >= a.rows) break;
+      load(p[0], r0 + step);
+      work(p[1], r0);
+      r0 += step;
+    }
+  } else {
+    for (; r0 < a.rows; r0 += step) {
+      Row p;
+      load(p, r0);
+      work(p, r0);
     }
   }
 }
 
-// The sums of the block's rows of threads for column piece i, into dst (those of slot 0 write).
+// The sums of the block's rows of threads for a column piece (those of slot 0 get them).
 template <int TPR, int N>
 __device__ __forceinline__ bool sum_slots(const Rows<TPR>& at, float* cols, float (&v)[N]) {
   if constexpr (TPR == 0) return true;
@@ -215,161 +292,235 @@ __device__ __forceinline__ bool sum_slots(const Rows<TPR>& at, float* cols, floa
   return true;
 }
 
-template <int N>
-__device__ __forceinline__ void store_columns(float* p, int c, int D, const float (&v)[N]) {
+// How rows read gates.
+enum Gate { kNoGate = 0, kOwnGate = 1, kSharedGate = 2 };
+
+// w and cp = scale pw of a thread's columns, from LDS, whose reads are counted apart from the
+// loads of the next row that are on their way.  The quarters of all pieces lie behind one another, so
+// that a wavefront's 16-byte reads meet every bank once.
+template <typename T, bool kShort>
+struct Params {
+  static constexpr int N = kPer<T>;
+  const float* lds;
+  int pieces;
+  __device__ __forceinline__ void stage(const ResidualNormArgs& a, float* room, int n) {
+    lds = room;
+    pieces = n;
+    for (int q = threadIdx.x; q < n; q += blockDim.x) {
+      const Columns<T, kShort> col(q, static_cast<int>(a.D));
+      for (int j = 0; j < N; ++j) {
+        room[(j / 4 * n + q) * 4 + j % 4] = col.param(a.weight, j);
+        room[((N / 4 + j / 4) * n + q) * 4 + j % 4] =
+            col.param(a.post_weight, j) * col.param(a.scale, j);
+      }
+    }
+    block_sync();
+  }
+  // Columns 4 h .. of a piece.
+  __device__ __forceinline__ void get(int piece, int h, f32x4& w, f32x4& cp) const {
+    __builtin_memcpy(&w, lds + (h * pieces + piece) * 4, 16);
+    __builtin_memcpy(&cp, lds + ((N / 4 + h) * pieces + piece) * 4, 16);
+  }
+};
+
+// A row's pieces as they lie in memory.
+template <int VPT, int kGate, bool kSum>
+struct BwdRow {
+  uint4 g[VPT], t[VPT], y[VPT], z[kGate == kNoGate ? 1 : VPT], e[kSum ? VPT : 1];
+  float rstd, post;
+  static __device__ __forceinline__ void keep(uint4& u) {
+    asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w));
+  }
+  // The row is widened twice; kept as it was loaded in between it takes half the registers.
+  __device__ __forceinline__ void keep_packed() {
 #pragma unroll
-  for (int j = 0; j < N; ++j)
-    if (c + j < D) p[c + j] = v[j];
-}
+    for (int i = 0; i < VPT; ++i) {
+      keep(g[i]), keep(t[i]), keep(y[i]);
+      if constexpr (kGate != kNoGate) keep(z[i]);
+      if constexpr (kSum) keep(e[i]);
+    }
+  }
+};
 
 // Rows in `sets` of `rows` each that share a gate (one set of all rows where each has its own, or
-// none has one); `split` blocks work on a set.  part: [gridDim.x, 3, D] the blocks' sums
-// for w, pw and the scale; gpart: [sets, split, D] those for the shared gates, where split > 1.
-template <typename T, int TPR, int VPT, bool kGate>
-__global__ __launch_bounds__(TPR ? 256 : 1024) void residual_norm_bwd_kernel(
+// none has one); `split` blocks work on a set.  part: [gridDim.x, 2, D] the blocks' sums
+// dw and S; gpart: [sets, split, D] those for the shared gates, where split > 1.
+template <typename T, int TPR, int VPT, int kThreads, bool kShort, int kGate, bool kSum>
+__global__ __launch_bounds__(kThreads, kMinWaves) void residual_norm_bwd_kernel(
     ResidualNormArgs a, ResidualNormGrads d, int64_t sets, int64_t rows, int64_t split, float* part,
     float* gpart) {
   constexpr int N = kPer<T>;
+  using Col = Columns<T, kShort>;
+  extern __shared__ __align__(16) float room[];
   __shared__ float red[2][kMaxWaves][4];
   __shared__ float cols[TPR ? 256 * N : 1];
   int flip = 0;
   const Rows<TPR> at;
   const int D = static_cast<int>(a.D);
   const float inv = 1.0f / static_cast<float>(D);
-  const bool shared = kGate && a.gate_rows > 1;
-  float w[VPT][N], pw[VPT][N], sc[VPT][N], dw[VPT][N], dpw[VPT][N], dsc[VPT][N];
+  const float* post_rstd = a.post_weight ? a.post_rstd : a.rstd;
+  Params<T, kShort> params;
+  params.stage(a, room, at.tpr * VPT);
+  float dw[VPT][N], ds[VPT][N], dz[kGate == kSharedGate ? VPT : 1][N];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (at.lane + at.tpr * i) * N;
-    load_columns<T>(a.weight, c, D, 1.0f, w[i]);
-    load_columns<T>(a.post_weight, c, D, 1.0f, pw[i]);
-    load_columns<T>(a.scale, c, D, 1.0f, sc[i]);
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) dw[i][j] = dpw[i][j] = dsc[i][j] = 0.0f;
-  }
-  const int64_t part_of = blockIdx.x % split, set_step = gridDim.x / split;
-  for (int64_t set = blockIdx.x / split; set < sets; set += set_step) {
-    float dz[VPT][N];
+    for (int j = 0; j < N; ++j) dw[i][j] = ds[i][j] = 0.0f;
+  using Row = BwdRow<VPT, kGate, kSum>;
+  auto load = [&](Row& p, int64_t set, int64_t r0) __attribute__((always_inline)) {
+    const int64_t r = set * rows + at.at(r0, rows);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+      const Col col(at.lane + at.tpr * i, D);
+      p.t[i] = col.load(a.total, r);
+      p.g[i] = col.load(d.dout, r);
+      p.y[i] = col.load(a.y, r);
+      if constexpr (kGate != kNoGate) p.z[i] = col.load(a.gate, kGate == kSharedGate ? set : r);
+      if constexpr (kSum) p.e[i] = col.load(d.dtotal, r);
+    }
+    p.rstd = a.rstd[r];
+    p.post = post_rstd[r];
+  };
+  auto work = [&](Row& p, int64_t set, int64_t r0) __attribute__((always_inline)) {
+    const int64_t r = set * rows + at.at(r0, rows);
+    const bool mine = TPR == 0 || r0 + at.slot < rows;
+    const float rstd = p.rstd, post = a.post_weight ? p.post : 1.0f;
+    float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < N; ++j) dz[i][j] = 0.0f;
-    for (int64_t r0 = part_of * at.per; r0 < rows; r0 += split * at.per) {
-      const bool mine = r0 + at.slot < rows;
-      const int64_t r = set * rows + (mine ? r0 + at.slot : rows - 1);
-      uint4 g[VPT], e[VPT], t[VPT], y[VPT], z[VPT];
+    for (int i = 0; i < VPT; ++i) {
+      const int piece = at.lane + at.tpr * i;
+      const Col col(piece, D);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (at.lane + at.tpr * i) * N;
-        g[i] = load_piece(static_cast<const T*>(d.dout) + r * D, c, D);
-        t[i] = load_piece(static_cast<const T*>(a.total) + r * D, c, D);
-        y[i] = load_piece(static_cast<const T*>(a.y) + r * D, c, D);
-        if constexpr (kGate)
-          z[i] = load_piece(static_cast<const T*>(a.gate) + (shared ? set : r) * D, c, D);
-        if (d.dtotal) e[i] = load_piece(static_cast<const T*>(d.dtotal) + r * D, c, D);
-        else e[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      const float rstd = a.rstd[r];
-      const float post = a.post_weight ? a.post_rstd[r] : 1.0f;
-      float s[3] = {0.0f, 0.0f, 0.0f};
+      for (int h = 0; h < N / 4; ++h) {
+        f32x4 w, cp;
+        params.get(piece, h, w, cp);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (at.lane + at.tpr * i) * N;
-        float gv[N], ev[N], tv[N], yv[N], zv[N];
-        get_piece<T>(g[i], c, D, gv);
-        get_piece<T>(e[i], c, D, ev);
-        get_piece<T>(t[i], c, D, tv);
-        get_piece<T>(y[i], c, D, yv);
-        if constexpr (kGate) get_piece<T>(z[i], c, D, zv);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float that = tv[j] * rstd, wd = gv[j] * w[i][j];
-          float q = sc[i][j] * pw[i][j] * (yv[j] * post);
-          if constexpr (kGate) q *= gate_of(zv[j], a.silu).value;
+        for (int k = 0; k < 4; ++k) {
+          const int j = 4 * h + k;
+          const float that = value<T>(p.t[i], j) * rstd;
+          float wd = value<T>(p.g[i], j) * w[k];
+          float q = cp[k] * (value<T>(p.y[i], j) * post);
+          if constexpr (kGate != kNoGate) q *= gate_of(value<T>(p.z[i], j), a.silu).value;
+          wd = col.own(j) ? wd : 0.0f;
+          q = col.own(j) ? q : 0.0f;
+          float e = rstd * wd;
+          if constexpr (kSum) e += value<T>(p.e[i], j);
           s[0] = __builtin_fmaf(wd, that, s[0]);
-          s[1] = __builtin_fmaf(__builtin_fmaf(rstd, wd, ev[j]), q, s[1]);
+          s[1] = __builtin_fmaf(e, q, s[1]);
           s[2] = __builtin_fmaf(that, q, s[2]);
         }
       }
-      sum_row<TPR>(s, red, flip);
-      const float m1 = s[0] * inv;
-      const float m2 = a.post_weight ? (s[1] - rstd * m1 * s[2]) * inv : 0.0f;
+    }
+    p.keep_packed();
+    sum_row<TPR>(s, red, flip);
+    const float m1 = s[0] * inv;
+    const float m2 = a.post_weight ? (s[1] - rstd * m1 * s[2]) * inv : 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (at.lane + at.tpr * i) * N;
-        float gv[N], ev[N], tv[N], yv[N], zv[N], dy[N], dr[N];
-        get_piece<T>(g[i], c, D, gv);
-        get_piece<T>(e[i], c, D, ev);
-        get_piece<T>(t[i], c, D, tv);
-        get_piece<T>(y[i], c, D, yv);
-        if constexpr (kGate) get_piece<T>(z[i], c, D, zv);
+    for (int i = 0; i < VPT; ++i) {
+      const int piece = at.lane + at.tpr * i;
+      const Col col(piece, D);
+      float dy[N], dr[N], dg[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float that = tv[j] * rstd, wd = gv[j] * w[i][j], yh = yv[j] * post;
-          Slope k = {1.0f, 0.0f};
-          if constexpr (kGate) k = gate_of(zv[j], a.silu);
-          const float dt = __builtin_fmaf(rstd, wd - that * m1, ev[j]);
-          const float dg = dt * k.value;                     // before the scale
-          const float dc = dg * sc[i][j];
+      for (int h = 0; h < N / 4; ++h) {
+        f32x4 w, cp;
+        params.get(piece, h, w, cp);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = 4 * h + k;
+          const float gv = value<T>(p.g[i], j), that = value<T>(p.t[i], j) * rstd;
+          const float yh = value<T>(p.y[i], j) * post;
+          Slope z = {1.0f, 0.0f};
+          if constexpr (kGate != kNoGate) z = gate_of(value<T>(p.z[i], j), a.silu);
+          float dt = rstd * (gv * w[k] - that * m1);
+          if constexpr (kSum) dt += value<T>(p.e[i], j);
+          const float dv = dt * z.value;
           dr[j] = dt;
-          dy[j] = post * __builtin_fmaf(-yh, m2, dc * pw[i][j]);
-          if (mine) {
-            dw[i][j] = __builtin_fmaf(gv[j], that, dw[i][j]);
-            dpw[i][j] = __builtin_fmaf(dc, yh, dpw[i][j]);
-            dsc[i][j] = __builtin_fmaf(dg, yh * pw[i][j], dsc[i][j]);
-          }
-          if constexpr (kGate) {
-            zv[j] = dt * yh * pw[i][j] * sc[i][j] * k.slope;
-            if (mine) dz[i][j] += zv[j];
-          }
-        }
-        if (mine) {
-          store_piece(static_cast<T*>(d.dresidual) + r * D, c, D, dr);
-          store_piece(static_cast<T*>(d.dy) + r * D, c, D, dy);
-          if constexpr (kGate)
-            if (!shared) store_piece(static_cast<T*>(d.dgate) + r * D, c, D, zv);
+          dy[j] = post * __builtin_fmaf(-yh, m2, dv * cp[k]);
+          dg[j] = dt * (yh * cp[k]) * z.slope;
+          dw[i][j] = mine ? __builtin_fmaf(gv, that, dw[i][j]) : dw[i][j];
+          ds[i][j] = mine ? __builtin_fmaf(dv, yh, ds[i][j]) : ds[i][j];
+          if constexpr (kGate == kSharedGate) dz[i][j] = mine ? dz[i][j] + dg[j] : dz[i][j];
         }
       }
+      col.store(d.dresidual, r, dr);
+      col.store(d.dy, r, dy);
+      if constexpr (kGate == kOwnGate) col.store(d.dgate, r, dg);
     }
-    if (shared) {
+  };
+  const int64_t part_of = blockIdx.x % split, set_step = gridDim.x / split;
+  const int64_t first = part_of * at.per, step = split * at.per;
+  for (int64_t set = blockIdx.x / split; set < sets; set += set_step) {
+    if constexpr (kGate == kSharedGate) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) dz[i][j] = 0.0f;
+    }
+    int64_t r0 = first;
+    if constexpr (kLoadsAhead<VPT, kThreads>) {
+      // two rows' registers in turn: the next row is on its way while one is worked on
+      Row p[2];
+      load(p[0], set, r0);
+      while (r0 < rows) {
+        load(p[1], set, r0 + step);
+        work(p[0], set, r0);
+        r0 += step;
+        if (r0 >= rows) break;
+        load(p[0], set, r0 + step);
+        work(p[1], set, r0);
+        r0 += step;
+      }
+    } else {
+      for (; r0 < rows; r0 += step) {
+        Row p;
+        load(p, set, r0);
+        work(p, set, r0);
+      }
+    }
+    if constexpr (kGate == kSharedGate) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (at.lane + at.tpr * i) * N;
+        const Col col(at.lane + at.tpr * i, D);
         if (sum_slots<TPR>(at, cols, dz[i])) {
-          if (split == 1) store_piece(static_cast<T*>(d.dgate) + set * D, c, D, dz[i]);
-          else store_columns(gpart + (set * split + part_of) * D, c, D, dz[i]);
+          if (split == 1) col.store(d.dgate, set, dz[i]);
+          else col.store_sums(gpart + (set * split + part_of) * D, dz[i]);
         }
       }
     }
   }
-  float* dst = part + int64_t(blockIdx.x) * 3 * D;
+  float* dst = part + int64_t(blockIdx.x) * 2 * D;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (at.lane + at.tpr * i) * N;
-    if (sum_slots<TPR>(at, cols, dw[i])) store_columns(dst, c, D, dw[i]);
-    if (sum_slots<TPR>(at, cols, dpw[i])) store_columns(dst + D, c, D, dpw[i]);
-    if (sum_slots<TPR>(at, cols, dsc[i])) store_columns(dst + 2 * D, c, D, dsc[i]);
+    const Col col(at.lane + at.tpr * i, D);
+    if (sum_slots<TPR>(at, cols, dw[i])) col.store_sums(dst, dw[i]);
+    if (sum_slots<TPR>(at, cols, ds[i])) col.store_sums(dst + D, ds[i]);
   }
 }
 
-// Sums of the rows of part for w, pw and the scale (blockIdx.y), in a fixed order.
+// dw, and dpw and dscale from S: the sums of the rows of part (blockIdx.y: which), in a fixed order.
 __global__ __launch_bounds__(1024) void residual_norm_sum_kernel(const float* __restrict__ part,
                                                                  int64_t blocks, int64_t D,
-                                                                 float* dw, float* dpw,
-                                                                 float* dsc) {
+                                                                 const float* pw,
+                                                                 const float* scale, float* dw,
+                                                                 float* dpw, float* dscale) {
   __shared__ double m[16][64];
   const int col = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.y;
-  float* to = k == 0 ? dw : k == 1 ? dpw : dsc;
-  if (!to) return;
   const int64_t c = int64_t(blockIdx.x) * 64 + col;
   double s = 0.0;
-  if (c < D)
-    for (int64_t b = w; b < blocks; b += 16) s += part[(b * 3 + k) * D + c];
+  if (c < D) {
+#pragma unroll 8
+    for (int64_t b = w; b < blocks; b += 16) s += part[(b * 2 + k) * D + c];
+  }
   m[w][col] = s;
   block_sync();
   if (w != 0 || c >= D) return;
   for (int j = 1; j < 16; ++j) s += m[j][col];
-  to[c] = static_cast<float>(s);
+  if (k == 0) {
+    dw[c] = static_cast<float>(s);
+  } else {
+    if (dpw) dpw[c] = static_cast<float>(scale ? s * scale[c] : s);
+    if (dscale) dscale[c] = static_cast<float>(pw ? s * pw[c] : s);
+  }
 }
 
 // dgate [sets, D] = the sums of each set's `split` rows.
@@ -390,39 +541,52 @@ __global__ __launch_bounds__(256) void residual_norm_zero_kernel(float* p, int64
   if (i < n) p[i] = 0.0f;
 }
 
-// Calls f.template operator()<TPR, VPT>(threads of a block): a part of a wavefront for short
-// rows, else the wavefronts that hold the row with VPT pieces a thread.
+// Calls f.template operator()<TPR, VPT, kThreads, kShort>(threads of a block, at most kThreads): a
+// part of a wavefront for short rows, else the wavefronts that hold the row with VPT pieces a
+// thread.
 template <typename T, typename F>
 hipError_t dispatch(int64_t D, F f) {
   const int64_t pieces = (D + kPer<T> - 1) / kPer<T>;
-  if (pieces <= 8) return f.template operator()<8, 1>(256);
-  if (pieces <= 16) return f.template operator()<16, 1>(256);
-  if (pieces <= 32) return f.template operator()<32, 1>(256);
-  if (pieces <= 64) return f.template operator()<64, 1>(256);
+  if (D < kPer<T>) return f.template operator()<8, 1, 256, true>(256);
+  if (pieces <= 8) return f.template operator()<8, 1, 256, false>(256);
+  if (pieces <= 16) return f.template operator()<16, 1, 256, false>(256);
+  if (pieces <= 32) return f.template operator()<32, 1, 256, false>(256);
+  if (pieces <= 64) return f.template operator()<64, 1, 256, false>(256);
   auto threads = [&](int64_t vpt) {
     return static_cast<uint32_t>((pieces + 64 * vpt - 1) / (64 * vpt) * 64);
   };
-  if (pieces <= 1024) return f.template operator()<0, 1>(threads(1));
-  if (pieces <= 2048) return f.template operator()<0, 2>(threads(2));
+  if (pieces <= 512) return f.template operator()<0, 1, 512, false>(threads(1));
+  if (pieces <= 1024) return f.template operator()<0, 1, 1024, false>(threads(1));
+  if (pieces <= 2048) return f.template operator()<0, 2, 1024, false>(threads(2));
   if constexpr (sizeof(T) == 4)
-    if (pieces <= 4096) return f.template operator()<0, 4>(threads(4));
+    if (pieces <= 4096) return f.template operator()<0, 4, 1024, false>(threads(4));
   return hipErrorInvalidValue;
+}
+
+// Blocks: what 256 compute units hold at about ten wavefronts each, since more of them only meet
+// in the caches (32768 x 2560 bf16, 5 wavefronts a block: 210, 187, 170 us with 256, 384, 512 blocks and
+// 176, 191 with 768, 1024; 8192 x 4096, 8 wavefronts: 65, 69 us with 256, 512; gradients alike).
+// Narrow rows have up to `most` blocks a unit (30000 x 1001: 131, 92, 81 us with 256, 512, 768).
+int64_t blocks_for(uint32_t threads, int64_t most) {
+  const int64_t fit = 10 / (threads / 64);
+  return 256 * (fit < 1 ? 1 : fit > most ? most : fit);
 }
 
 template <typename T>
 struct Fwd {
   const ResidualNormArgs& a;
   hipStream_t stream;
-  template <int TPR, int VPT>
+  template <int TPR, int VPT, int kThreads, bool kShort>
   hipError_t operator()(uint32_t threads) const {
     const int64_t per = TPR ? threads / TPR : 1;
     int64_t blocks = (a.rows + per - 1) / per;
-    if (blocks > 4096) blocks = 4096;
+        const int64_t most = blocks_for(threads, 3);
+    if (blocks > most) blocks = most;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(threads);
     if (a.gate)
-      hipLaunchKernelGGL((residual_norm_kernel<T, TPR, VPT, true>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((residual_norm_kernel<T, TPR, VPT, kThreads, kShort, true>), grid, block, 0, stream, a);
     else
-      hipLaunchKernelGGL((residual_norm_kernel<T, TPR, VPT, false>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((residual_norm_kernel<T, TPR, VPT, kThreads, kShort, false>), grid, block, 0, stream, a);
     return hipGetLastError();
   }
 };
@@ -436,10 +600,10 @@ template <typename T>
 struct MakeDeal {
   int64_t rows, gate_rows;
   Deal* out;
-  template <int TPR, int VPT>
+  template <int TPR, int VPT, int kThreads, bool kShort>
   hipError_t operator()(uint32_t threads) const {
     const int64_t per = TPR ? threads / TPR : 1;
-    const int64_t most = 1024;
+    const int64_t most = blocks_for(threads, 2);
     out->sets = gate_rows > 1 ? rows / gate_rows : 1;
     out->rows = rows / out->sets;
     const int64_t room = (out->rows + per - 1) / per;
@@ -453,8 +617,8 @@ struct MakeDeal {
 
 Deal deal_of(int64_t rows, int64_t D, int64_t gate_rows, mssm_dtype dtype) {
   Deal d;
-  if (dtype == MSSM_BFLOAT16) dispatch<uint16_t>(D, MakeDeal<uint16_t>{rows, gate_rows, &d});
-  else dispatch<float>(D, MakeDeal<float>{rows, gate_rows, &d});
+  if (dtype == MSSM_BFLOAT16) (void)dispatch<uint16_t>(D, MakeDeal<uint16_t>{rows, gate_rows, &d});
+  else (void)dispatch<float>(D, MakeDeal<float>{rows, gate_rows, &d});
   return d;
 }
 
@@ -466,15 +630,23 @@ struct Bwd {
   float* part;
   float* gpart;
   hipStream_t stream;
-  template <int TPR, int VPT>
+  template <int TPR, int VPT, int kThreads, bool kShort>
   hipError_t operator()(uint32_t threads) const {
     const dim3 grid(static_cast<uint32_t>(deal.blocks)), block(threads);
-    if (a.gate)
-      hipLaunchKernelGGL((residual_norm_bwd_kernel<T, TPR, VPT, true>), grid, block, 0, stream, a,
-                         d, deal.sets, deal.rows, deal.split, part, gpart);
-    else
-      hipLaunchKernelGGL((residual_norm_bwd_kernel<T, TPR, VPT, false>), grid, block, 0, stream, a,
-                         d, deal.sets, deal.rows, deal.split, part, gpart);
+    const size_t lds = 2 * kPer<T> * sizeof(float) * VPT * (TPR ? TPR : threads);
+    auto go = [&](auto gate, auto sum) {
+      hipLaunchKernelGGL((residual_norm_bwd_kernel<T, TPR, VPT, kThreads, kShort, decltype(gate)::value,
+                                                   decltype(sum)::value>),
+                         grid, block, lds, stream, a, d, deal.sets, deal.rows, deal.split, part,
+                         gpart);
+    };
+    auto with_sum = [&](auto gate) {
+      if (d.dtotal) go(gate, std::true_type());
+      else go(gate, std::false_type());
+    };
+    if (!a.gate) with_sum(std::integral_constant<int, kNoGate>());
+    else if (a.gate_rows > 1) with_sum(std::integral_constant<int, kSharedGate>());
+    else with_sum(std::integral_constant<int, kOwnGate>());
     return hipGetLastError();
   }
 };
@@ -490,7 +662,7 @@ size_t residual_norm_bwd_workspace(int64_t rows, int64_t D, int64_t gate_rows, m
   if (rows == 0 || D == 0) return 0;
   const Deal d = deal_of(rows, D, gate_rows, dtype);
   const size_t gates = gate_rows > 1 && d.split > 1 ? static_cast<size_t>(d.sets) * d.split : 0;
-  return (static_cast<size_t>(d.blocks) * 3 + gates) * D * sizeof(float);
+  return (static_cast<size_t>(d.blocks) * 2 + gates) * D * sizeof(float);
 }
 
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const ResidualNormGrads& d, void* ws,
@@ -507,7 +679,7 @@ hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const ResidualNor
   }
   const Deal deal = deal_of(a.rows, a.D, a.gate_rows, a.dtype);
   float* part = static_cast<float*>(ws);
-  float* gpart = part + deal.blocks * 3 * a.D;
+  float* gpart = part + deal.blocks * 2 * a.D;
   hipError_t e;
   if (a.dtype == MSSM_BFLOAT16)
     e = dispatch<uint16_t>(a.D, Bwd<uint16_t>{a, d, deal, part, gpart, stream});
@@ -526,9 +698,9 @@ hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, const ResidualNor
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(residual_norm_sum_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64), 3),
-                     dim3(1024), 0, stream, part, deal.blocks, a.D, d.dweight, d.dpost_weight,
-                     d.dscale);
+  hipLaunchKernelGGL(residual_norm_sum_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64), 2),
+                     dim3(1024), 0, stream, part, deal.blocks, a.D, a.post_weight, a.scale,
+                     d.dweight, d.dpost_weight, d.dscale);
   return hipGetLastError();
 }
 

@@ -1483,8 +1483,7 @@ def _residual_norm_check(y, weight, post_weight, gate, gate_form, scale):
 def mssm_residual_norm_fwd(y, residual, weight, out, total, *, post_weight=None, gate=None,
                            gate_form="silu", scale=None, rstd=None, post_rstd=None, eps=1e-5,
                            stream=None):
-    """out, total (and rstd, post_rstd) <- residual norm (see residual_norm); total may be residual
-    or y."""
+    """out, total (and rstd, post_rstd) <- residual norm (see residual_norm)."""
     dev, rows, D, form, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form,
                                                          scale)
     dt, shape = y.dtype, y.shape

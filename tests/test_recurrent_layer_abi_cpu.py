@@ -164,7 +164,7 @@ def test_conv_errors(lib):
 
 def test_residual_norm_errors(lib):
     # y residual weight post gate scale out total rstd post_rstd | form gate_rows eps rows D
-    ptrs = [FAKE, FAKE, FAKE, None, None, None, FAKE, FAKE, None, None]
+    ptrs = [FAKE, FAKE, FAKE, None, None, None, OTHER, OTHER, None, None]
 
     def f(p=ptrs, form=1, gate_rows=1, eps=1e-5, rows=8, D=40, dtype=BF16):
         return lib.mssm_residual_norm_fwd(*p, form, gate_rows, eps, rows, D, dtype, None)
@@ -178,6 +178,8 @@ def test_residual_norm_errors(lib):
     assert f(D=16385) == UNSUPPORTED and f(rows=1 << 32) == UNSUPPORTED
     assert f(rows=1 << 60, D=100) == OVERFLOW
     assert f(put(ptrs, 9, FAKE)) == INVALID                             # post_rstd alone
+    for i in (6, 7):
+        assert f(put(ptrs, i, FAKE)) == INVALID                         # an output that is an input
     assert f([None] * 10, rows=0) == OK and f([None] * 10, D=0) == OK
 
     q = lib.mssm_residual_norm_bwd_workspace_size
@@ -188,11 +190,13 @@ def test_residual_norm_errors(lib):
     assert query(q, 4096, 520, 3, BF16)[0] == INVALID
     assert q(8, 40, 1, BF16, None) == INVALID
     # dout dtotal y total weight post gate scale rstd post_rstd dy dresidual dgate dweight dpost dscale
-    b = [FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE, None, FAKE, FAKE, None, FAKE, None, None]
+    b = [FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE, None, OTHER, OTHER, None, FAKE, None, None]
     g = lambda p=b, ws=None, wsb=0, rows=8: lib.mssm_residual_norm_bwd(*p, 1, 1, ws, wsb, rows, 40,
                                                                        BF16, None)
     for i in (0, 2, 3, 4, 8, 10, 11, 13):
         assert g(put(b, i, None), FAKE, 1 << 30) == INVALID, i
     for i in (5, 6, 7, 9, 12, 14, 15):                                  # one without its gradient
         assert g(put(b, i, OTHER), FAKE, 1 << 30) == INVALID, i
+    for i in (10, 11):
+        assert g(put(b, i, FAKE), FAKE, 1 << 30) == INVALID, i          # an output that is an input
     assert g() == WORKSPACE
