@@ -9,10 +9,15 @@
 //   e = lambda (a h_{t-1} - g x a^2 / m)      (the gradient of log a: dm / dlog a = -a^2 / m)
 //   dr = e A s (1 - s),   dA = sum over tokens of e s.
 //
-// A wavefront takes kSteps tokens of 64 V channels (a lane holds V channels) and a block kWaves
-// wavefronts behind one another: a tile.  Every affine map h -> P h + H of a wavefront's
-// tokens is formed from registers; the wavefronts' maps are joined in LDS, the tiles'
-// by a pass over them.
+// A wavefront takes a few tokens of 64 V channels (a lane holds V channels) and a block kWaves
+// wavefronts behind one another: a tile.  The affine map h -> P h + H of a wavefront's tokens
+// is formed from registers and the wavefronts' maps are joined in LDS, so every input is read
+// once.  Tiles of the same channels form a chain: a block publishes its tile's map, then
+// looks back over the tiles before it for the nearest one whose state is known, takes that state
+// through the maps in between, and publishes its own.  Blocks take their tiles in the order in which
+// they start (a counter for each chain), so the tiles that one waits for are all being worked on, and the
+// first of them waits for none.  A state is always made by the same operations from the one
+// before it, wherever the look-back began: results do not depend on the timing.
 #include <type_traits>
 
 #include "mssm_internal.h"
@@ -24,11 +29,24 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kBlock = 64 * kWaves;
+constexpr int kSavedTokens = 64;          // a saved state for every so many tokens
+constexpr int kLookBack = 8;              // tiles looked at together
+constexpr int kMaxPolls = 1 << 22;
+constexpr int64_t kTicketStride = 32;     // counters on cache lines of their own
+#ifndef BW
+#define BW 4
+#endif
 
+#ifndef FS
+#define FS 16
+#endif
+#ifndef BS
+#define BS 8
+#endif
 template <typename T>
-constexpr int kSteps = sizeof(T) == 2 ? 16 : 8;   // tokens of a wavefront
+constexpr int kFwdSteps = sizeof(T) == 2 ? FS : 8;   // tokens of a wavefront
 template <typename T>
-constexpr int kTile = kWaves * kSteps<T>;
+constexpr int kBwdSteps = BS;
 
 // Joins the affine map (P, H) behind state h.  P = 0 stands for a sequence's first token in between
 // (or a decay of nothing): what h was, infinite or NaN too, is forgotten.
@@ -36,27 +54,109 @@ __device__ __forceinline__ float join(float P, float H, float h) {
   return P == 0.0f ? H : __builtin_fmaf(P, h, H);
 }
 
+// A chain's slots, [tiles, D]: a tile's map (P, H) in one word, or its state, marked by P = -1
+// (decays are not negative), or nothing yet (all bits set, which no map is).  A word is written and
+// read whole, so it needs no other order.
+constexpr uint32_t kEmpty = 0xffffffffu, kState = 0xbf800000u, kNan = 0x7fc00000u;
+
+__device__ __forceinline__ void publish(uint64_t* slot, uint32_t P, float H) {
+  __hip_atomic_store(slot, static_cast<uint64_t>(__float_as_uint(H)) << 32 | P, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state before the chain's tile j, whose map is (P, H): one wavefront, each lane its V channels
+// from c on.  Also publishes the tile's map and its state.  (The tiles it waits for are being
+// worked on, some microseconds each; should another call overwrite the workspace meanwhile, the
+// wait still ends, seconds later, with NaN.)
+template <int V>
+__device__ __forceinline__ void look_back(uint64_t* slots, int64_t j, int64_t D, int c,
+                                          const float (&P)[V], const float (&H)[V], float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = 0.0f;
+  if (j > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      publish(slots + j * D + c + v, P[v] == P[v] ? __float_as_uint(P[v]) : kNan, H[v]);
+    for (int polls = 0;; ++polls) {
+      uint64_t w[kLookBack][V];
+#pragma unroll
+      for (int i = 0; i < kLookBack; ++i) {
+        const int64_t k = j - 1 - i > 0 ? j - 1 - i : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          w[i][v] = __hip_atomic_load(slots + k * D + c + v, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+      }
+      bool known = true;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        bool found = false;
+        h[v] = 0.0f;
+#pragma unroll
+        for (int i = kLookBack - 1; i >= 0; --i) {      // from the farthest on
+          const uint32_t p = static_cast<uint32_t>(w[i][v]);
+          const float u = __uint_as_float(static_cast<uint32_t>(w[i][v] >> 32));
+          h[v] = p == kState ? u : join(__uint_as_float(p), u, h[v]);
+          found = (found || p == kState) && p != kEmpty;
+        }
+        known = known && found;
+      }
+      if (__all(known)) break;
+      if (polls == kMaxPolls) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = __uint_as_float(kNan);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) publish(slots + j * D + c + v, kState, join(P[v], H[v], h[v]));
+}
+
+// Sets the slots to "nothing yet" and the chains' counters to zero.
+__global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* slots, int64_t n,
+                                                               uint32_t* tickets, int64_t groups) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t k = i; k < n; k += int64_t(gridDim.x) * 256)
+    slots[k] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+  if (i < groups) tickets[i * kTicketStride] = 0;
+}
+
 struct Place {
-  int64_t tile, t0;       // t0: the wavefront's first token
+  int64_t link;           // the tile's place in its chain
+  int64_t t0;             // the wavefront's first token
   int wave, lane;
   int c;                  // the lane's first channel
   bool active;            // not a copy of another lane
 };
 
-template <typename T, int V>
-__device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t block) {
+// tiles: how many a chain has; with one there is nothing to take a ticket for.  (Every block gets a
+// tile; one beyond them, which only a workspace in use elsewhere could give, is not worked on.)
+template <int V, int S, bool kReverse>
+__device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t tiles,
+                                          uint32_t* tickets) {
+  __shared__ uint32_t ticket;
   Place p;
   p.wave = MSSM_UNIFORM(static_cast<int>(threadIdx.x >> 6));
   p.lane = static_cast<int>(threadIdx.x & 63);
-  p.tile = block / groups;
-  const int64_t c0 = (block % groups) * (64 * V) + p.lane * V;
+  const int64_t group = blockIdx.x % groups;
+  p.link = 0;
+  if (tiles > 1) {
+    if (threadIdx.x == 0)
+      ticket = __hip_atomic_fetch_add(tickets + group * kTicketStride, 1u, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+    block_sync();
+    p.link = MSSM_UNIFORM(ticket);
+  }
+  const int64_t c0 = group * (64 * V) + p.lane * V;
   p.active = c0 < D;
   p.c = static_cast<int>(c0 < D - V ? c0 : D - V);
-  p.t0 = p.tile * kTile<T> + p.wave * kSteps<T>;
+  p.t0 = (kReverse ? tiles - 1 - p.link : p.link) * (kWaves * S) + p.wave * S;
   return p;
 }
 
-// kSteps rows of a tensor from token t0 on, each lane its V channels.
+// S rows of a tensor from token t0 on, each lane its V channels.
 template <typename T, int V, int S>
 __device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t t0, int64_t tokens,
                                           int c, Raw<T, V> (&v)[S]) {
@@ -67,15 +167,76 @@ __device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t
   }
 }
 
-// agg: [tiles, D] (P, H) of each tile, written without kOut; carry: [tiles, D] the state
-// before each tile, read with kOut (null: zero, for a single tile).
+// What the wavefronts of a block tell one another.
+template <int V>
+struct Maps {
+  float p[kWaves][64 * V], h[kWaves][64 * V], in[64 * V];
+  __device__ __forceinline__ void put(const Place& at, const float (&P)[V], const float (&H)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[at.wave][at.lane * V + v] = P[v], h[at.wave][at.lane * V + v] = H[v];
+  }
+  // The map of all wavefronts' tokens, in the chain's order.
+  template <bool kReverse>
+  __device__ __forceinline__ void all(int lane, float (&P)[V], float (&H)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      P[v] = 1.0f, H[v] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        const int w = kReverse ? kWaves - 1 - k : k;
+        const float q = p[w][lane * V + v];
+        H[v] = join(q, h[w][lane * V + v], H[v]);
+        P[v] = q == 0.0f ? 0.0f : P[v] * q;
+      }
+    }
+  }
+  // The state x before the block's tokens, taken to the wavefront's own.
+  template <bool kReverse>
+  __device__ __forceinline__ void take(const Place& at, float (&x)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      for (int k = 0; k < (kReverse ? kWaves - 1 - at.wave : at.wave); ++k) {
+        const int w = kReverse ? kWaves - 1 - k : k;
+        x[v] = join(p[w][at.lane * V + v], h[w][at.lane * V + v], x[v]);
+      }
+  }
+};
+
+// The state (backward: psi) before this wavefront's tokens.  P, H: its own map.
+template <int V, bool kReverse>
+__device__ __forceinline__ void chain(const Place& at, Maps<V>& m, uint64_t* slots, int64_t tiles,
+                                      int64_t D, const float (&P)[V], const float (&H)[V],
+                                      float (&x)[V]) {
+  m.put(at, P, H);
+  block_sync();
+  if (tiles > 1) {
+    if (at.wave == 0) {
+      float tp[V], th[V];
+      m.template all<kReverse>(at.lane, tp, th);
+      look_back<V>(slots, at.link, D, at.c, tp, th, x);
+#pragma unroll
+      for (int v = 0; v < V; ++v) m.in[at.lane * V + v] = x[v];
+    }
+    block_sync();
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = m.in[at.lane * V + v];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = 0.0f;
+  }
+  m.template take<kReverse>(at, x);
+}
+
+// h (kOut) and the last and saved states.
 template <typename T, int V, bool kOut>
-__global__ __launch_bounds__(kBlock) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
-                                                            float2* agg, const float* carry) {
-  constexpr int S = kSteps<T>;
-  __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V];
+__global__ __launch_bounds__(kBlock, 4) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
+                                                               int64_t tiles, uint32_t* tickets,
+                                                               uint64_t* slots) {
+  constexpr int S = kFwdSteps<T>;
+  __shared__ Maps<V> maps;
   const int64_t D = a.D;
-  const Place p = place_of<T, V>(D, groups, blockIdx.x);
+  const Place p = place_of<V, S, false>(D, groups, tiles, tickets);
+  if (p.link >= tiles) return;
   Raw<T, V> x[S], gi[S], gr[S];
   load_rows<T, V, S>(a.r, a.r_row, p.t0, a.seqs.tokens, p.c, gr);
   load_rows<T, V, S>(a.i, a.i_row, p.t0, a.seqs.tokens, p.c, gi);
@@ -103,7 +264,7 @@ __global__ __launch_bounds__(kBlock) void recurrence_kernel(RecurrenceArgs a, in
         for (int v = 0; v < V; ++v) b[s][v] = __builtin_fmaf(da[s][v], h0[v], b[s][v]);
       }
   }
-  float P[V], H[V];
+  float P[V], H[V], h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
 #pragma unroll
@@ -113,32 +274,13 @@ __global__ __launch_bounds__(kBlock) void recurrence_kernel(RecurrenceArgs a, in
       if (span.first >> s & 1) P[v] = 0.0f, H[v] = b[s][v];
       else H[v] = __builtin_fmaf(da[s][v], H[v], b[s][v]), P[v] *= da[s][v];
     }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sp[p.wave][p.lane * V + v] = P[v], sh[p.wave][p.lane * V + v] = H[v];
-  block_sync();
-  if constexpr (!kOut) {
-    if (p.wave == 0 && p.active) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float pp = 1.0f, hh = 0.0f;
-        for (int w = 0; w < kWaves; ++w) {
-          const float q = sp[w][p.lane * V + v];
-          hh = join(q, sh[w][p.lane * V + v], hh);
-          pp = q == 0.0f ? 0.0f : pp * q;
-        }
-        agg[p.tile * D + p.c + v] = make_float2(pp, hh);
-      }
-    }
-    return;
-  }
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = carry ? carry[p.tile * D + p.c + v] : 0.0f;
-    for (int w = 0; w < p.wave; ++w)
-      h[v] = join(sp[w][p.lane * V + v], sh[w][p.lane * V + v], h[v]);
-  }
+  chain<V, false>(p, maps, slots, tiles, D, P, H, h);
   if (!p.active) return;
+  if (a.saved && p.t0 % kSavedTokens == 0 && p.t0 < a.seqs.tokens) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.saved[p.t0 / kSavedTokens * D + p.c + v] = h[v];
+  }
+  if constexpr (!kOut) return;
   T* out = static_cast<T*>(a.h) + p.t0 * D + p.c;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -154,33 +296,6 @@ __global__ __launch_bounds__(kBlock) void recurrence_kernel(RecurrenceArgs a, in
   }
 }
 
-// carry[tile] = the state before it, over the tiles in order (backward: behind it, from
-// the last one back).
-__global__ __launch_bounds__(64) void recurrence_carry_kernel(const float2* __restrict__ agg,
-                                                              float* __restrict__ carry,
-                                                              int64_t tiles, int64_t D,
-                                                              int backward) {
-  const int64_t c = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (c >= D) return;
-  float h = 0.0f;
-  for (int64_t j0 = 0; j0 < tiles; j0 += 16) {
-    float2 u[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int64_t k = j0 + j < tiles ? j0 + j : tiles - 1;
-      u[j] = agg[(backward ? tiles - 1 - k : k) * D + c];
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int64_t k = j0 + j;
-      if (k < tiles) {
-        carry[(backward ? tiles - 1 - k : k) * D + c] = h;
-        h = join(u[j].x, u[j].y, h);
-      }
-    }
-  }
-}
-
 // Sequences without tokens: to = from, or zero.
 __global__ __launch_bounds__(256) void empty_states_kernel(Sequences seqs, const float* from,
                                                            float* to, int64_t D) {
@@ -189,28 +304,30 @@ __global__ __launch_bounds__(256) void empty_states_kernel(Sequences seqs, const
   for (int64_t c = threadIdx.x; c < D; c += 256) to[q * D + c] = from ? from[q * D + c] : 0.0f;
 }
 
-// ragg: [tiles, D] (P, H) of each tile's map of psi, written without kOut; rcarry: psi behind
-// each tile (null: zero); saved: the state before each tile (null: zero); part: [tiles, D]
-// the tiles' sums of dA.
-template <typename T, int V, bool kOut>
-__global__ __launch_bounds__(kBlock) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
-                                                                int64_t groups, float2* ragg,
-                                                                const float* rcarry,
+// saved: the state before each tile (null: zero); part: [tiles, D] the tiles' sums of dA.
+template <typename T, int V>
+__global__ __launch_bounds__(kBlock, BW) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
+                                                                int64_t groups, int64_t tiles,
+                                                                uint32_t* tickets, uint64_t* slots,
                                                                 const float* saved, float* part) {
-  constexpr int S = kSteps<T>;
-  __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], sq[kWaves][64 * V];
+  constexpr int S = kBwdSteps<T>;
+  static_assert(S * kWaves == kSavedTokens, "a saved state for each tile");
+  __shared__ Maps<V> fwd, rev;
   const int64_t D = a.D;
-  const Place p = place_of<T, V>(D, groups, blockIdx.x);
+  const Place p = place_of<V, S, true>(D, groups, tiles, tickets);
+  if (p.link >= tiles) return;
+  const int64_t tile = tiles - 1 - p.link;
   Raw<T, V> x[S], gi[S], gr[S], dh[S];
   load_rows<T, V, S>(a.r, a.r_row, p.t0, a.seqs.tokens, p.c, gr);
   load_rows<T, V, S>(d.dh, D, p.t0, a.seqs.tokens, p.c, dh);
-  if constexpr (kOut) {
-    load_rows<T, V, S>(a.i, a.i_row, p.t0, a.seqs.tokens, p.c, gi);
-    load_rows<T, V, S>(a.x, a.x_row, p.t0, a.seqs.tokens, p.c, x);
-  }
-  float rate[V];
+  load_rows<T, V, S>(a.i, a.i_row, p.t0, a.seqs.tokens, p.c, gi);
+  load_rows<T, V, S>(a.x, a.x_row, p.t0, a.seqs.tokens, p.c, x);
+  float rate[V], h[V], psi[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) rate[v] = a.A[p.c + v];
+  for (int v = 0; v < V; ++v) {
+    rate[v] = a.A[p.c + v];
+    h[v] = saved ? saved[tile * D + p.c + v] : 0.0f;
+  }
   const Span span = span_of<S>(a.seqs, p.t0);
   auto dstate = [&](int s, int v) {
     return d.dlast ? d.dlast[span.sequence(s) * D + p.c + v] : 0.0f;
@@ -230,28 +347,10 @@ __global__ __launch_bounds__(kBlock) void recurrence_bwd_kernel(RecurrenceArgs a
       H[v] = da[s][v] * (dh[s].get(v) + H[v]);
       P[v] = P[v] == 0.0f ? 0.0f : P[v] * da[s][v];
     }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sp[p.wave][p.lane * V + v] = P[v], sh[p.wave][p.lane * V + v] = H[v];
-  if constexpr (!kOut) {
-    block_sync();
-    if (p.wave == 0 && p.active) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float pp = 1.0f, hh = 0.0f;
-        for (int w = kWaves - 1; w >= 0; --w) {
-          const float q = sp[w][p.lane * V + v];
-          hh = join(q, sh[w][p.lane * V + v], hh);
-          pp = q == 0.0f ? 0.0f : pp * q;
-        }
-        ragg[p.tile * D + p.c + v] = make_float2(pp, hh);
-      }
-    }
-    return;
-  }
   // the states: the wavefront's own map first, joined behind the earlier ones'
-  float hp[S][V];        // h_{t-1}
-  float Pf[V], Hf[V];
+  float hp[S][V];        // the input term, then h_{t-1}
   {
+    float Pf[V], Hf[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) Pf[v] = 1.0f, Hf[v] = 0.0f;
 #pragma unroll
@@ -266,27 +365,12 @@ __global__ __launch_bounds__(kBlock) void recurrence_bwd_kernel(RecurrenceArgs a
         } else {
           Hf[v] = __builtin_fmaf(da[s][v], Hf[v], b), Pf[v] *= da[s][v];
         }
-        hp[s][v] = b;    // for now: the input term
+        hp[s][v] = b;
       }
+    fwd.put(p, Pf, Hf);
   }
-  float psi[V], h[V];
-  block_sync();
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    psi[v] = rcarry ? rcarry[p.tile * D + p.c + v] : 0.0f;
-    for (int w = kWaves - 1; w > p.wave; --w)
-      psi[v] = join(sp[w][p.lane * V + v], sh[w][p.lane * V + v], psi[v]);
-  }
-  block_sync();
-#pragma unroll
-  for (int v = 0; v < V; ++v) sp[p.wave][p.lane * V + v] = Pf[v], sh[p.wave][p.lane * V + v] = Hf[v];
-  block_sync();
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = saved ? saved[p.tile * D + p.c + v] : 0.0f;
-    for (int w = 0; w < p.wave; ++w)
-      h[v] = join(sp[w][p.lane * V + v], sh[w][p.lane * V + v], h[v]);
-  }
+  chain<V, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
+  fwd.template take<false>(p, h);
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -332,15 +416,16 @@ __global__ __launch_bounds__(kBlock) void recurrence_bwd_kernel(RecurrenceArgs a
       }
     }
   }
+  block_sync();
 #pragma unroll
-  for (int v = 0; v < V; ++v) sq[p.wave][p.lane * V + v] = sum[v];
+  for (int v = 0; v < V; ++v) rev.p[p.wave][p.lane * V + v] = sum[v];
   block_sync();
   if (p.wave == 0 && p.active) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float t = 0.0f;
-      for (int w = 0; w < kWaves; ++w) t += sq[w][p.lane * V + v];
-      part[p.tile * D + p.c + v] = t;
+      for (int w = 0; w < kWaves; ++w) t += rev.p[w][p.lane * V + v];
+      part[tile * D + p.c + v] = t;
     }
   }
 }
@@ -398,8 +483,8 @@ __global__ __launch_bounds__(256) void recurrence_zero_kernel(float* p, int64_t 
   if (i < n) p[i] = 0.0f;
 }
 
-int64_t tile_of(mssm_dtype dtype) {
-  return dtype == MSSM_BFLOAT16 ? kTile<uint16_t> : kTile<float>;
+int64_t fwd_tile(mssm_dtype dtype) {
+  return kWaves * (dtype == MSSM_BFLOAT16 ? kFwdSteps<uint16_t> : kFwdSteps<float>);
 }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -419,21 +504,26 @@ hipError_t with_type(mssm_dtype dtype, int64_t D, F f) {
 RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool saved,
                                mssm_dtype dtype) {
   RecurrencePlan p;
-  p.tiles = (tokens + tile_of(dtype) - 1) / tile_of(dtype);
+  p.tiles = (tokens + fwd_tile(dtype) - 1) / fwd_tile(dtype);
+  p.bwd_tiles = (tokens + kSavedTokens - 1) / kSavedTokens;
   p.groups = (D + (D > 64 ? 127 : 63)) / (D > 64 ? 128 : 64);
-  const size_t states = static_cast<size_t>(p.tiles) * D;
-  p.saved_bytes = states * sizeof(float);
+  const size_t states = static_cast<size_t>(p.bwd_tiles) * D * sizeof(float);
+  p.saved_bytes = states;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += align256(bytes);
     return at;
   };
-  if (p.tiles > 1) p.agg = take(states * sizeof(float2));
-  if (p.tiles > 1 && !saved) p.states = take(states * sizeof(float));
+  // the two directions follow one another and share the counters and slots
+  const int64_t links = backward ? p.bwd_tiles : p.tiles;
+  if (links > 1) {
+    p.tickets = take(static_cast<size_t>(p.groups) * kTicketStride * sizeof(uint32_t));
+    p.slots = take(static_cast<size_t>(links) * D * sizeof(uint64_t));
+  }
   if (backward) {
-    if (p.tiles > 1) p.rcarry = take(states * sizeof(float));
-    p.part = take(states * sizeof(float));
+    if (p.bwd_tiles > 1 && !saved) p.states = take(states);
+    p.part = take(states);
   }
   p.bytes = off;
   return p;
@@ -456,47 +546,45 @@ hipError_t empty_states(const Sequences& s, const float* from, float* to, int64_
   return hipSuccess;
 }
 
-// The states before every tile, into carry.
-hipError_t tile_states(const RecurrenceArgs& a, const RecurrencePlan& p, char* ws, float* carry,
-                       hipStream_t stream) {
+hipError_t clear(const RecurrencePlan& p, int64_t links, int64_t D, char* ws, hipStream_t stream) {
+  const int64_t n = (links * D + 1) / 2;             // (slots end at a multiple of 256 bytes)
+  int64_t blocks = (n + 255) / 256;
+  const int64_t least = (p.groups + 255) / 256;
+  if (blocks > 2048) blocks = 2048;
+  if (blocks < least) blocks = least;
+  hipLaunchKernelGGL(recurrence_clear_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0,
+                     stream, reinterpret_cast<uint4*>(ws + p.slots), n,
+                     reinterpret_cast<uint32_t*>(ws + p.tickets), p.groups);
+  return hipGetLastError();
+}
+
+// h, last and saved states; kOut false: the saved states alone.
+template <bool kOut>
+hipError_t forward(const RecurrenceArgs& a, const RecurrencePlan& p, char* ws, hipStream_t stream) {
+  if (p.tiles > 1) {
+    const hipError_t e = clear(p, p.tiles, a.D, ws, stream);
+    if (e != hipSuccess) return e;
+  }
   const dim3 grid(static_cast<uint32_t>(p.tiles * p.groups));
-  float2* agg = reinterpret_cast<float2*>(ws + p.agg);
-  const hipError_t e = with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_kernel<decltype(t), decltype(v)::value, false>), grid,
-                       dim3(kBlock), 0, stream, a, p.groups, agg, nullptr);
+  return with_type(a.dtype, a.D, [&](auto t, auto v) {
+    hipLaunchKernelGGL((recurrence_kernel<decltype(t), decltype(v)::value, kOut>), grid,
+                       dim3(kBlock), 0, stream, a, p.groups, p.tiles,
+                       reinterpret_cast<uint32_t*>(ws + p.tickets),
+                       reinterpret_cast<uint64_t*>(ws + p.slots));
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(recurrence_carry_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64)), dim3(64),
-                     0, stream, agg, carry, p.tiles, a.D, 0);
-  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_recurrence(const RecurrenceArgs& a, const RecurrencePlan& p, void* ws_,
+hipError_t launch_recurrence(const RecurrenceArgs& a, const RecurrencePlan& p, void* ws,
                              hipStream_t stream) {
-  char* ws = static_cast<char*>(ws_);
   if (a.last && (a.seqs.offsets || a.seqs.L == 0)) {
     const hipError_t e = empty_states(a.seqs, a.state, a.last, a.D, stream);
     if (e != hipSuccess) return e;
   }
   if (a.seqs.tokens == 0) return hipSuccess;
-  float* carry = nullptr;
-  if (p.tiles > 1) {
-    carry = a.saved ? a.saved : reinterpret_cast<float*>(ws + p.states);
-    const hipError_t e = tile_states(a, p, ws, carry, stream);
-    if (e != hipSuccess) return e;
-  } else if (a.saved) {
-    hipLaunchKernelGGL(recurrence_zero_kernel, dim3(static_cast<uint32_t>((a.D + 255) / 256)),
-                       dim3(256), 0, stream, a.saved, a.D);
-  }
-  const dim3 grid(static_cast<uint32_t>(p.tiles * p.groups));
-  return with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_kernel<decltype(t), decltype(v)::value, true>), grid,
-                       dim3(kBlock), 0, stream, a, p.groups, nullptr, carry);
-    return hipGetLastError();
-  });
+  return forward<true>(a, p, static_cast<char*>(ws), stream);
 }
 
 hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads& d,
@@ -511,37 +599,31 @@ hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads&
                        dim3(256), 0, stream, d.dA, a.D);
     return hipGetLastError();
   }
-  const dim3 grid(static_cast<uint32_t>(p.tiles * p.groups));
-  const float* states = nullptr;
-  float* rcarry = nullptr;
-  float* part = reinterpret_cast<float*>(ws + p.part);
-  if (p.tiles > 1) {
-    float2* agg = reinterpret_cast<float2*>(ws + p.agg);
-    states = a.saved;
-    if (!states) {
-      float* to = reinterpret_cast<float*>(ws + p.states);
-      const hipError_t e = tile_states(a, p, ws, to, stream);
-      if (e != hipSuccess) return e;
-      states = to;
+  const float* saved = nullptr;
+  hipError_t e;
+  if (p.bwd_tiles > 1) {
+    saved = a.saved;
+    if (!saved) {
+      RecurrenceArgs f = a;
+      f.saved = reinterpret_cast<float*>(ws + p.states);
+      f.last = nullptr;
+      if ((e = forward<false>(f, p, ws, stream)) != hipSuccess) return e;
+      saved = f.saved;
     }
-    rcarry = reinterpret_cast<float*>(ws + p.rcarry);
-    const hipError_t e = with_type(a.dtype, a.D, [&](auto t, auto v) {
-      hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value, false>), grid,
-                         dim3(kBlock), 0, stream, a, d, p.groups, agg, nullptr, nullptr, nullptr);
-      return hipGetLastError();
-    });
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(recurrence_carry_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64)),
-                       dim3(64), 0, stream, agg, rcarry, p.tiles, a.D, 1);
+    if ((e = clear(p, p.bwd_tiles, a.D, ws, stream)) != hipSuccess) return e;
   }
-  const hipError_t e = with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value, true>), grid,
-                       dim3(kBlock), 0, stream, a, d, p.groups, nullptr, rcarry, states, part);
+  float* part = reinterpret_cast<float*>(ws + p.part);
+  const dim3 grid(static_cast<uint32_t>(p.bwd_tiles * p.groups));
+  e = with_type(a.dtype, a.D, [&](auto t, auto v) {
+    hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value>), grid, dim3(kBlock),
+                       0, stream, a, d, p.groups, p.bwd_tiles,
+                       reinterpret_cast<uint32_t*>(ws + p.tickets),
+                       reinterpret_cast<uint64_t*>(ws + p.slots), saved, part);
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(recurrence_sum_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64)),
-                     dim3(1024), 0, stream, part, p.tiles, a.D, d.dA);
+                     dim3(1024), 0, stream, part, p.bwd_tiles, a.D, d.dA);
   return hipGetLastError();
 }
 

@@ -507,7 +507,7 @@ struct RecurrenceArgs {
   const float* state = nullptr;   // [seqs, D] or null
   void* h = nullptr;              // [tokens, D]
   float* last = nullptr;          // [seqs, D] or null
-  float* saved = nullptr;         // the state before each tile [tiles, D], or null
+  float* saved = nullptr;         // the state before every 64th token, or null
   mssm_dtype dtype = MSSM_FLOAT32;
 };
 struct RecurrenceGrads {
@@ -519,10 +519,10 @@ struct RecurrenceGrads {
   float* dA = nullptr;            // [D]
   float* dstate = nullptr;        // [seqs, D] or null
 };
-// Tiles of tokens by groups of channels, and the workspace.
+// Tiles of tokens (forward and backward) by groups of channels, and the workspace.
 struct RecurrencePlan {
-  int64_t tiles = 0, groups = 0;
-  size_t agg = 0, states = 0, rcarry = 0, part = 0;
+  int64_t tiles = 0, bwd_tiles = 0, groups = 0;
+  size_t tickets = 0, slots = 0, states = 0, part = 0;
   size_t saved_bytes = 0;
   size_t bytes = 0;
 };
