@@ -614,7 +614,7 @@ mssm_status mssm_layer_norm_bwd(const void *dy, const void *dsum, const void *x,
  * its first).  Offsets outside 0 .. L are taken as 0 or L; tokens before the first and behind the
  * last sequence may hold anything, and their outputs and gradients are left as they were.
  * What is not finite in a sequence stays in that sequence and channel.  Any element-aligned
- * address.  D below 2^28.  Sums over tokens or rows run in a fixed order, so results are
+ * address.  D is below 2^24; so are rows, but in the single-token calls.  Sums over tokens or rows run in a fixed order, so results are
  * deterministic.  tokens, seqs or D equal to zero are valid: last states and the parameters'
  * gradients are still set.
  */

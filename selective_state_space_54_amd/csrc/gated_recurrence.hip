@@ -30,7 +30,10 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kSavedTokens = 64;          // a saved state for every so many tokens
-constexpr int kLookBack = 8;              // tiles looked at together
+#ifndef LB
+#define LB 8
+#endif
+constexpr int kLookBack = LB;              // tiles looked at together
 constexpr int kMaxPolls = 1 << 22;
 constexpr int64_t kTicketStride = 32;     // counters on cache lines of their own
 #ifndef BW
@@ -156,15 +159,26 @@ __device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t til
   return p;
 }
 
-// S rows of a tensor from token t0 on, each lane its V channels.
+// S rows of a tensor from token t0 on as a buffer: addresses are a lane's own part and a wave-uniform
+// one for the row.  step: bytes from row to row; bytes: of a row.
+template <int S>
+__device__ __forceinline__ buf_t rows_from(const void* base, int64_t t0, int64_t step,
+                                           int64_t bytes) {
+  return make_buf(static_cast<const char*>(base) + t0 * step,
+                  static_cast<uint32_t>((S - 1) * step + bytes));
+}
+
+// S rows from token t0 on, each lane its V channels; rows past the last token repeat it.
 template <typename T, int V, int S>
-__device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t t0, int64_t tokens,
-                                          int c, Raw<T, V> (&v)[S]) {
+__device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t D, int64_t t0,
+                                          int64_t tokens, int c, Raw<T, V> (&v)[S]) {
+  const int64_t step = row * static_cast<int64_t>(sizeof(T));
+  const int64_t left = tokens - t0;
+  const buf_t r = rows_from<S>(base, left > 0 ? t0 : tokens - 1, step, D * sizeof(T));
+  const int last = left > S ? S - 1 : left > 0 ? static_cast<int>(left) - 1 : 0;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int64_t t = t0 + s < tokens ? t0 + s : tokens - 1;
-    v[s].load(static_cast<const T*>(base) + t * row + c);
-  }
+  for (int s = 0; s < S; ++s)
+    v[s].load(r, c * static_cast<int>(sizeof(T)), (s < last ? s : last) * static_cast<int>(step));
 }
 
 // What the wavefronts of a block tell one another.
@@ -238,42 +252,57 @@ __global__ __launch_bounds__(kBlock, 4) void recurrence_kernel(RecurrenceArgs a,
   const Place p = place_of<V, S, false>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   Raw<T, V> x[S], gi[S], gr[S];
-  load_rows<T, V, S>(a.r, a.r_row, p.t0, a.seqs.tokens, p.c, gr);
-  load_rows<T, V, S>(a.i, a.i_row, p.t0, a.seqs.tokens, p.c, gi);
-  load_rows<T, V, S>(a.x, a.x_row, p.t0, a.seqs.tokens, p.c, x);
+  load_rows<T, V, S>(a.r, a.r_row, D, p.t0, a.seqs.tokens, p.c, gr);
+  load_rows<T, V, S>(a.i, a.i_row, D, p.t0, a.seqs.tokens, p.c, gi);
+  load_rows<T, V, S>(a.x, a.x_row, D, p.t0, a.seqs.tokens, p.c, x);
   float rate[V];
+  bool near = true;
 #pragma unroll
-  for (int v = 0; v < V; ++v) rate[v] = a.A[p.c + v];
+  for (int v = 0; v < V; ++v) {
+    rate[v] = a.A[p.c + v];
+    near = near && rate[v] > kSeries;
+  }
   const Span span = span_of<S>(a.seqs, p.t0);
 
   float da[S][V], b[S][V];
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Decay d = decay_of(rate[v], gr[s].get(v));
-      da[s][v] = d.a;
-      b[s][v] = sqrt_(d.m2) * sigmoid(gi[s].get(v)) * x[s].get(v);
-    }
-  if (span.borders && a.state) {
+  auto gates = [&](auto near_) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < S; ++s)
-      if (span.first >> s & 1) {
-        const float* h0 = a.state + span.sequence(s) * D + p.c;
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[s][v] = __builtin_fmaf(da[s][v], h0[v], b[s][v]);
+      for (int v = 0; v < V; ++v) {
+        constexpr bool kNear = decltype(near_)::value;
+        const float q = decay_of<kNear>(rate[v] * sigmoid(gr[s].get(v)));
+        da[s][v] = decay<kNear>(q);
+        b[s][v] = sqrt_(one_minus_square<kNear>(q)) * (sigmoid(gi[s].get(v)) * x[s].get(v));
       }
-  }
+  };
+  if (__all(near)) gates(std::true_type());
+  else gates(std::false_type());
+
   float P[V], H[V], h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
+  if (!span.borders) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (span.first >> s & 1) P[v] = 0.0f, H[v] = b[s][v];
-      else H[v] = __builtin_fmaf(da[s][v], H[v], b[s][v]), P[v] *= da[s][v];
+      for (int v = 0; v < V; ++v) H[v] = __builtin_fmaf(da[s][v], H[v], b[s][v]), P[v] *= da[s][v];
+  } else {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (span.first >> s & 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (a.state)
+            b[s][v] = __builtin_fmaf(da[s][v], a.state[span.sequence(s) * D + p.c + v], b[s][v]);
+          P[v] = 0.0f, H[v] = b[s][v];
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) H[v] = __builtin_fmaf(da[s][v], H[v], b[s][v]), P[v] *= da[s][v];
+      }
     }
+  }
   chain<V, false>(p, maps, slots, tiles, D, P, H, h);
   if (!p.active) return;
   if (a.saved && p.t0 % kSavedTokens == 0 && p.t0 < a.seqs.tokens) {
@@ -281,17 +310,29 @@ __global__ __launch_bounds__(kBlock, 4) void recurrence_kernel(RecurrenceArgs a,
     for (int v = 0; v < V; ++v) a.saved[p.t0 / kSavedTokens * D + p.c + v] = h[v];
   }
   if constexpr (!kOut) return;
-  T* out = static_cast<T*>(a.h) + p.t0 * D + p.c;
+  const int step = static_cast<int>(D * sizeof(T));
+  const buf_t out = rows_from<S>(a.h, p.t0, step, step);
+  const int at = p.c * static_cast<int>(sizeof(T));
+  if (!span.borders) {
+    if (!span.valid) return;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < S; ++s) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      h[v] = span.first >> s & 1 ? b[s][v] : __builtin_fmaf(da[s][v], h[v], b[s][v]);
-    if ((span.valid >> s & 1) && p.t0 + s < a.seqs.tokens) Raw<T, V>::store(out + s * D, h);
-    if (a.last && (span.last >> s & 1)) {
-      float* to = a.last + span.sequence(s) * D + p.c;
+      for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(da[s][v], h[v], b[s][v]);
+      Raw<T, V>::store(out, at, s * step, h);
+    }
+  } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) to[v] = h[v];
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        h[v] = span.first >> s & 1 ? b[s][v] : __builtin_fmaf(da[s][v], h[v], b[s][v]);
+      if (span.valid >> s & 1) Raw<T, V>::store(out, at, s * step, h);
+      if (a.last && (span.last >> s & 1)) {
+        float* to = a.last + span.sequence(s) * D + p.c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) to[v] = h[v];
+      }
     }
   }
 }
@@ -317,105 +358,139 @@ __global__ __launch_bounds__(kBlock, BW) void recurrence_bwd_kernel(RecurrenceAr
   const Place p = place_of<V, S, true>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   const int64_t tile = tiles - 1 - p.link;
-  Raw<T, V> x[S], gi[S], gr[S], dh[S];
-  load_rows<T, V, S>(a.r, a.r_row, p.t0, a.seqs.tokens, p.c, gr);
-  load_rows<T, V, S>(d.dh, D, p.t0, a.seqs.tokens, p.c, dh);
-  load_rows<T, V, S>(a.i, a.i_row, p.t0, a.seqs.tokens, p.c, gi);
-  load_rows<T, V, S>(a.x, a.x_row, p.t0, a.seqs.tokens, p.c, x);
-  float rate[V], h[V], psi[V];
+  float rate[V], h[V], psi[V], sum[V];
+  Raw<T, V> x[S], dh[S], gi[S], gr[S];
+  load_rows<T, V, S>(a.r, a.r_row, D, p.t0, a.seqs.tokens, p.c, gr);
+  load_rows<T, V, S>(a.i, a.i_row, D, p.t0, a.seqs.tokens, p.c, gi);
+  load_rows<T, V, S>(a.x, a.x_row, D, p.t0, a.seqs.tokens, p.c, x);
+  load_rows<T, V, S>(d.dh, D, D, p.t0, a.seqs.tokens, p.c, dh);
+  bool near = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     rate[v] = a.A[p.c + v];
+    near = near && rate[v] > kSeries;
     h[v] = saved ? saved[tile * D + p.c + v] : 0.0f;
+    sum[v] = 0.0f;
   }
   const Span span = span_of<S>(a.seqs, p.t0);
-  auto dstate = [&](int s, int v) {
+  auto state = [&](int s, int v) {
+    return a.state ? a.state[span.sequence(s) * D + p.c + v] : 0.0f;
+  };
+  auto dlast = [&](int s, int v) {
     return d.dlast ? d.dlast[span.sequence(s) * D + p.c + v] : 0.0f;
   };
 
-  float P[V], H[V];      // psi before the wavefront's tokens = P psi behind them + H
-#pragma unroll
-  for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
-  float da[S][V];
-#pragma unroll
-  for (int s = S - 1; s >= 0; --s)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      da[s][v] = decay_of(rate[v], gr[s].get(v)).a;
-      if (p.t0 + s >= a.seqs.tokens) continue;
-      if (span.last >> s & 1) P[v] = 0.0f, H[v] = dstate(s, v);
-      H[v] = da[s][v] * (dh[s].get(v) + H[v]);
-      P[v] = P[v] == 0.0f ? 0.0f : P[v] * da[s][v];
-    }
-  // the states: the wavefront's own map first, joined behind the earlier ones'
-  float hp[S][V];        // the input term, then h_{t-1}
-  {
-    float Pf[V], Hf[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) Pf[v] = 1.0f, Hf[v] = 0.0f;
+  // (the wavefronts of a block have the same channels: all of them take the same branch)
+  auto work = [&](auto near_) __attribute__((always_inline)) {
+    constexpr bool kNear = decltype(near_)::value;
+    float sg[S][V], e[S][V], bb[S][V];     // sigmoid(r), the decay; the input term, then h_{t-1}
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Decay k = decay_of(rate[v], gr[s].get(v));
-        const float b = sqrt_(k.m2) * sigmoid(gi[s].get(v)) * x[s].get(v);
-        if (span.first >> s & 1) {
-          const float h0 = a.state ? a.state[span.sequence(s) * D + p.c + v] : 0.0f;
-          Pf[v] = 0.0f, Hf[v] = __builtin_fmaf(da[s][v], h0, b);
-        } else {
-          Hf[v] = __builtin_fmaf(da[s][v], Hf[v], b), Pf[v] *= da[s][v];
+        sg[s][v] = sigmoid(gr[s].get(v));
+        e[s][v] = decay_of<kNear>(rate[v] * sg[s][v]);
+        bb[s][v] = sqrt_(one_minus_square<kNear>(e[s][v])) * (sigmoid(gi[s].get(v)) * x[s].get(v));
+      }
+#pragma unroll
+    for (int s = 0; s < S; ++s) x[s].keep(), gi[s].keep();      // widened again below
+
+    // The wavefront's maps: of the state, and of psi (from behind its tokens to before them).
+    float P[V], H[V], Pf[V], Hf[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = Pf[v] = 1.0f, H[v] = Hf[v] = 0.0f;
+    if (!span.borders) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float k = decay<kNear>(e[s][v]);
+          Hf[v] = __builtin_fmaf(k, Hf[v], bb[s][v]), Pf[v] *= k;
+          const float q = decay<kNear>(e[S - 1 - s][v]);
+          H[v] = q * (dh[S - 1 - s].get(v) + H[v]);
         }
-        hp[s][v] = b;
-      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) P[v] = Pf[v];
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float k = decay<kNear>(e[s][v]);
+          if (span.first >> s & 1) Pf[v] = 0.0f, Hf[v] = __builtin_fmaf(k, state(s, v), bb[s][v]);
+          else Hf[v] = __builtin_fmaf(k, Hf[v], bb[s][v]), Pf[v] *= k;
+        }
+#pragma unroll
+      for (int s = S - 1; s >= 0; --s)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float k = decay<kNear>(e[s][v]);
+          if (span.last >> s & 1) P[v] = 0.0f, H[v] = dlast(s, v);
+          H[v] = k * (dh[s].get(v) + H[v]);
+          P[v] = P[v] == 0.0f ? 0.0f : P[v] * k;
+        }
+    }
     fwd.put(p, Pf, Hf);
-  }
-  chain<V, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
-  fwd.template take<false>(p, h);
+    chain<V, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
+    fwd.template take<false>(p, h);
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (span.first >> s & 1) h[v] = a.state ? a.state[span.sequence(s) * D + p.c + v] : 0.0f;
-      const float b = hp[s][v];
-      hp[s][v] = h[v];
-      h[v] = __builtin_fmaf(da[s][v], h[v], b);
-    }
-  float sum[V];
+      for (int v = 0; v < V; ++v) {
+        if (span.borders && (span.first >> s & 1)) h[v] = state(s, v);
+        const float b = bb[s][v];
+        bb[s][v] = h[v];
+        h[v] = __builtin_fmaf(decay<kNear>(e[s][v]), h[v], b);
+      }
+    const int step = static_cast<int>(D * sizeof(T));
+    const buf_t to_x = rows_from<S>(d.dx, p.t0, step, step), to_i = rows_from<S>(d.di, p.t0, step, step),
+                to_r = rows_from<S>(d.dr, p.t0, step, step);
+    // (lanes that copy another's channels write out of bounds, which is dropped)
+    const int at = p.active ? p.c * static_cast<int>(sizeof(T)) : S * step;
+    // Gradients of token s; psi goes from behind it to before it.
+    auto token = [&](int s) __attribute__((always_inline)) {
+      float dx[V], di[V], dr[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+      for (int v = 0; v < V; ++v) {
+        const float lam = dh[s].get(v) + psi[v];
+        const float k = decay<kNear>(e[s][v]), m2 = one_minus_square<kNear>(e[s][v]);
+        const float w = m2 > 0.0f ? rsqrt_(m2) : 0.0f;              // 1 / m
+        const float lm = lam * (m2 * w), g = sigmoid(gi[s].get(v)), gx = g * x[s].get(v);
+        dx[v] = lm * g;
+        di[v] = lm * gx * (1.0f - g);
+        psi[v] = k * lam;
+        const float es = psi[v] * __builtin_fmaf(-gx * k, w, bb[s][v]) * sg[s][v];
+        dr[v] = es * rate[v] * (1.0f - sg[s][v]);
+        sum[v] += es;
+      }
+      Raw<T, V>::store(to_x, at, s * step, dx);
+      Raw<T, V>::store(to_i, at, s * step, di);
+      Raw<T, V>::store(to_r, at, s * step, dr);
+    };
+    if (!span.borders) {
+      if (span.valid) {
 #pragma unroll
-  for (int s = S - 1; s >= 0; --s) {
-    if (p.t0 + s >= a.seqs.tokens) continue;
-    const bool valid = span.valid >> s & 1;
-    float dx[V], di[V], dr[V];
+        for (int s = S - 1; s >= 0; --s) token(s);
+      }
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (span.last >> s & 1) psi[v] = dstate(s, v);
-      const float lam = dh[s].get(v) + psi[v];
-      const Decay k = decay_of(rate[v], gr[s].get(v));
-      const float w = k.m2 > 0.0f ? rsqrt_(k.m2) : 0.0f;          // 1 / m
-      const float m = k.m2 * w;
-      const float g = sigmoid(gi[s].get(v)), gx = g * x[s].get(v);
-      dx[v] = lam * m * g;
-      di[v] = lam * m * gx * (1.0f - g);
-      const float e = lam * k.a * (hp[s][v] - gx * k.a * w);
-      const float es = e * k.s;
-      dr[v] = es * rate[v] * (1.0f - k.s);
-      if (valid) sum[v] += es;
-      psi[v] = k.a * lam;
-    }
-    if (p.active && valid) {
-      const int64_t at = (p.t0 + s) * D + p.c;
-      Raw<T, V>::store(static_cast<T*>(d.dx) + at, dx);
-      Raw<T, V>::store(static_cast<T*>(d.di) + at, di);
-      Raw<T, V>::store(static_cast<T*>(d.dr) + at, dr);
-      if (d.dstate && (span.first >> s & 1)) {
-        float* to = d.dstate + span.sequence(s) * D + p.c;
+      for (int s = S - 1; s >= 0; --s) {
+        if (!(span.valid >> s & 1)) continue;
+        if (span.last >> s & 1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) to[v] = psi[v];
+          for (int v = 0; v < V; ++v) psi[v] = dlast(s, v);
+        }
+        token(s);
+        if (d.dstate && p.active && (span.first >> s & 1)) {
+          float* to = d.dstate + span.sequence(s) * D + p.c;
+#pragma unroll
+          for (int v = 0; v < V; ++v) to[v] = psi[v];
+        }
       }
     }
-  }
+  };
+  if (__all(near)) work(std::true_type());
+  else work(std::false_type());
   block_sync();
 #pragma unroll
   for (int v = 0; v < V; ++v) rev.p[p.wave][p.lane * V + v] = sum[v];
@@ -462,9 +537,9 @@ __global__ __launch_bounds__(256) void recurrence_step_kernel(RecurrenceArgs a, 
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Decay d = decay_of(a.A[c + v], gr.get(v));
-    const float b = sqrt_(d.m2) * sigmoid(gi.get(v)) * x.get(v);
-    h[v] = __builtin_fmaf(d.a, state[q * a.D + c + v], b);
+    const float k = decay_of<false>(a.A[c + v] * sigmoid(gr.get(v)));
+    const float b = sqrt_(one_minus_square<false>(k)) * (sigmoid(gi.get(v)) * x.get(v));
+    h[v] = __builtin_fmaf(decay<false>(k), state[q * a.D + c + v], b);
   }
   // (where V does not divide D, the last thread's first channels are another's)
   if (c == c0) {

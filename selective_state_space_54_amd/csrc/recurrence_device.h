@@ -5,6 +5,9 @@
 #include "scan_device.h"
 #include "sequences.h"
 
+// Fused multiply-adds are written out: every kernel forms the same numbers, bit for bit.
+#pragma clang fp contract(off)
+
 namespace mssm {
 
 // V adjacent values as they lie in memory (any element-aligned address).
@@ -16,9 +19,26 @@ struct Raw {
     if constexpr (sizeof(T) * V < 4) w[0] = *p;
     else __builtin_memcpy(w, p, sizeof(w));
   }
+  // At `voff` bytes of the lane's plus `soff` of the wavefront's own in a buffer.
+  __device__ __forceinline__ void load(buf_t r, int voff, int soff) {
+    if constexpr (sizeof(T) * V == 2) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+    } else if constexpr (sizeof(T) * V == 4) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+    } else {
+      static_assert(sizeof(T) * V == 8, "two, four or eight bytes");
+      const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0);
+      w[0] = u.x, w[1] = u.y;
+    }
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) w[k] = 0u;
+  }
+  // Here the values are in registers as they were loaded.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) asm volatile("" : "+v"(w[k]));
   }
   __device__ __forceinline__ float get(int v) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[v]);
@@ -35,6 +55,23 @@ struct Raw {
       __builtin_memcpy(p, e, sizeof(e));
     }
   }
+  static __device__ __forceinline__ void store(buf_t r, int voff, int soff, const float (&f)[V]) {
+    T e[V];
+    store(e, f);
+    if constexpr (sizeof(e) == 2) {
+      unsigned short u;
+      __builtin_memcpy(&u, e, 2);
+      __builtin_amdgcn_raw_buffer_store_b16(u, r, voff, soff, 0);
+    } else if constexpr (sizeof(e) == 4) {
+      uint32_t u;
+      __builtin_memcpy(&u, e, 4);
+      __builtin_amdgcn_raw_buffer_store_b32(u, r, voff, soff, 0);
+    } else {
+      u32x2 u;
+      __builtin_memcpy(&u, e, 8);
+      __builtin_amdgcn_raw_buffer_store_b64(u, r, voff, soff, 0);
+    }
+  }
 };
 
 __device__ __forceinline__ float sigmoid(float v) {
@@ -43,33 +80,39 @@ __device__ __forceinline__ float sigmoid(float v) {
 __device__ __forceinline__ float sqrt_(float v) { return __builtin_amdgcn_sqrtf(v); }
 __device__ __forceinline__ float rsqrt_(float v) { return __builtin_amdgcn_rsqf(v); }
 
-// a = exp(A s) and m2 = 1 - a^2 with s = sigmoid(r), A <= 0.
+// The decay a = exp(u), u = A s <= 0, as one number q that keeps both a and 1 - a^2.
 //
 // A state that remembers thousands of tokens has a within 1e-3 of 1, where 1 - a^2 cancels and
 // where a bias of a's last place (the exponential's own rounding) adds up over those tokens.
-// So e = exp(A s) - 1 comes from its series down to A s = -1/4 (the next term is 2e-9 of it) and
-// a = 1 + e is rounded once; below, decays forget within a few tokens and the
-// exponential's last place is enough.  (dA of 4 x 8192 x 2048 bf16, whose terms
-// cancel to 1 in 100: off by 1e-5 of its norm with the exponential alone.)
-struct Decay {
-  float s, a, m2;
-};
+// So down to u = -1/4 q is e = exp(u) - 1 <= 0 from its series (the next term is 2e-9 of it): a = 1 + e
+// is rounded once, 1 - a^2 = -e (2 + e).  Below, q is a itself, positive; decays forget within a
+// few tokens and the exponential's last place is enough.  (dA of 4 x 8192 x 2048 bf16, whose
+// terms cancel to 1 in 100: off by 1e-5 of its norm with the exponential alone.)
+// kNear: u > -1/4 everywhere.
 constexpr float kSeries = -0.25f;
 
-__device__ __forceinline__ Decay decay_of(float A, float r) {
-  Decay d;
-  d.s = sigmoid(r);
-  const float u = A * d.s;
+template <bool kNear>
+__device__ __forceinline__ float decay_of(float u) {
   float e = __builtin_fmaf(u, 1.0f / 5040.0f, 1.0f / 720.0f);
   e = __builtin_fmaf(e, u, 1.0f / 120.0f);
   e = __builtin_fmaf(e, u, 1.0f / 24.0f);
   e = __builtin_fmaf(e, u, 1.0f / 6.0f);
   e = __builtin_fmaf(e, u, 0.5f);
   e = __builtin_fmaf(e, u, 1.0f) * u;
-  const float b = fast_exp2(u * kLog2e);
-  d.a = u > kSeries ? 1.0f + e : b;
-  d.m2 = u > kSeries ? -e * (2.0f + e) : __builtin_fmaf(-b, b, 1.0f);
-  return d;
+  if constexpr (!kNear) {
+    // (a decay below the normal numbers stays positive; NaN goes on as it is)
+    const float a = fast_exp2(u * kLog2e);
+    e = u <= kSeries ? (a > 1.2e-38f ? a : 1.2e-38f) : e;
+  }
+  return e;
+}
+template <bool kNear>
+__device__ __forceinline__ float decay(float q) {
+  return kNear || !(q > 0.0f) ? 1.0f + q : q;
+}
+template <bool kNear>
+__device__ __forceinline__ float one_minus_square(float q) {
+  return kNear || !(q > 0.0f) ? -q * (2.0f + q) : __builtin_fmaf(-q, q, 1.0f);
 }
 
 }  // namespace mssm

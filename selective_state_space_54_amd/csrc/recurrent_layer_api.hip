@@ -9,7 +9,8 @@ using mssm::check_workspace;
 using mssm::done;
 using mssm::product;
 
-constexpr int64_t kMaxD = int64_t(1) << 28;
+// A row of values, or from one token's to the next one's: sixteen of them are reached in 31 bits.
+constexpr int64_t kMaxRow = int64_t(1) << 24;
 constexpr int64_t kMaxSeqs = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxThreads = int64_t(1) << 32;       // of a launch, in one dimension
 
@@ -19,7 +20,7 @@ mssm_status sequences_of(const int64_t* offsets, bool packed, int64_t seqs, int6
   int64_t tokens = L, n;
   if (!packed && !product({seqs, L}, &tokens)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (!product({tokens, D, 64}, &n) || !product({seqs, D, 64}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
-  if (D >= kMaxD || seqs > kMaxSeqs) return MSSM_ERROR_NOT_SUPPORTED;
+  if (D >= kMaxRow || seqs > kMaxSeqs) return MSSM_ERROR_NOT_SUPPORTED;
   s->offsets = offsets;
   s->n = seqs;
   s->L = packed ? 0 : L;
@@ -27,11 +28,14 @@ mssm_status sequences_of(const int64_t* offsets, bool packed, int64_t seqs, int6
   return MSSM_SUCCESS;
 }
 
-// Token rows hold their channels.
-mssm_status check_rows(const mssm::Sequences& s, int64_t D, std::initializer_list<int64_t> rows) {
+// Token rows hold their channels.  (A single token's are reached in 64 bits, whatever lies
+// between them.)
+mssm_status check_rows(const mssm::Sequences& s, int64_t D, std::initializer_list<int64_t> rows,
+                       bool single = false) {
   for (int64_t row : rows) {
     int64_t n;
     if (row < D) return MSSM_ERROR_INVALID_VALUE;
+    if (!single && row >= kMaxRow) return MSSM_ERROR_NOT_SUPPORTED;
     if (!product({s.tokens, row, 8}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   }
   return MSSM_SUCCESS;
@@ -120,7 +124,7 @@ mssm_status mssm_gated_recurrence_step(const void* x, const void* input_gate,
   if (st != MSSM_SUCCESS) return st;
   if (seqs == 0 || D == 0) return MSSM_SUCCESS;
   if (!x || !input_gate || !decay_gate || !A || !state || !h) return MSSM_ERROR_INVALID_VALUE;
-  if ((st = check_rows(a.seqs, D, {x_row, i_row, r_row})) != MSSM_SUCCESS) return st;
+  if ((st = check_rows(a.seqs, D, {x_row, i_row, r_row}, true)) != MSSM_SUCCESS) return st;
   int64_t n;
   if (!product({seqs, D}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (n >= kMaxThreads - 256) return MSSM_ERROR_NOT_SUPPORTED;
@@ -227,7 +231,7 @@ mssm_status mssm_causal_conv1d_step(const void* u, const float* weight, const fl
   if ((st = check_conv(act, k)) != MSSM_SUCCESS) return st;
   if (seqs == 0 || D == 0) return MSSM_SUCCESS;
   if (!u || !weight || !y || (k > 1 && !state)) return MSSM_ERROR_INVALID_VALUE;
-  if ((st = check_rows(a.seqs, D, {u_row})) != MSSM_SUCCESS) return st;
+  if ((st = check_rows(a.seqs, D, {u_row}, true)) != MSSM_SUCCESS) return st;
   int64_t n;
   if (!product({seqs, D}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (n >= kMaxThreads - 256) return MSSM_ERROR_NOT_SUPPORTED;

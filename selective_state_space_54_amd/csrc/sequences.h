@@ -59,12 +59,12 @@ __device__ __forceinline__ int64_t seq_after(const Sequences& s, int64_t t) {
   return lo;
 }
 
-// The tokens t0 .. t0 + S - 1 (S up to 64) of one wavefront.  Bit s of a mask stands for token
+// The tokens t0 .. t0 + S - 1 (S up to 32) of one wavefront.  Bit s of a mask stands for token
 // t0 + s.  Without borders every token is in the same sequence (or in none) and neither
 // its first nor its last.
 struct Span {
   bool borders = false;
-  uint64_t valid = 0, first = 0, last = 0;
+  uint32_t valid = 0, first = 0, last = 0;
   int owner = 0;              // in lane s: the sequence of token t0 + s
   __device__ __forceinline__ int64_t sequence(int s) const {
     return static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(owner, s)));
@@ -73,12 +73,13 @@ struct Span {
 
 template <int S>
 __device__ __forceinline__ Span span_of(const Sequences& seqs, int64_t t0) {
+  static_assert(S <= 32, "a mask's bits");
   Span p;
   const int64_t after = uniform64(seq_after(seqs, t0 - 1));   // the first border at or after t0
   // a border at t0 + S makes the last of these tokens its sequence's last
   const bool plain = after > seqs.n || uniform64(seq_begin(seqs, after)) > t0 + S;
   if (plain) {
-    p.valid = after >= 1 && after <= seqs.n ? ~0ull : 0ull;
+    p.valid = after >= 1 && after <= seqs.n ? 0xffffffffu : 0u;
     return p;
   }
   p.borders = true;
@@ -88,9 +89,9 @@ __device__ __forceinline__ Span span_of(const Sequences& seqs, int64_t t0) {
   const bool valid = lane < S && q >= 0 && q < seqs.n && t < seqs.tokens;
   const int64_t at = valid ? q : 0;
   p.owner = static_cast<int>(at);
-  p.valid = __ballot(valid);
-  p.first = __ballot(valid && seq_begin(seqs, at) == t);
-  p.last = __ballot(valid && seq_begin(seqs, at + 1) == t + 1);
+  p.valid = static_cast<uint32_t>(__ballot(valid));
+  p.first = static_cast<uint32_t>(__ballot(valid && seq_begin(seqs, at) == t));
+  p.last = static_cast<uint32_t>(__ballot(valid && seq_begin(seqs, at + 1) == t + 1));
   return p;
 }
 

@@ -49,7 +49,7 @@ def test_recurrence_sizes(lib):
         assert query(sv, *bad, 0, FP32)[0] == INVALID
     assert query(ws, 1, 5, 40, 0, 0, 0, 7)[0] == INVALID
     assert query(ws, 1 << 40, 1 << 40, 4, 0, 0, 0, FP32)[0] == OVERFLOW
-    assert query(ws, 1, 1, 1 << 28, 0, 0, 0, FP32)[0] == UNSUPPORTED
+    assert query(ws, 1, 1, 1 << 24, 0, 0, 0, FP32)[0] == UNSUPPORTED
     assert query(ws, 1 << 31, 0, 4, 0, 0, 0, FP32)[0] == UNSUPPORTED
     assert query(ws, 1, 1 << 36, 64, 0, 0, 0, FP32)[0] == UNSUPPORTED   # more than a launch takes
     assert ws(1, 5, 40, 0, 0, 0, FP32, None) == INVALID
@@ -72,7 +72,7 @@ def test_recurrence_forward_errors(lib):
         assert fwd(lib, shape=put(SHAPE, i, -1)) == INVALID, i
     for i in (3, 4, 5):
         assert fwd(lib, shape=put(SHAPE, i, 39)) == INVALID, i           # rows that overlap
-        assert fwd(lib, shape=put(SHAPE, i, 1 << 60)) == OVERFLOW, i
+        assert fwd(lib, shape=put(SHAPE, i, 1 << 24)) == UNSUPPORTED, i
     assert fwd(lib, dtype=9) == INVALID
     assert fwd(lib, put(put(FWD, 5, FAKE), 7, FAKE)) == INVALID          # last_state is state
     long = (1, 5000, 40, 40, 40, 40)
@@ -94,6 +94,7 @@ def test_recurrence_step_errors(lib):
         assert f(s=put(shape, i, 39)) == INVALID, i
     assert f(s=put(shape, 0, -1)) == INVALID and f(d=4) == INVALID
     assert f(s=(1 << 20, 1 << 20, 1 << 20, 1 << 20, 1 << 20)) == UNSUPPORTED
+    assert f(s=put(shape, 3, 1 << 60)) == OVERFLOW
     assert f([None] * 6, (0, 40, 40, 40, 40)) == OK
 
 
