@@ -27,8 +27,10 @@ namespace mssm {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kBlock = 64 * kWaves;
+#ifndef FW
+#define FW 8
+#endif
+constexpr int kFwdWaves = FW, kBwdWaves = 8;          // of a block
 constexpr int kSavedTokens = 64;          // a saved state for every so many tokens
 #ifndef LB
 #define LB 8
@@ -126,6 +128,11 @@ __global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* slots, int
   if (i < groups) tickets[i * kTicketStride] = 0;
 }
 
+// A barrier for what lies in LDS alone: loads and stores in flight go on.
+__device__ __forceinline__ void lds_sync() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 struct Place {
   int64_t link;           // the tile's place in its chain
   int64_t t0;             // the wavefront's first token
@@ -136,7 +143,7 @@ struct Place {
 
 // tiles: how many a chain has; with one there is nothing to take a ticket for.  (Every block gets a
 // tile; one beyond them, which only a workspace in use elsewhere could give, is not worked on.)
-template <int V, int S, bool kReverse>
+template <int V, int S, int W, bool kReverse>
 __device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t tiles,
                                           uint32_t* tickets) {
   __shared__ uint32_t ticket;
@@ -149,13 +156,13 @@ __device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t til
     if (threadIdx.x == 0)
       ticket = __hip_atomic_fetch_add(tickets + group * kTicketStride, 1u, __ATOMIC_RELAXED,
                                       __HIP_MEMORY_SCOPE_AGENT);
-    block_sync();
+    lds_sync();
     p.link = MSSM_UNIFORM(ticket);
   }
   const int64_t c0 = group * (64 * V) + p.lane * V;
   p.active = c0 < D;
   p.c = static_cast<int>(c0 < D - V ? c0 : D - V);
-  p.t0 = (kReverse ? tiles - 1 - p.link : p.link) * (kWaves * S) + p.wave * S;
+  p.t0 = (kReverse ? tiles - 1 - p.link : p.link) * (W * S) + p.wave * S;
   return p;
 }
 
@@ -182,9 +189,9 @@ __device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t
 }
 
 // What the wavefronts of a block tell one another.
-template <int V>
+template <int V, int W>
 struct Maps {
-  float p[kWaves][64 * V], h[kWaves][64 * V], in[64 * V];
+  float p[W][64 * V], h[W][64 * V], in[64 * V];
   __device__ __forceinline__ void put(const Place& at, const float (&P)[V], const float (&H)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) p[at.wave][at.lane * V + v] = P[v], h[at.wave][at.lane * V + v] = H[v];
@@ -196,8 +203,8 @@ struct Maps {
     for (int v = 0; v < V; ++v) {
       P[v] = 1.0f, H[v] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        const int w = kReverse ? kWaves - 1 - k : k;
+      for (int k = 0; k < W; ++k) {
+        const int w = kReverse ? W - 1 - k : k;
         const float q = p[w][lane * V + v];
         H[v] = join(q, h[w][lane * V + v], H[v]);
         P[v] = q == 0.0f ? 0.0f : P[v] * q;
@@ -209,20 +216,20 @@ struct Maps {
   __device__ __forceinline__ void take(const Place& at, float (&x)[V]) const {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      for (int k = 0; k < (kReverse ? kWaves - 1 - at.wave : at.wave); ++k) {
-        const int w = kReverse ? kWaves - 1 - k : k;
+      for (int k = 0; k < (kReverse ? W - 1 - at.wave : at.wave); ++k) {
+        const int w = kReverse ? W - 1 - k : k;
         x[v] = join(p[w][at.lane * V + v], h[w][at.lane * V + v], x[v]);
       }
   }
 };
 
 // The state (backward: psi) before this wavefront's tokens.  P, H: its own map.
-template <int V, bool kReverse>
-__device__ __forceinline__ void chain(const Place& at, Maps<V>& m, uint64_t* slots, int64_t tiles,
+template <int V, int W, bool kReverse>
+__device__ __forceinline__ void chain(const Place& at, Maps<V, W>& m, uint64_t* slots, int64_t tiles,
                                       int64_t D, const float (&P)[V], const float (&H)[V],
                                       float (&x)[V]) {
   m.put(at, P, H);
-  block_sync();
+  lds_sync();
   if (tiles > 1) {
     if (at.wave == 0) {
       float tp[V], th[V];
@@ -231,7 +238,7 @@ __device__ __forceinline__ void chain(const Place& at, Maps<V>& m, uint64_t* slo
 #pragma unroll
       for (int v = 0; v < V; ++v) m.in[at.lane * V + v] = x[v];
     }
-    block_sync();
+    lds_sync();
 #pragma unroll
     for (int v = 0; v < V; ++v) x[v] = m.in[at.lane * V + v];
   } else {
@@ -243,13 +250,13 @@ __device__ __forceinline__ void chain(const Place& at, Maps<V>& m, uint64_t* slo
 
 // h (kOut) and the last and saved states.
 template <typename T, int V, bool kOut>
-__global__ __launch_bounds__(kBlock, 4) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
+__global__ __launch_bounds__(64 * kFwdWaves, 4) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
                                                                int64_t tiles, uint32_t* tickets,
                                                                uint64_t* slots) {
   constexpr int S = kFwdSteps<T>;
-  __shared__ Maps<V> maps;
+  __shared__ Maps<V, kFwdWaves> maps;
   const int64_t D = a.D;
-  const Place p = place_of<V, S, false>(D, groups, tiles, tickets);
+  const Place p = place_of<V, S, kFwdWaves, false>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   Raw<T, V> x[S], gi[S], gr[S];
   load_rows<T, V, S>(a.r, a.r_row, D, p.t0, a.seqs.tokens, p.c, gr);
@@ -303,7 +310,7 @@ __global__ __launch_bounds__(kBlock, 4) void recurrence_kernel(RecurrenceArgs a,
       }
     }
   }
-  chain<V, false>(p, maps, slots, tiles, D, P, H, h);
+  chain<V, kFwdWaves, false>(p, maps, slots, tiles, D, P, H, h);
   if (!p.active) return;
   if (a.saved && p.t0 % kSavedTokens == 0 && p.t0 < a.seqs.tokens) {
 #pragma unroll
@@ -347,15 +354,15 @@ __global__ __launch_bounds__(256) void empty_states_kernel(Sequences seqs, const
 
 // saved: the state before each tile (null: zero); part: [tiles, D] the tiles' sums of dA.
 template <typename T, int V>
-__global__ __launch_bounds__(kBlock, BW) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
+__global__ __launch_bounds__(64 * kBwdWaves, BW) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
                                                                 int64_t groups, int64_t tiles,
                                                                 uint32_t* tickets, uint64_t* slots,
                                                                 const float* saved, float* part) {
   constexpr int S = kBwdSteps<T>;
-  static_assert(S * kWaves == kSavedTokens, "a saved state for each tile");
-  __shared__ Maps<V> fwd, rev;
+  static_assert(S * kBwdWaves == kSavedTokens, "a saved state for each tile");
+  __shared__ Maps<V, kBwdWaves> fwd, rev;
   const int64_t D = a.D;
-  const Place p = place_of<V, S, true>(D, groups, tiles, tickets);
+  const Place p = place_of<V, S, kBwdWaves, true>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   const int64_t tile = tiles - 1 - p.link;
   float rate[V], h[V], psi[V], sum[V];
@@ -431,7 +438,7 @@ __global__ __launch_bounds__(kBlock, BW) void recurrence_bwd_kernel(RecurrenceAr
         }
     }
     fwd.put(p, Pf, Hf);
-    chain<V, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
+    chain<V, kBwdWaves, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
     fwd.template take<false>(p, h);
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -499,7 +506,7 @@ __global__ __launch_bounds__(kBlock, BW) void recurrence_bwd_kernel(RecurrenceAr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float t = 0.0f;
-      for (int w = 0; w < kWaves; ++w) t += rev.p[w][p.lane * V + v];
+      for (int w = 0; w < kBwdWaves; ++w) t += rev.p[w][p.lane * V + v];
       part[tile * D + p.c + v] = t;
     }
   }
@@ -559,7 +566,7 @@ __global__ __launch_bounds__(256) void recurrence_zero_kernel(float* p, int64_t 
 }
 
 int64_t fwd_tile(mssm_dtype dtype) {
-  return kWaves * (dtype == MSSM_BFLOAT16 ? kFwdSteps<uint16_t> : kFwdSteps<float>);
+  return kFwdWaves * (dtype == MSSM_BFLOAT16 ? kFwdSteps<uint16_t> : kFwdSteps<float>);
 }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -643,7 +650,7 @@ hipError_t forward(const RecurrenceArgs& a, const RecurrencePlan& p, char* ws, h
   const dim3 grid(static_cast<uint32_t>(p.tiles * p.groups));
   return with_type(a.dtype, a.D, [&](auto t, auto v) {
     hipLaunchKernelGGL((recurrence_kernel<decltype(t), decltype(v)::value, kOut>), grid,
-                       dim3(kBlock), 0, stream, a, p.groups, p.tiles,
+                       dim3(64 * kFwdWaves), 0, stream, a, p.groups, p.tiles,
                        reinterpret_cast<uint32_t*>(ws + p.tickets),
                        reinterpret_cast<uint64_t*>(ws + p.slots));
     return hipGetLastError();
@@ -690,7 +697,7 @@ hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads&
   float* part = reinterpret_cast<float*>(ws + p.part);
   const dim3 grid(static_cast<uint32_t>(p.bwd_tiles * p.groups));
   e = with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value>), grid, dim3(kBlock),
+    hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value>), grid, dim3(64 * kBwdWaves),
                        0, stream, a, d, p.groups, p.bwd_tiles,
                        reinterpret_cast<uint32_t*>(ws + p.tickets),
                        reinterpret_cast<uint64_t*>(ws + p.slots), saved, part);
