@@ -9,8 +9,8 @@
 //   e = lambda (a h_{t-1} - g x a^2 / m)      (the gradient of log a: dm / dlog a = -a^2 / m)
 //   dr = e A s (1 - s),   dA = sum over tokens of e s.
 //
-// A wavefront takes a few tokens of 64 V channels (a lane holds V channels) and a block kWaves
-// wavefronts behind one another: a tile.  The affine map h -> P h + H of a wavefront's tokens
+// A wavefront takes a few tokens of 64 V channels (a lane holds V channels) and a block
+// several wavefronts behind one another: a tile.  The affine map h -> P h + H of a wavefront's tokens
 // is formed from registers and the wavefronts' maps are joined in LDS, so every input is read
 // once.  Tiles of the same channels form a chain: a block publishes its tile's map, then
 // looks back over the tiles before it for the nearest one whose state is known, takes that state
@@ -27,31 +27,29 @@ namespace mssm {
 
 namespace {
 
-#ifndef FW
-#define FW 8
-#endif
-constexpr int kFwdWaves = FW, kBwdWaves = 8;          // of a block
 constexpr int kSavedTokens = 64;          // a saved state for every so many tokens
-#ifndef LB
-#define LB 8
-#endif
-constexpr int kLookBack = LB;              // tiles looked at together
+constexpr int kLookBack = 6;              // tiles looked at together
 constexpr int kMaxPolls = 1 << 22;
 constexpr int64_t kTicketStride = 32;     // counters on cache lines of their own
-#ifndef BW
-#define BW 4
-#endif
 
-#ifndef FS
-#define FS 16
-#endif
-#ifndef BS
-#define BS 8
-#endif
+// A wavefront's tokens and a block's wavefronts.  Forward: tiles of 128 tokens (float32: 64) of 128
+// channels, two blocks a compute unit; what a tile takes is mostly waiting (15 us: ticket 1, loads 3,
+// gates 3, its wavefronts 3, look-back 4), so smaller tiles are no better (131072 x 2560 bf16: 645 us,
+// 850 with four wavefronts, 887 with 8 tokens), nor is one block that loads ahead (780 us).
 template <typename T>
-constexpr int kFwdSteps = sizeof(T) == 2 ? FS : 8;   // tokens of a wavefront
+struct Forward {
+  static constexpr int S = sizeof(T) == 2 ? 16 : 8, W = 8;
+};
+// All tokens in one tile: shorter chains of operations (45 x 2560 bf16: kernel 6.3 us, 10.4 with tiles of 128).
 template <typename T>
-constexpr int kBwdSteps = BS;
+struct Short {
+  static constexpr int S = 4, W = 16;
+};
+// Backward: a tile for each saved state.
+template <typename T>
+struct Backward {
+  static constexpr int S = 8, W = 8;
+};
 
 // Joins the affine map (P, H) behind state h.  P = 0 stands for a sequence's first token in between
 // (or a decay of nothing): what h was, infinite or NaN too, is forgotten.
@@ -119,13 +117,34 @@ __device__ __forceinline__ void look_back(uint64_t* slots, int64_t j, int64_t D,
   for (int v = 0; v < V; ++v) publish(slots + j * D + c + v, kState, join(P[v], H[v], h[v]));
 }
 
-// Sets the slots to "nothing yet" and the chains' counters to zero.
-__global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* slots, int64_t n,
-                                                               uint32_t* tickets, int64_t groups) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  for (int64_t k = i; k < n; k += int64_t(gridDim.x) * 256)
-    slots[k] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
-  if (i < groups) tickets[i * kTicketStride] = 0;
+// Before a pass: the slots are set to "nothing yet" and the chains' counters to zero (by the first
+// clear_blocks blocks), and sequences without tokens pass their state on, to = from or zero.
+struct Prepare {
+  uint4* slots;
+  int64_t n;
+  uint32_t* tickets;
+  int64_t groups;
+  int64_t clear_blocks;
+  Sequences seqs;
+  const float* from;
+  float* to;
+  int64_t D;
+};
+__global__ __launch_bounds__(256) void recurrence_prepare_kernel(Prepare a) {
+  if (blockIdx.x < a.clear_blocks) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    for (int64_t k = i; k < a.n; k += a.clear_blocks * 256)
+      a.slots[k] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+    for (int64_t k = i; k < a.groups; k += a.clear_blocks * 256) a.tickets[k * kTicketStride] = 0;
+    return;
+  }
+  for (int64_t q = blockIdx.x - a.clear_blocks; q < a.seqs.n; q += gridDim.x - a.clear_blocks) {
+    if (seq_begin(a.seqs, q + 1) > seq_begin(a.seqs, q)) continue;
+    for (int64_t c = threadIdx.x; c < a.D; c += 256) {
+      const int64_t e = q * a.D + c;
+      a.to[e] = a.from ? a.from[e] : 0.0f;
+    }
+  }
 }
 
 // A barrier for what lies in LDS alone: loads and stores in flight go on.
@@ -164,28 +183,6 @@ __device__ __forceinline__ Place place_of(int64_t D, int64_t groups, int64_t til
   p.c = static_cast<int>(c0 < D - V ? c0 : D - V);
   p.t0 = (kReverse ? tiles - 1 - p.link : p.link) * (W * S) + p.wave * S;
   return p;
-}
-
-// S rows of a tensor from token t0 on as a buffer: addresses are a lane's own part and a wave-uniform
-// one for the row.  step: bytes from row to row; bytes: of a row.
-template <int S>
-__device__ __forceinline__ buf_t rows_from(const void* base, int64_t t0, int64_t step,
-                                           int64_t bytes) {
-  return make_buf(static_cast<const char*>(base) + t0 * step,
-                  static_cast<uint32_t>((S - 1) * step + bytes));
-}
-
-// S rows from token t0 on, each lane its V channels; rows past the last token repeat it.
-template <typename T, int V, int S>
-__device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t D, int64_t t0,
-                                          int64_t tokens, int c, Raw<T, V> (&v)[S]) {
-  const int64_t step = row * static_cast<int64_t>(sizeof(T));
-  const int64_t left = tokens - t0;
-  const buf_t r = rows_from<S>(base, left > 0 ? t0 : tokens - 1, step, D * sizeof(T));
-  const int last = left > S ? S - 1 : left > 0 ? static_cast<int>(left) - 1 : 0;
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-    v[s].load(r, c * static_cast<int>(sizeof(T)), (s < last ? s : last) * static_cast<int>(step));
 }
 
 // What the wavefronts of a block tell one another.
@@ -249,14 +246,13 @@ __device__ __forceinline__ void chain(const Place& at, Maps<V, W>& m, uint64_t* 
 }
 
 // h (kOut) and the last and saved states.
-template <typename T, int V, bool kOut>
-__global__ __launch_bounds__(64 * kFwdWaves, 4) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
+template <typename T, int V, int S, int W, bool kOut>
+__global__ __launch_bounds__(64 * W, 4) void recurrence_kernel(RecurrenceArgs a, int64_t groups,
                                                                int64_t tiles, uint32_t* tickets,
                                                                uint64_t* slots) {
-  constexpr int S = kFwdSteps<T>;
-  __shared__ Maps<V, kFwdWaves> maps;
+  __shared__ Maps<V, W> maps;
   const int64_t D = a.D;
-  const Place p = place_of<V, S, kFwdWaves, false>(D, groups, tiles, tickets);
+  const Place p = place_of<V, S, W, false>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   Raw<T, V> x[S], gi[S], gr[S];
   load_rows<T, V, S>(a.r, a.r_row, D, p.t0, a.seqs.tokens, p.c, gr);
@@ -310,7 +306,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void recurrence_kernel(Recurrenc
       }
     }
   }
-  chain<V, kFwdWaves, false>(p, maps, slots, tiles, D, P, H, h);
+  chain<V, W, false>(p, maps, slots, tiles, D, P, H, h);
   if (!p.active) return;
   if (a.saved && p.t0 % kSavedTokens == 0 && p.t0 < a.seqs.tokens) {
 #pragma unroll
@@ -344,25 +340,17 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void recurrence_kernel(Recurrenc
   }
 }
 
-// Sequences without tokens: to = from, or zero.
-__global__ __launch_bounds__(256) void empty_states_kernel(Sequences seqs, const float* from,
-                                                           float* to, int64_t D) {
-  const int64_t q = blockIdx.x;
-  if (seq_begin(seqs, q + 1) > seq_begin(seqs, q)) return;
-  for (int64_t c = threadIdx.x; c < D; c += 256) to[q * D + c] = from ? from[q * D + c] : 0.0f;
-}
-
 // saved: the state before each tile (null: zero); part: [tiles, D] the tiles' sums of dA.
 template <typename T, int V>
-__global__ __launch_bounds__(64 * kBwdWaves, BW) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
+__global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
                                                                 int64_t groups, int64_t tiles,
                                                                 uint32_t* tickets, uint64_t* slots,
                                                                 const float* saved, float* part) {
-  constexpr int S = kBwdSteps<T>;
-  static_assert(S * kBwdWaves == kSavedTokens, "a saved state for each tile");
-  __shared__ Maps<V, kBwdWaves> fwd, rev;
+  constexpr int S = Backward<T>::S, W = Backward<T>::W;
+  static_assert(S * W == kSavedTokens, "a saved state for each tile");
+  __shared__ Maps<V, W> fwd, rev;
   const int64_t D = a.D;
-  const Place p = place_of<V, S, kBwdWaves, true>(D, groups, tiles, tickets);
+  const Place p = place_of<V, S, W, true>(D, groups, tiles, tickets);
   if (p.link >= tiles) return;
   const int64_t tile = tiles - 1 - p.link;
   float rate[V], h[V], psi[V], sum[V];
@@ -438,7 +426,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, BW) void recurrence_bwd_kernel(Recu
         }
     }
     fwd.put(p, Pf, Hf);
-    chain<V, kBwdWaves, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
+    chain<V, W, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
     fwd.template take<false>(p, h);
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -506,7 +494,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, BW) void recurrence_bwd_kernel(Recu
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float t = 0.0f;
-      for (int w = 0; w < kBwdWaves; ++w) t += rev.p[w][p.lane * V + v];
+      for (int w = 0; w < W; ++w) t += rev.p[w][p.lane * V + v];
       part[tile * D + p.c + v] = t;
     }
   }
@@ -519,8 +507,10 @@ __global__ __launch_bounds__(1024) void recurrence_sum_kernel(const float* __res
   const int col = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = int64_t(blockIdx.x) * 64 + col;
   double s = 0.0;
-  if (c < D)
+  if (c < D) {
+#pragma unroll 8
     for (int64_t r = w; r < rows; r += 16) s += part[r * D + c];
+  }
   m[w][col] = s;
   block_sync();
   if (w == 0 && c < D) {
@@ -566,18 +556,24 @@ __global__ __launch_bounds__(256) void recurrence_zero_kernel(float* p, int64_t 
 }
 
 int64_t fwd_tile(mssm_dtype dtype) {
-  return kFwdWaves * (dtype == MSSM_BFLOAT16 ? kFwdSteps<uint16_t> : kFwdSteps<float>);
+  return dtype == MSSM_BFLOAT16 ? Forward<uint16_t>::S * Forward<uint16_t>::W
+                                : Forward<float>::S * Forward<float>::W;
 }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Calls f with the element type and the channels a lane holds: two, or one for up to 64 channels,
-// which fill a wavefront only so.
+// Channels a lane holds: two, or one for up to 64 channels, which fill a wavefront only so.  The
+// backward kernel keeps more numbers a channel and takes one (two spill registers: training
+// pass 4 x 8192 x 2048 bf16 480 -> 445 us).
+constexpr int kBackwardChannels = 1;
+int lane_channels(int64_t D) { return D > 64 ? 2 : 1; }
+
+// Calls f with the element type and the channels a lane holds.
 template <typename F>
-hipError_t with_type(mssm_dtype dtype, int64_t D, F f) {
+hipError_t with_type(mssm_dtype dtype, int V, F f) {
   if (dtype == MSSM_BFLOAT16)
-    return D > 64 ? f(uint16_t(), std::integral_constant<int, 2>())
+    return V == 2 ? f(uint16_t(), std::integral_constant<int, 2>())
                   : f(uint16_t(), std::integral_constant<int, 1>());
-  return D > 64 ? f(float(), std::integral_constant<int, 2>())
+  return V == 2 ? f(float(), std::integral_constant<int, 2>())
                 : f(float(), std::integral_constant<int, 1>());
 }
 
@@ -588,7 +584,12 @@ RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool sa
   RecurrencePlan p;
   p.tiles = (tokens + fwd_tile(dtype) - 1) / fwd_tile(dtype);
   p.bwd_tiles = (tokens + kSavedTokens - 1) / kSavedTokens;
-  p.groups = (D + (D > 64 ? 127 : 63)) / (D > 64 ? 128 : 64);
+  auto groups = [&](bool back) {
+    const int64_t wide = 64 * (back ? kBackwardChannels : lane_channels(D));
+    return (D + wide - 1) / wide;
+  };
+  p.groups = groups(false);
+  p.bwd_groups = groups(true);
   const size_t states = static_cast<size_t>(p.bwd_tiles) * D * sizeof(float);
   p.saved_bytes = states;
   size_t off = 0;
@@ -600,7 +601,7 @@ RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool sa
   // the two directions follow one another and share the counters and slots
   const int64_t links = backward ? p.bwd_tiles : p.tiles;
   if (links > 1) {
-    p.tickets = take(static_cast<size_t>(p.groups) * kTicketStride * sizeof(uint32_t));
+    p.tickets = take(static_cast<size_t>(backward ? p.bwd_groups : p.groups) * kTicketStride * sizeof(uint32_t));
     p.slots = take(static_cast<size_t>(links) * D * sizeof(uint64_t));
   }
   if (backward) {
@@ -613,47 +614,46 @@ RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool sa
 
 namespace {
 
-hipError_t empty_states(const Sequences& s, const float* from, float* to, int64_t D,
-                        hipStream_t stream) {
-  for (int64_t q = 0; q < s.n; q += 1 << 22) {       // a launch's blocks
-    const int64_t n = s.n - q < (1 << 22) ? s.n - q : 1 << 22;
-    Sequences part = s;
-    if (part.offsets) part.offsets += q;
-    part.n = n;
-    hipLaunchKernelGGL(empty_states_kernel, dim3(static_cast<uint32_t>(n)), dim3(256), 0, stream,
-                       part, from ? from + q * D : nullptr, to + q * D, D);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
-hipError_t clear(const RecurrencePlan& p, int64_t links, int64_t D, char* ws, hipStream_t stream) {
-  const int64_t n = (links * D + 1) / 2;             // (slots end at a multiple of 256 bytes)
-  int64_t blocks = (n + 255) / 256;
-  const int64_t least = (p.groups + 255) / 256;
-  if (blocks > 2048) blocks = 2048;
-  if (blocks < least) blocks = least;
-  hipLaunchKernelGGL(recurrence_clear_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0,
-                     stream, reinterpret_cast<uint4*>(ws + p.slots), n,
-                     reinterpret_cast<uint32_t*>(ws + p.tickets), p.groups);
+// links: of a chain, to be cleared where there are several; from, to: what sequences without tokens
+// pass on, with to.
+hipError_t prepare(const RecurrencePlan& p, int64_t links, int64_t groups, const Sequences& seqs,
+                   const float* from, float* to, int64_t D, char* ws, hipStream_t stream) {
+  Prepare a;
+  const bool clear = links > 1, states = to && (seqs.offsets || seqs.L == 0);
+  if (!clear && !states) return hipSuccess;
+  a.slots = reinterpret_cast<uint4*>(ws + p.slots);
+  a.n = (links * D + 1) / 2;                         // (slots end at a multiple of 256 bytes)
+  a.tickets = reinterpret_cast<uint32_t*>(ws + p.tickets);
+  a.groups = groups;
+  a.clear_blocks = !clear ? 0 : a.n < 2048 * 256 ? (a.n + 255) / 256 : 2048;
+  a.seqs = seqs;
+  a.from = from;
+  a.to = to;
+  a.D = D;
+  const int64_t more = !states ? 0 : seqs.n < 65536 ? seqs.n : 65536;
+  hipLaunchKernelGGL(recurrence_prepare_kernel, dim3(static_cast<uint32_t>(a.clear_blocks + more)),
+                     dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 // h, last and saved states; kOut false: the saved states alone.
 template <bool kOut>
 hipError_t forward(const RecurrenceArgs& a, const RecurrencePlan& p, char* ws, hipStream_t stream) {
-  if (p.tiles > 1) {
-    const hipError_t e = clear(p, p.tiles, a.D, ws, stream);
-    if (e != hipSuccess) return e;
-  }
-  const dim3 grid(static_cast<uint32_t>(p.tiles * p.groups));
-  return with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_kernel<decltype(t), decltype(v)::value, kOut>), grid,
-                       dim3(64 * kFwdWaves), 0, stream, a, p.groups, p.tiles,
-                       reinterpret_cast<uint32_t*>(ws + p.tickets),
-                       reinterpret_cast<uint64_t*>(ws + p.slots));
-    return hipGetLastError();
+  const hipError_t e = prepare(p, p.tiles, p.groups, a.seqs, a.state, a.last, a.D, ws, stream);
+  if (e != hipSuccess || a.seqs.tokens == 0) return e;
+  return with_type(a.dtype, lane_channels(a.D), [&](auto t, auto v) {
+    using T = decltype(t);
+    auto go = [&](auto shape) {
+      using Shape = decltype(shape);
+      hipLaunchKernelGGL((recurrence_kernel<T, decltype(v)::value, Shape::S, Shape::W, kOut>),
+                         dim3(static_cast<uint32_t>(p.tiles * p.groups)), dim3(64 * Shape::W), 0,
+                         stream, a, p.groups, p.tiles, reinterpret_cast<uint32_t*>(ws + p.tickets),
+                         reinterpret_cast<uint64_t*>(ws + p.slots));
+      return hipGetLastError();
+    };
+    if constexpr (kOut)
+      if (a.seqs.tokens <= Short<T>::S * Short<T>::W) return go(Short<T>());
+    return go(Forward<T>());
   });
 }
 
@@ -661,26 +661,12 @@ hipError_t forward(const RecurrenceArgs& a, const RecurrencePlan& p, char* ws, h
 
 hipError_t launch_recurrence(const RecurrenceArgs& a, const RecurrencePlan& p, void* ws,
                              hipStream_t stream) {
-  if (a.last && (a.seqs.offsets || a.seqs.L == 0)) {
-    const hipError_t e = empty_states(a.seqs, a.state, a.last, a.D, stream);
-    if (e != hipSuccess) return e;
-  }
-  if (a.seqs.tokens == 0) return hipSuccess;
   return forward<true>(a, p, static_cast<char*>(ws), stream);
 }
 
 hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads& d,
                                  const RecurrencePlan& p, void* ws_, hipStream_t stream) {
   char* ws = static_cast<char*>(ws_);
-  if (d.dstate && (a.seqs.offsets || a.seqs.L == 0)) {
-    const hipError_t e = empty_states(a.seqs, d.dlast, d.dstate, a.D, stream);
-    if (e != hipSuccess) return e;
-  }
-  if (a.seqs.tokens == 0) {
-    hipLaunchKernelGGL(recurrence_zero_kernel, dim3(static_cast<uint32_t>((a.D + 255) / 256)),
-                       dim3(256), 0, stream, d.dA, a.D);
-    return hipGetLastError();
-  }
   const float* saved = nullptr;
   hipError_t e;
   if (p.bwd_tiles > 1) {
@@ -692,17 +678,25 @@ hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads&
       if ((e = forward<false>(f, p, ws, stream)) != hipSuccess) return e;
       saved = f.saved;
     }
-    if ((e = clear(p, p.bwd_tiles, a.D, ws, stream)) != hipSuccess) return e;
+  }
+  e = prepare(p, p.bwd_tiles, p.bwd_groups, a.seqs, d.dlast, d.dstate, a.D, ws, stream);
+  if (e != hipSuccess) return e;
+  if (a.seqs.tokens == 0) {
+    hipLaunchKernelGGL(recurrence_zero_kernel, dim3(static_cast<uint32_t>((a.D + 255) / 256)),
+                       dim3(256), 0, stream, d.dA, a.D);
+    return hipGetLastError();
   }
   float* part = reinterpret_cast<float*>(ws + p.part);
-  const dim3 grid(static_cast<uint32_t>(p.bwd_tiles * p.groups));
-  e = with_type(a.dtype, a.D, [&](auto t, auto v) {
-    hipLaunchKernelGGL((recurrence_bwd_kernel<decltype(t), decltype(v)::value>), grid, dim3(64 * kBwdWaves),
-                       0, stream, a, d, p.groups, p.bwd_tiles,
+  const dim3 grid(static_cast<uint32_t>(p.bwd_tiles * p.bwd_groups));
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    hipLaunchKernelGGL((recurrence_bwd_kernel<T, kBackwardChannels>), grid,
+                       dim3(64 * Backward<T>::W), 0, stream, a, d, p.bwd_groups, p.bwd_tiles,
                        reinterpret_cast<uint32_t*>(ws + p.tickets),
                        reinterpret_cast<uint64_t*>(ws + p.slots), saved, part);
     return hipGetLastError();
-  });
+  };
+  e = a.dtype == MSSM_BFLOAT16 ? go(uint16_t()) : go(float());
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(recurrence_sum_kernel, dim3(static_cast<uint32_t>((a.D + 63) / 64)),
                      dim3(1024), 0, stream, part, p.bwd_tiles, a.D, d.dA);
@@ -710,7 +704,7 @@ hipError_t launch_recurrence_bwd(const RecurrenceArgs& a, const RecurrenceGrads&
 }
 
 hipError_t launch_recurrence_step(const RecurrenceArgs& a, float* state, hipStream_t stream) {
-  return with_type(a.dtype, a.D, [&](auto t, auto v) {
+  return with_type(a.dtype, lane_channels(a.D), [&](auto t, auto v) {
     constexpr int V = decltype(v)::value;
     const int64_t threads = a.seqs.n * ((a.D + V - 1) / V);
     hipLaunchKernelGGL((recurrence_step_kernel<decltype(t), V>),

@@ -521,7 +521,7 @@ struct RecurrenceGrads {
 };
 // Tiles of tokens (forward and backward) by groups of channels, and the workspace.
 struct RecurrencePlan {
-  int64_t tiles = 0, bwd_tiles = 0, groups = 0;
+  int64_t tiles = 0, bwd_tiles = 0, groups = 0, bwd_groups = 0;
   size_t tickets = 0, slots = 0, states = 0, part = 0;
   size_t saved_bytes = 0;
   size_t bytes = 0;

@@ -67,12 +67,37 @@ struct Raw {
       __builtin_memcpy(&u, e, 4);
       __builtin_amdgcn_raw_buffer_store_b32(u, r, voff, soff, 0);
     } else {
+      // (no more: nothing keeps the instruction after a store of more than eight bytes with a
+      // wave-uniform offset from writing the registers it has not read yet)
+      static_assert(sizeof(e) == 8, "two, four or eight bytes");
       u32x2 u;
       __builtin_memcpy(&u, e, 8);
       __builtin_amdgcn_raw_buffer_store_b64(u, r, voff, soff, 0);
     }
   }
 };
+
+// S rows of a tensor from token t0 on as a buffer: addresses are a lane's own part and a wave-uniform
+// one for the row.  step: bytes from row to row; bytes: of a row.
+template <int S>
+__device__ __forceinline__ buf_t rows_from(const void* base, int64_t t0, int64_t step,
+                                           int64_t bytes) {
+  return make_buf(static_cast<const char*>(base) + t0 * step,
+                  static_cast<uint32_t>((S - 1) * step + bytes));
+}
+
+// S rows from token t0 on, each lane its V channels; rows past the last token repeat it.
+template <typename T, int V, int S>
+__device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t D, int64_t t0,
+                                          int64_t tokens, int c, Raw<T, V> (&v)[S]) {
+  const int64_t step = row * static_cast<int64_t>(sizeof(T));
+  const int64_t left = tokens - t0;
+  const buf_t r = rows_from<S>(base, left > 0 ? t0 : tokens - 1, step, D * sizeof(T));
+  const int last = left > S ? S - 1 : left > 0 ? static_cast<int>(left) - 1 : 0;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    v[s].load(r, c * static_cast<int>(sizeof(T)), (s < last ? s : last) * static_cast<int>(step));
+}
 
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));

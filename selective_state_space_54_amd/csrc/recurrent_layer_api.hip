@@ -45,7 +45,7 @@ mssm_status recurrence_plan(const mssm::Sequences& s, int64_t D, bool backward, 
                             mssm_dtype dtype, mssm::RecurrencePlan* p) {
   *p = mssm::plan_recurrence(s.tokens, D, backward, saved, dtype);
   int64_t n;
-  if (!product({p->bwd_tiles, p->groups, 512}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
+  if (!product({p->bwd_tiles, p->bwd_groups, 512}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   return n < kMaxThreads ? MSSM_SUCCESS : MSSM_ERROR_NOT_SUPPORTED;
 }
 
