@@ -8,8 +8,10 @@
 //   dw_i = sum_t dz_t u_{t - (k - 1) + i},   dbias = sum_t dz_t.
 //
 // A wavefront takes a run of consecutive tokens of 64 V channels, the last k - 1 inputs in
-// registers; borders between sequences are wave-uniform and rare.  Bound by memory:
-// a run reads k - 1 rows beside its own (the gradient 2 (k - 1)).
+// registers.  Bound by memory: a run reads k - 1 rows beside its own (the gradient 2 (k - 1)).  Two
+// batches of rows take turns in registers, the next on its way while one is worked on, and no
+// branch stands around their loads and stores: what is not to be written goes to a buffer
+// of no bytes.  A batch with a border between sequences goes token by token instead.
 #include <type_traits>
 
 #include "mssm_internal.h"
@@ -22,6 +24,12 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kBatch = 8;             // tokens loaded together
+// Channels a lane and tokens a run at most, forward and backward.  131072 x 2560 values of bfloat16 in
+// 32 sequences: 4 bytes a lane 144 us, 8 bytes 148, 16 bytes 155 (runs of 128 tokens 150); its gradient
+// with 8 bytes 230 us and runs of 64 tokens about the same.
+constexpr int kFwdBytes = 4, kBwdBytes = 8;
+constexpr int64_t kFwdRun = 64, kBwdRun = 128;
+constexpr int64_t kWavesWanted = 4096;
 
 struct Lane {
   int64_t group, run;
@@ -47,22 +55,33 @@ __device__ __forceinline__ void widen(const Raw<T, V>& r, float (&v)[V]) {
   for (int j = 0; j < V; ++j) v[j] = r.get(j);
 }
 
-// win[j] = the input k - 1 - j places before token t of the cursor's sequence.
+// The input at place `at` of the cursor's sequence (valid, at < end): a token's, or one of the state's
+// K - 1 rows before it.
+template <typename T, int V, int K>
+__device__ __forceinline__ void load_place(const ConvArgs& a, const Cursor& q, int64_t at, int c,
+                                           float (&v)[V]) {
+  Raw<T, V> r;
+  r.clear();
+  if (at >= q.begin)
+    r.load(static_cast<const T*>(a.u) + at * a.u_row + c);
+  else if (a.state)
+    r.load(static_cast<const T*>(a.state) + (q.q * (K - 1) + (at - q.begin) + (K - 1)) * a.D + c);
+  r.keep();
+  widen(r, v);
+}
+
+// win[j] = the input K - 1 - j places before token t of the cursor's sequence (zero outside of one).
 template <typename T, int V, int K>
 __device__ __forceinline__ void load_window(const ConvArgs& a, const Cursor& q, int64_t t, int c,
                                             float (&win)[K > 1 ? K - 1 : 1][V]) {
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
-    const int64_t at = t - (K - 1) + j;
-    Raw<T, V> r;
-    r.clear();
     if (q.valid) {
-      if (at >= q.begin)
-        r.load(static_cast<const T*>(a.u) + at * a.u_row + c);
-      else if (a.state)
-        r.load(static_cast<const T*>(a.state) + (q.q * (K - 1) + (at - q.begin) + (K - 1)) * a.D + c);
+      load_place<T, V, K>(a, q, t - (K - 1) + j, c, win[j]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
     }
-    widen(r, win[j]);
   }
 }
 
@@ -76,88 +95,126 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int c, float (&w)[K
   }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void load_batch(const void* base, int64_t row, int64_t t0, int64_t tokens,
-                                           int c, Raw<T, V> (&v)[kBatch]) {
-#pragma unroll
-  for (int s = 0; s < kBatch; ++s) {
-    const int64_t t = t0 + s < tokens ? t0 + s : tokens - 1;
-    v[s].load(static_cast<const T*>(base) + t * row + c);
+// The last k - 1 places of each sequence, as they are: block `block` of `blocks`.
+template <typename T>
+__device__ __forceinline__ void copy_last(const ConvArgs& a, int64_t block, int64_t blocks) {
+  constexpr int64_t kPiece = 2048;
+  const int64_t K1 = a.k - 1, pieces = (K1 * a.D + kPiece - 1) / kPiece;
+  const T* u = static_cast<const T*>(a.u);
+  const T* state = static_cast<const T*>(a.state);
+  for (int64_t w = block; w < a.seqs.n * pieces; w += blocks) {
+    const int64_t q = w / pieces, e0 = (w - q * pieces) * kPiece;
+    const int64_t begin = seq_begin(a.seqs, q), end = seq_begin(a.seqs, q + 1);
+    const int64_t n = end > begin ? end - begin : 0;
+    T* last = static_cast<T*>(a.last) + q * K1 * a.D;
+    for (int64_t e = e0 + threadIdx.x; e < e0 + kPiece && e < K1 * a.D; e += kBlock) {
+      const int64_t j = e / a.D, c = e - j * a.D;
+      const int64_t at = n + j - K1;                 // token of the sequence, or before it
+      last[e] = at >= 0 ? u[(begin + at) * a.u_row + c]
+                        : state ? state[(q * K1 + n + j) * a.D + c] : T();
+    }
   }
 }
 
+// A buffer that takes what is written at rows of a batch, or nothing.
+__device__ __forceinline__ buf_t when(bool open, const char* base, int bytes) {
+  return make_buf(base, open ? static_cast<uint32_t>(bytes) : 0u);
+}
+
+// Blocks past the first `main` copy the last states.
 template <typename T, int V, int K>
-__global__ __launch_bounds__(kBlock) void conv_kernel(ConvArgs a, int64_t groups, int64_t len) {
+__global__ __launch_bounds__(kBlock, 2) void conv_kernel(ConvArgs a, int64_t groups, int64_t len,
+                                                      int64_t main) {
+  if (blockIdx.x >= main) {
+    copy_last<T>(a, blockIdx.x - main, gridDim.x - main);
+    return;
+  }
   const int64_t id = int64_t(blockIdx.x) * kWaves + MSSM_UNIFORM(static_cast<int>(threadIdx.x >> 6));
   const Lane p = lane_of<V>(a.D, id % groups, id / groups);
   const int64_t T0 = a.seqs.tokens;
   const int64_t t0 = p.run * len;
   if (t0 >= T0) return;                       // no barriers in this kernel
   const int64_t t1 = t0 + len < T0 ? t0 + len : T0;
-  Raw<T, V> u[kBatch];
-  load_batch<T, V>(a.u, a.u_row, t0, T0, p.c, u);
+  using Batch = Raw<T, V>[kBatch];
+  Batch u[2];
+  auto load = [&](Batch& to, int64_t tb) __attribute__((always_inline)) {
+    load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, T0, p.c, to);
+  };
+  load(u[0], t0);
   float w[K][V], bias[V], win[K > 1 ? K - 1 : 1][V];
   load_taps<T, V, K>(a, p.c, w, bias);
   Cursor q = cursor_at(a.seqs, t0);
   load_window<T, V, K>(a, q, t0, p.c, win);
-  T* y = static_cast<T*>(a.y) + p.c;
-  for (int64_t tb = t0; tb < t1; tb += kBatch) {
-    Raw<T, V> next[kBatch];
-    load_batch<T, V>(a.u, a.u_row, tb + kBatch, T0, p.c, next);
+  const int step = static_cast<int>(a.D * sizeof(T));
+  // (lanes that copy another's channels write out of bounds, which is dropped)
+  const int at = p.active ? p.c * static_cast<int>(sizeof(T)) : kBatch * step;
+  auto work = [&](Batch& now, int64_t tb) __attribute__((always_inline)) {
+    const char* y = static_cast<const char*>(a.y) + tb * step;
+    if (tb + kBatch <= q.end) {
+      const buf_t to = when(q.valid, y, kBatch * step);
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const int64_t t = tb + s;
-      if (t >= t1) break;
-      if (t >= q.end) {
-        q = cursor_at(a.seqs, t);
-        load_window<T, V, K>(a, q, t, p.c, win);
-      }
-      float cur[V], out[V];
-      widen(u[s], cur);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float c = bias[v];
-#pragma unroll
-        for (int i = 0; i < K - 1; ++i) c = __builtin_fmaf(w[i][v], win[i][v], c);
-        c = __builtin_fmaf(w[K - 1][v], cur[v], c);
-        out[v] = a.silu ? silu(c) : c;
-      }
-      if (q.valid && p.active) Raw<T, V>::store(y + t * a.D, out);
-      if constexpr (K > 1) {
+      for (int s = 0; s < kBatch; ++s) {
+        float cur[V], out[V];
+        widen(now[s], cur);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+          float c = bias[v];
 #pragma unroll
-          for (int i = 0; i < K - 2; ++i) win[i][v] = win[i + 1][v];
-          win[K - 2][v] = cur[v];
+          for (int i = 0; i < K - 1; ++i) c = __builtin_fmaf(w[i][v], win[i][v], c);
+          c = __builtin_fmaf(w[K - 1][v], cur[v], c);
+          out[v] = a.silu ? silu(c) : c;
+        }
+        Raw<T, V>::store(to, at, s * step, out);
+        if constexpr (K > 1) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int i = 0; i < K - 2; ++i) win[i][v] = win[i + 1][v];
+            win[K - 2][v] = cur[v];
+          }
         }
       }
+      return;
     }
+    const int64_t te = tb + kBatch < t1 ? tb + kBatch : t1;
+#pragma unroll 1
+    for (int64_t t = tb; t < te; ++t) {
+      if (t >= q.end) q = cursor_at(a.seqs, t);
+      if (!q.valid) continue;
+      float c[V];
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) u[s] = next[s];
+      for (int v = 0; v < V; ++v) c[v] = bias[v];
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        float cur[V];
+        load_place<T, V, K>(a, q, t - (K - 1) + i, p.c, cur);
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = __builtin_fmaf(w[i][v], cur[v], c[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = a.silu ? silu(c[v]) : c[v];
+      Raw<T, V>::store(when(true, y, kBatch * step), at, static_cast<int>(t - tb) * step, c);
+    }
+    if (te < t1) {
+      if (te >= q.end) q = cursor_at(a.seqs, te);
+      load_window<T, V, K>(a, q, te, p.c, win);
+    }
+  };
+  for (int64_t tb = t0; tb < t1;) {
+    load(u[1], tb + kBatch);
+    work(u[0], tb);
+    tb += kBatch;
+    if (tb >= t1) break;
+    load(u[0], tb + kBatch);
+    work(u[1], tb);
+    tb += kBatch;
   }
 }
 
-// The last k - 1 places of each sequence, as they are.
-template <typename T>
-__global__ __launch_bounds__(256) void conv_last_kernel(ConvArgs a, int64_t q0) {
-  const int64_t q = q0 + blockIdx.x, K1 = a.k - 1;
-  const int64_t begin = seq_begin(a.seqs, q), end = seq_begin(a.seqs, q + 1);
-  const int64_t n = end > begin ? end - begin : 0;
-  const T* u = static_cast<const T*>(a.u);
-  const T* state = static_cast<const T*>(a.state);
-  T* last = static_cast<T*>(a.last) + q * K1 * a.D;
-  for (int64_t e = threadIdx.x; e < K1 * a.D; e += 256) {
-    const int64_t j = e / a.D, c = e - j * a.D;
-    const int64_t at = n + j - K1;                   // token of the sequence, or before it
-    last[e] = at >= 0 ? u[(begin + at) * a.u_row + c]
-                      : state ? state[(q * K1 + n + j) * a.D + c] : T();
-  }
-}
-
-// part: [gridDim.y, K + 1, D]: the blocks' sums for the taps and the bias.
+// part: [rows of blocks, K + 1, D]: the blocks' sums for the taps and the bias.
 template <typename T, int V, int K>
-__global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvArgs a, ConvGrads d, int64_t groups,
-                                                          int64_t len, float* part) {
+__global__ __launch_bounds__(kBlock, 2) void conv_bwd_kernel(ConvArgs a, ConvGrads d, int64_t groups,
+                                                             int64_t len, float* part) {
   __shared__ float m[kWaves][(K + 1) * V][64];
   const int wave = MSSM_UNIFORM(static_cast<int>(threadIdx.x >> 6));
   const int64_t brow = blockIdx.x / groups;
@@ -173,28 +230,29 @@ __global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvArgs a, ConvGrads 
     for (int i = 0; i < K; ++i) dw[i][v] = 0.0f;
   }
   if (t0 < T0) {
-    Raw<T, V> u[kBatch], g[kBatch];
-    load_batch<T, V>(a.u, a.u_row, t0, T0, p.c, u);
-    load_batch<T, V>(d.dy, a.D, t0, T0, p.c, g);
+    using Batch = Raw<T, V>[kBatch];
+    Batch u[2], g[2];
+    auto load = [&](int k, int64_t tb) __attribute__((always_inline)) {
+      load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, T0, p.c, u[k]);
+      load_rows<T, V, kBatch>(d.dy, a.D, a.D, tb, T0, p.c, g[k]);
+    };
+    load(0, t0);
     float w[K][V], bias[V], win[K > 1 ? K - 1 : 1][V];
     load_taps<T, V, K>(a, p.c, w, bias);
     Cursor q = cursor_at(a.seqs, t0);
     load_window<T, V, K>(a, q, t0, p.c, win);
+    const int step = static_cast<int>(a.D * sizeof(T));
+    const int at = p.active ? p.c * static_cast<int>(sizeof(T)) : kBatch * step;
     float acc[K][V];              // du of the places t - (K - 1) .. t, so far
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[j][v] = 0.0f;
-    // du of place `at` of the cursor's sequence is complete: written by the run that has the token,
-    // or the sequence's first token for the state's rows.
-    auto emit = [&](int64_t at, const float (&val)[V]) __attribute__((always_inline)) {
-      if (at >= q.begin) {
-        if (at >= t0 && at < t1 && p.active)
-          Raw<T, V>::store(static_cast<T*>(d.du) + at * a.D + p.c, val);
-      } else if (d.dstate && q.begin >= t0 && q.begin < t1 && p.active) {
+    // du of a state's row is complete: written by the run that has the sequence's first token.
+    auto emit_state = [&](int64_t place, const float (&val)[V]) __attribute__((always_inline)) {
+      if (d.dstate && q.begin >= t0 && q.begin < t1 && p.active)
         Raw<T, V>::store(static_cast<T*>(d.dstate) +
-                             (q.q * (K - 1) + (at - q.begin) + (K - 1)) * a.D + p.c, val);
-      }
+                             (q.q * (K - 1) + (place - q.begin) + (K - 1)) * a.D + p.c, val);
     };
     // The sequence ends before token t: the K - 1 places before t are complete.
     auto flush = [&](int64_t t) __attribute__((always_inline)) {
@@ -210,70 +268,108 @@ __global__ __launch_bounds__(kBlock) void conv_bwd_kernel(ConvArgs a, ConvGrads 
 #pragma unroll
           for (int v = 0; v < V; ++v) val[v] += r.get(v);
         }
-        emit(t - (K - 1) + j, val);
+        const int64_t place = t - (K - 1) + j;
+        if (place < q.begin) emit_state(place, val);
+        else if (place >= t0 && place < t1 && p.active)
+          Raw<T, V>::store(static_cast<T*>(d.du) + place * a.D + p.c, val);
+      }
+    };
+    // Token t of the cursor's sequence with its input and gradient: the sums for the taps, and what it
+    // adds to the places it reaches; the oldest of them is complete then, in acc[0].
+    auto token = [&](int64_t t, const float (&cur)[V], float (&dz)[V]) __attribute__((always_inline)) {
+      if (a.silu) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float c = bias[v];
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i) c = __builtin_fmaf(w[i][v], win[i][v], c);
+          c = __builtin_fmaf(w[K - 1][v], cur[v], c);
+          const float e = sigmoid(c);
+          dz[v] *= e * __builtin_fmaf(c, 1.0f - e, 1.0f);
+        }
+      }
+      if (t < t1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i) dw[i][v] = __builtin_fmaf(dz[v], win[i][v], dw[i][v]);
+          dw[K - 1][v] = __builtin_fmaf(dz[v], cur[v], dw[K - 1][v]);
+          db[v] += dz[v];
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < K; ++j)             // place t - (K - 1) + j meets tap j
+          acc[j][v] = __builtin_fmaf(w[j][v], dz[v], acc[j][v]);
+    };
+    auto move_on = [&](const float (&cur)[V]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) acc[j][v] = acc[j + 1][v];
+        acc[K - 1][v] = 0.0f;
+        if constexpr (K > 1) {
+#pragma unroll
+          for (int i = 0; i < K - 2; ++i) win[i][v] = win[i + 1][v];
+          win[K - 2][v] = cur[v];
+        }
       }
     };
     const int64_t stop = t1 + K - 1;            // tokens up to t1 + K - 2 reach back into the run
-    for (int64_t tb = t0; tb < stop; tb += kBatch) {
-      Raw<T, V> un[kBatch], gn[kBatch];
-      load_batch<T, V>(a.u, a.u_row, tb + kBatch, T0, p.c, un);
-      load_batch<T, V>(d.dy, a.D, tb + kBatch, T0, p.c, gn);
+    auto work = [&](int k, int64_t tb) __attribute__((always_inline)) {
+      // the row that token tb completes
+      const char* du = static_cast<const char*>(d.du) + (tb - (K - 1)) * step;
+      if (tb + kBatch <= q.end && tb - (K - 1) >= q.begin) {
+        if (!q.valid) return;
 #pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        const int64_t t = tb + s;
-        if (t >= stop) break;
-        if (t >= q.end || t >= T0) {
+        for (int s = 0; s < kBatch; ++s) {
+          const int64_t t = tb + s, place = t - (K - 1);
+          float cur[V], dz[V];
+          widen(u[k][s], cur);
+          widen(g[k][s], dz);
+          token(t, cur, dz);
+          Raw<T, V>::store(when(place >= t0 && place < t1, du, kBatch * step), at, s * step, acc[0]);
+          move_on(cur);
+        }
+        return;
+      }
+      const int64_t te = tb + kBatch < stop ? tb + kBatch : stop;
+#pragma unroll 1
+      for (int64_t t = tb; t < te; ++t) {
+        if (t >= q.end) {                       // (past the last token: no sequence)
           flush(t);
 #pragma unroll
           for (int j = 0; j < K; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[j][v] = 0.0f;
-          if (t >= t1) {                        // what follows does not reach back
-            tb = stop;
-            break;
-          }
           q = cursor_at(a.seqs, t);
           load_window<T, V, K>(a, q, t, p.c, win);
         }
         if (!q.valid) continue;
+        const int64_t place = t - (K - 1);
         float cur[V], dz[V];
-        widen(u[s], cur);
-        widen(g[s], dz);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (a.silu) {
-            float c = bias[v];
-#pragma unroll
-            for (int i = 0; i < K - 1; ++i) c = __builtin_fmaf(w[i][v], win[i][v], c);
-            c = __builtin_fmaf(w[K - 1][v], cur[v], c);
-            const float e = sigmoid(c);
-            dz[v] *= e * __builtin_fmaf(c, 1.0f - e, 1.0f);
-          }
-          if (t < t1) {
-#pragma unroll
-            for (int i = 0; i < K - 1; ++i) dw[i][v] = __builtin_fmaf(dz[v], win[i][v], dw[i][v]);
-            dw[K - 1][v] = __builtin_fmaf(dz[v], cur[v], dw[K - 1][v]);
-            db[v] += dz[v];
-          }
-#pragma unroll
-          for (int j = 0; j < K; ++j)           // place t - (K - 1) + j meets tap j
-            acc[j][v] = __builtin_fmaf(w[j][v], dz[v], acc[j][v]);
-        }
-        emit(t - (K - 1), acc[0]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) acc[j][v] = acc[j + 1][v];
-          acc[K - 1][v] = 0.0f;
-          if constexpr (K > 1) {
-#pragma unroll
-            for (int i = 0; i < K - 2; ++i) win[i][v] = win[i + 1][v];
-            win[K - 2][v] = cur[v];
-          }
-        }
+        Raw<T, V> r;
+        load_place<T, V, K>(a, q, t, p.c, cur);
+        r.load(static_cast<const T*>(d.dy) + t * a.D + p.c);
+        r.keep();
+        widen(r, dz);
+        token(t, cur, dz);
+        if (place < q.begin) emit_state(place, acc[0]);
+        else
+          Raw<T, V>::store(when(place >= t0 && place < t1, du, kBatch * step), at,
+                           static_cast<int>(t - tb) * step, acc[0]);
+        move_on(cur);
       }
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) u[s] = un[s], g[s] = gn[s];
+    };
+    for (int64_t tb = t0; tb < stop;) {
+      load(1, tb + kBatch);
+      work(0, tb);
+      tb += kBatch;
+      if (tb >= stop) break;
+      load(0, tb + kBatch);
+      work(1, tb);
+      tb += kBatch;
     }
   }
 #pragma unroll
@@ -300,8 +396,10 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict_
   const int64_t c = int64_t(blockIdx.x) * 64 + col;
   const int i = blockIdx.y;
   double s = 0.0;
-  if (c < D)
+  if (c < D) {
+#pragma unroll 8
     for (int64_t r = w; r < rows; r += 16) s += part[(r * (K + 1) + i) * D + c];
+  }
   m[w][col] = s;
   block_sync();
   if (w != 0 || c >= D) return;
@@ -382,15 +480,12 @@ struct ConvGrid {
 ConvGrid conv_grid(int64_t tokens, int64_t D, int V, int64_t longest) {
   ConvGrid g;
   g.groups = (D + 64 * V - 1) / (64 * V);
-  int64_t len = tokens / (4096 / (g.groups < 4096 ? g.groups : 4096));
+  int64_t len = tokens / (kWavesWanted / (g.groups < kWavesWanted ? g.groups : kWavesWanted));
   len = (len + kBatch - 1) / kBatch * kBatch;
   g.len = len < kBatch ? kBatch : len > longest ? longest : len;
   g.runs = (tokens + g.len - 1) / g.len;
   return g;
 }
-constexpr int kFwdBytes = 16, kBwdBytes = 8;
-constexpr int64_t kFwdRun = 64, kBwdRun = 128;
-
 int vec_of(mssm_dtype dtype, int64_t D, int bytes) {
   const int V = bytes / (dtype == MSSM_BFLOAT16 ? 2 : 4);
   return D >= V ? V : 1;
@@ -420,24 +515,21 @@ size_t conv_bwd_workspace(int64_t tokens, int64_t D, int64_t k, mssm_dtype dtype
 }
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
-  if (a.last && a.k > 1) {
-    for (int64_t q = 0; q < a.seqs.n; q += kMaxSequences) {
-      const dim3 grid(static_cast<uint32_t>(a.seqs.n - q < kMaxSequences ? a.seqs.n - q
-                                                                         : kMaxSequences));
-      if (a.dtype == MSSM_BFLOAT16)
-        hipLaunchKernelGGL(conv_last_kernel<uint16_t>, grid, dim3(256), 0, stream, a, q);
-      else
-        hipLaunchKernelGGL(conv_last_kernel<float>, grid, dim3(256), 0, stream, a, q);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
+  int64_t main = 0, last = 0;
+  ConvGrid g{1, kBatch, 0};
+  if (a.seqs.tokens > 0) {
+    g = fwd_grid(a.seqs.tokens, a.D, a.dtype);
+    main = (g.groups * g.runs + kWaves - 1) / kWaves;
   }
-  if (a.seqs.tokens == 0) return hipSuccess;
-  const ConvGrid g = fwd_grid(a.seqs.tokens, a.D, a.dtype);
-  const dim3 grid(static_cast<uint32_t>((g.groups * g.runs + kWaves - 1) / kWaves));
+  if (a.last && a.k > 1) {
+    last = a.seqs.n * ((a.k * a.D + 2047) / 2048);
+    if (last > 4096) last = 4096;
+  }
+  if (main + last == 0) return hipSuccess;
   return with_taps<kFwdBytes>(a.dtype, a.D, a.k, [&](auto t, auto v, auto k) {
-    hipLaunchKernelGGL((conv_kernel<decltype(t), decltype(v)::value, decltype(k)::value>), grid,
-                       dim3(kBlock), 0, stream, a, g.groups, g.len);
+    hipLaunchKernelGGL((conv_kernel<decltype(t), decltype(v)::value, decltype(k)::value>),
+                       dim3(static_cast<uint32_t>(main + last)), dim3(kBlock), 0, stream, a,
+                       g.groups, g.len, main);
     return hipGetLastError();
   });
 }
