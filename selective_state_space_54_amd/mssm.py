@@ -1165,12 +1165,24 @@ _size_of = functools.lru_cache(maxsize=1024)(_size_query)
 
 
 def _expect_grads(grads, shapes, dev):
-    """Checks a dict of gradients; returns their addresses by name."""
+    """Checks a dict of gradients."""
     for name, t in grads.items():
         if name not in shapes:
             raise ValueError(f"unknown gradient {name}")
         _expect(t, name, *shapes[name], dev)
-    return lambda name: _address(grads.get(name))
+
+
+def _empty(t):
+    """A dense tensor of t's shape and dtype."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _room(nbytes, like):
+    """(tensor, address, bytes) of a workspace on `like`'s GPU; like is float32."""
+    if not nbytes:
+        return None, None, 0
+    t = like.new_empty((nbytes + 3) // 4)
+    return t, t.data_ptr(), nbytes
 
 
 _ACTIVATIONS = {None: MSSM_ACT_NONE, "silu": MSSM_ACT_SILU}
@@ -1223,31 +1235,37 @@ def causal_conv1d(u, weight, bias=None, *, activation="silu", state=None, seq_of
     dt = u.dtype
     _expect_optional(state, "state", dt, (seqs, k - 1, D), dev)
     with _on(stream):
-        y = torch.empty_like(u, memory_format=torch.contiguous_format)
-        last = torch.empty((seqs, k - 1, D), dtype=dt, device=dev) if return_state else None
+        y = _empty(u)
+        last = u.new_empty((seqs, k - 1, D)) if return_state else None
     _call("mssm_causal_conv1d_fwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
           _address(seq_offsets), _address(state), y.data_ptr(), _address(last), act, seqs, L, D, k,
           row, _DTYPES[dt])
     return (y, last) if return_state else y
 
 
-def mssm_causal_conv1d_step(u, weight, bias, state, y, *, activation="silu", stream=None):
-    """One token for each sequence: u, y [batch, D]; state [batch, k - 1, D] moves on by one
-    place."""
-    dev, (seqs, _, D, k), row = _conv_check(u, weight, bias, None, True)
+def _conv_step(checked, u, weight, bias, state, y, activation, stream):
+    dev, (seqs, _, D, k), row = checked
     act = _activation(activation)
     _expect(state, "state", u.dtype, (seqs, k - 1, D), dev)
-    _expect(y, "y", u.dtype, (seqs, D), dev)
     _call("mssm_causal_conv1d_step", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
           state.data_ptr(), y.data_ptr(), act, seqs, D, k, row, _DTYPES[u.dtype])
     return y
 
 
+def mssm_causal_conv1d_step(u, weight, bias, state, y, *, activation="silu", stream=None):
+    """One token for each sequence: u, y [batch, D]; state [batch, k - 1, D] moves on by one
+    place."""
+    checked = _conv_check(u, weight, bias, None, True)
+    _expect(y, "y", u.dtype, u.shape, checked[0])
+    return _conv_step(checked, u, weight, bias, state, y, activation, stream)
+
+
 def causal_conv1d_step(u, weight, bias, state, *, activation="silu", stream=None):
     """Allocate y, run mssm_causal_conv1d_step (state updated in place), return y."""
+    checked = _conv_check(u, weight, bias, None, True)
     with _on(stream):
-        y = torch.empty_like(u, memory_format=torch.contiguous_format)
-    return mssm_causal_conv1d_step(u, weight, bias, state, y, activation=activation, stream=stream)
+        y = _empty(u)
+    return _conv_step(checked, u, weight, bias, state, y, activation, stream)
 
 
 def mssm_causal_conv1d_bwd_workspace_size(seqs, L, D, k, dtype, *, packed=False) -> int:
@@ -1255,24 +1273,32 @@ def mssm_causal_conv1d_bwd_workspace_size(seqs, L, D, k, dtype, *, packed=False)
                        _dtype_code(dtype))
 
 
+def _conv_bwd(checked, u, weight, bias, dy, grads, workspace, activation, state, dstate, seq_offsets,
+              stream):
+    dev, (seqs, L, D, k), row = checked
+    act, dt, g = _activation(activation), u.dtype, grads.get
+    _expect(dy, "dy", dt, u.shape, dev)
+    _expect_optional(state, "state", dt, (seqs, k - 1, D), dev)
+    _expect_optional(dstate, "dstate", dt, (seqs, k - 1, D), dev)
+    _call("mssm_causal_conv1d_bwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
+          _address(seq_offsets), _address(state), dy.data_ptr(), _address(dstate),
+          _address(g("du")), _address(g("dweight")), _address(g("dbias")), _address(g("dstate")),
+          act, *workspace, seqs, L, D, k, row, _DTYPES[dt])
+    return grads
+
+
 def mssm_causal_conv1d_bwd(u, weight, bias, dy, grads, workspace, *, activation="silu", state=None,
                            dstate=None, seq_offsets=None, stream=None):
     """Gradients of sum(dy * y) + sum(dstate * last state) of causal_conv1d.  ``grads`` maps du,
     dweight and, where wanted, dbias and dstate (the initial state's) to dense tensors that are
     overwritten."""
-    dev, (seqs, L, D, k), row = _conv_check(u, weight, bias, seq_offsets)
-    act = _activation(activation)
-    states = (u.dtype, (seqs, k - 1, D))
-    _expect(dy, "dy", u.dtype, u.shape, dev)
-    _expect_optional(state, "state", *states, dev)
-    _expect_optional(dstate, "dstate", *states, dev)
-    g = _expect_grads(grads, {"du": (u.dtype, u.shape), "dweight": (torch.float32, (D, k)),
-                              "dbias": (torch.float32, (D,)), "dstate": states}, dev)
-    _call("mssm_causal_conv1d_bwd", dev, stream, u.data_ptr(), weight.data_ptr(), _address(bias),
-          _address(seq_offsets), _address(state), dy.data_ptr(), _address(dstate), g("du"),
-          g("dweight"), g("dbias"), g("dstate"), act, *_workspace_args(workspace, u.device), seqs,
-          L, D, k, row, _DTYPES[u.dtype])
-    return grads
+    checked = _conv_check(u, weight, bias, seq_offsets)
+    dev, (seqs, _, D, k), _ = checked
+    _expect_grads(grads, {"du": (u.dtype, u.shape), "dweight": (torch.float32, (D, k)),
+                          "dbias": (torch.float32, (D,)),
+                          "dstate": (u.dtype, (seqs, k - 1, D))}, dev)
+    return _conv_bwd(checked, u, weight, bias, dy, grads, _workspace_args(workspace, u.device),
+                     activation, state, dstate, seq_offsets, stream)
 
 
 def causal_conv1d_bwd(u, weight, bias, dy, *, activation="silu", state=None, dstate=None,
@@ -1281,21 +1307,19 @@ def causal_conv1d_bwd(u, weight, bias, dy, *, activation="silu", state=None, dst
     returns the dict of gradients: du, dweight, dbias where there is a bias, and dstate, the initial
     state's, where ``state`` is given.  ``dstate`` is the gradient of the last state, if it has
     one."""
-    dev, (seqs, L, D, k), _ = _conv_check(u, weight, bias, seq_offsets)
-    nbytes = _size_of("mssm_causal_conv1d_bwd_workspace_size", seqs, L, D, k,
+    checked = _conv_check(u, weight, bias, seq_offsets)
+    nbytes = _size_of("mssm_causal_conv1d_bwd_workspace_size", *checked[1],
                       int(seq_offsets is not None), _DTYPES[u.dtype])
     with _on(stream):
-        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
-        grads = {"du": empty(u), "dweight": empty(weight)}
+        grads = {"du": _empty(u), "dweight": _empty(weight)}
         if bias is not None:
-            grads["dbias"] = empty(bias)
+            grads["dbias"] = _empty(bias)
         if state is not None:
             _expect_tensor(state, "state")
-            grads["dstate"] = empty(state)
-        ws = _workspace(nbytes, dev)
-    return mssm_causal_conv1d_bwd(u, weight, bias, dy, grads, ws, activation=activation,
-                                  state=state, dstate=dstate, seq_offsets=seq_offsets,
-                                  stream=stream)
+            grads["dstate"] = _empty(state)
+        room, *ws = _room(nbytes, weight)
+    return _conv_bwd(checked, u, weight, bias, dy, grads, ws, activation, state, dstate,
+                     seq_offsets, stream)
 
 
 def _recurrence_check(x, input_gate, decay_gate, A, seq_offsets, single=False):
@@ -1326,8 +1350,7 @@ def _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h
     dev, sizes, tail = checked
     _call("mssm_gated_recurrence_fwd", dev, stream, x.data_ptr(), input_gate.data_ptr(),
           decay_gate.data_ptr(), A.data_ptr(), _address(seq_offsets), _address(state),
-          h.data_ptr(), _address(last), *_workspace_args(saved, x.device),
-          *_workspace_args(workspace, x.device), *sizes, *tail)
+          h.data_ptr(), _address(last), *saved, *workspace, *sizes, *tail)
 
 
 def mssm_gated_recurrence_fwd(x, input_gate, decay_gate, A, h, workspace, *, state=None,
@@ -1339,8 +1362,8 @@ def mssm_gated_recurrence_fwd(x, input_gate, decay_gate, A, h, workspace, *, sta
     _expect(h, "h", x.dtype, x.shape, dev)
     _expect_optional(state, "state", torch.float32, (seqs, D), dev)
     _expect_optional(last_state, "last_state", torch.float32, (seqs, D), dev)
-    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last_state, saved,
-                    workspace, stream)
+    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last_state,
+                    _workspace_args(saved, x.device), _workspace_args(workspace, x.device), stream)
     return h
 
 
@@ -1363,14 +1386,15 @@ def gated_recurrence(x, input_gate, decay_gate, A, *, state=None, seq_offsets=No
     nbytes = _size_of("mssm_gated_recurrence_workspace_size", *sizes, packed, 0, int(return_saved),
                       tail[3])
     with _on(stream):
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
-        last = torch.empty((seqs, D), dtype=torch.float32, device=dev) if return_state else None
-        saved = None
+        h = _empty(x)
+        last = A.new_empty((seqs, D)) if return_state else None
+        saved, kept = None, (None, 0)
         if return_saved:
             size = _size_of("mssm_gated_recurrence_saved_size", *sizes, packed, tail[3])
             saved = torch.empty(size, dtype=torch.uint8, device=dev)
-        ws = _workspace(nbytes, dev)
-    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last, saved, ws,
+            kept = (saved.data_ptr() if size else None, size)
+        room, *ws = _room(nbytes, A)
+    _recurrence_fwd(checked, x, input_gate, decay_gate, A, seq_offsets, state, h, last, kept, ws,
                     stream)
     if not return_state and not return_saved:
         return h
@@ -1397,8 +1421,24 @@ def gated_recurrence_step(x, input_gate, decay_gate, A, state, *, stream=None):
     """Allocate h, run mssm_gated_recurrence_step (state updated in place), return h."""
     checked = _recurrence_check(x, input_gate, decay_gate, A, None, True)
     with _on(stream):
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = _empty(x)
     return _recurrence_step(checked, x, input_gate, decay_gate, A, state, h, stream)
+
+
+def _recurrence_bwd(checked, x, input_gate, decay_gate, A, dh, grads, workspace, saved, state, dstate,
+                    seq_offsets, stream):
+    dev, sizes, tail = checked
+    seqs, _, D = sizes
+    _expect(dh, "dh", x.dtype, x.shape, dev)
+    _expect_optional(state, "state", torch.float32, (seqs, D), dev)
+    _expect_optional(dstate, "dstate", torch.float32, (seqs, D), dev)
+    g = grads.get
+    _call("mssm_gated_recurrence_bwd", dev, stream, x.data_ptr(), input_gate.data_ptr(),
+          decay_gate.data_ptr(), A.data_ptr(), _address(seq_offsets), _address(state),
+          *_workspace_args(saved, x.device), dh.data_ptr(), _address(dstate), _address(g("dx")),
+          _address(g("dinput_gate")), _address(g("ddecay_gate")), _address(g("dA")),
+          _address(g("dstate")), *workspace, *sizes, *tail)
+    return grads
 
 
 def mssm_gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, grads, workspace, *, saved=None,
@@ -1407,22 +1447,15 @@ def mssm_gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, grads, workspace
     dinput_gate, ddecay_gate (of x's dtype), dA (float32) and, where wanted, dstate (the initial
     state's) to dense tensors that are overwritten.  The workspace is that of a call with or without
     ``saved``."""
-    dev, sizes, tail = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
-    seqs, _, D = sizes
+    checked = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    dev, (seqs, _, D), _ = checked
     dt, shape = x.dtype, x.shape
-    states = (torch.float32, (seqs, D))
-    _expect(dh, "dh", dt, shape, dev)
-    _expect_optional(state, "state", *states, dev)
-    _expect_optional(dstate, "dstate", *states, dev)
-    g = _expect_grads(grads, {"dx": (dt, shape), "dinput_gate": (dt, shape),
-                              "ddecay_gate": (dt, shape), "dA": (torch.float32, (D,)),
-                              "dstate": states}, dev)
-    _call("mssm_gated_recurrence_bwd", dev, stream, x.data_ptr(), input_gate.data_ptr(),
-          decay_gate.data_ptr(), A.data_ptr(), _address(seq_offsets), _address(state),
-          *_workspace_args(saved, x.device), dh.data_ptr(), _address(dstate), g("dx"),
-          g("dinput_gate"), g("ddecay_gate"), g("dA"), g("dstate"),
-          *_workspace_args(workspace, x.device), *sizes, *tail)
-    return grads
+    _expect_grads(grads, {"dx": (dt, shape), "dinput_gate": (dt, shape),
+                          "ddecay_gate": (dt, shape), "dA": (torch.float32, (D,)),
+                          "dstate": (torch.float32, (seqs, D))}, dev)
+    return _recurrence_bwd(checked, x, input_gate, decay_gate, A, dh, grads,
+                           _workspace_args(workspace, x.device), saved, state, dstate, seq_offsets,
+                           stream)
 
 
 def gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, *, saved=None, state=None, dstate=None,
@@ -1431,19 +1464,19 @@ def gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, *, saved=None, state=
     returns the dict of gradients: dx, dinput_gate, ddecay_gate, dA, and dstate, the initial
     state's, where ``state`` is given.  ``saved``: what gated_recurrence returned for the same
     inputs; ``dstate``: the gradient of the last state, if it has one."""
-    dev, sizes, tail = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    checked = _recurrence_check(x, input_gate, decay_gate, A, seq_offsets)
+    _, sizes, tail = checked
     nbytes = _size_of("mssm_gated_recurrence_workspace_size", *sizes, int(seq_offsets is not None),
                       1, int(saved is not None), tail[3])
     with _on(stream):
-        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
-        grads = {"dx": empty(x), "dinput_gate": empty(x), "ddecay_gate": empty(x), "dA": empty(A)}
+        grads = {"dx": _empty(x), "dinput_gate": _empty(x), "ddecay_gate": _empty(x),
+                 "dA": _empty(A)}
         if state is not None:
             _expect_tensor(state, "state")
-            grads["dstate"] = empty(state)
-        ws = _workspace(nbytes, dev)
-    return mssm_gated_recurrence_bwd(x, input_gate, decay_gate, A, dh, grads, ws, saved=saved,
-                                     state=state, dstate=dstate, seq_offsets=seq_offsets,
-                                     stream=stream)
+            grads["dstate"] = _empty(state)
+        room, *ws = _room(nbytes, A)
+    return _recurrence_bwd(checked, x, input_gate, decay_gate, A, dh, grads, ws, saved, state,
+                           dstate, seq_offsets, stream)
 
 
 _GATE_FORMS = {"silu": MSSM_ACT_SILU, "linear": MSSM_ACT_NONE}
@@ -1516,7 +1549,7 @@ def residual_norm(y, residual, weight, *, post_weight=None, gate=None, gate_form
     with _on(stream):
         out, total = torch.empty_like(y), torch.empty_like(y)
         if return_stats:
-            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            rstd = weight.new_empty(shape[:-1])
             post_rstd = torch.empty_like(rstd) if post_weight is not None else None
     _call("mssm_residual_norm_fwd", dev, stream, y.data_ptr(), residual.data_ptr(),
           weight.data_ptr(), _address(post_weight), _address(gate), _address(scale),
@@ -1531,14 +1564,9 @@ def mssm_residual_norm_bwd_workspace_size(rows, D, dtype, *, gate_rows=1) -> int
                        _dtype_code(dtype))
 
 
-def mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, workspace, *, dtotal=None,
-                           post_weight=None, post_rstd=None, gate=None, gate_form="silu",
-                           scale=None, stream=None):
-    """Gradients of sum(dout * out) (+ sum(dtotal * total)) of residual_norm.  ``grads`` maps dy,
-    dresidual, dweight and, with post_weight, gate and scale, dpost_weight, dgate and dscale to
-    dense tensors that are overwritten."""
-    dev, rows, D, form, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form,
-                                                         scale)
+def _residual_norm_bwd(checked, dout, y, total, weight, rstd, grads, workspace, dtotal, post_weight,
+                       post_rstd, gate, scale, stream):
+    dev, rows, D, form, gate_rows = checked
     dt, shape = y.dtype, y.shape
     _expect(dout, "dout", dt, shape, dev)
     _expect(total, "total", dt, shape, dev)
@@ -1546,21 +1574,37 @@ def mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, workspace, *, dt
     _expect_optional(dtotal, "dtotal", dt, shape, dev)
     if post_weight is not None:
         _expect(post_rstd, "post_rstd", torch.float32, shape[:-1], dev)
-    shapes = {"dy": (dt, shape), "dresidual": (dt, shape), "dweight": (torch.float32, (D,))}
-    if post_weight is not None:
-        shapes["dpost_weight"] = (torch.float32, (D,))
-    if gate is not None:
-        shapes["dgate"] = (dt, gate.shape)
-    if scale is not None:
-        shapes["dscale"] = (torch.float32, (D,))
-    g = _expect_grads(grads, shapes, dev)
+    g = grads.get
     _call("mssm_residual_norm_bwd", dev, stream, dout.data_ptr(), _address(dtotal), y.data_ptr(),
           total.data_ptr(), weight.data_ptr(), _address(post_weight), _address(gate),
           _address(scale), rstd.data_ptr(),
-          _address(post_rstd) if post_weight is not None else None, g("dy"), g("dresidual"),
-          g("dgate"), g("dweight"), g("dpost_weight"), g("dscale"), form, gate_rows,
-          *_workspace_args(workspace, y.device), rows, D, _DTYPES[dt])
+          _address(post_rstd) if post_weight is not None else None, _address(g("dy")),
+          _address(g("dresidual")), _address(g("dgate")), _address(g("dweight")),
+          _address(g("dpost_weight")), _address(g("dscale")), form, gate_rows, *workspace, rows, D,
+          _DTYPES[dt])
     return grads
+
+
+def mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, workspace, *, dtotal=None,
+                           post_weight=None, post_rstd=None, gate=None, gate_form="silu",
+                           scale=None, stream=None):
+    """Gradients of sum(dout * out) (+ sum(dtotal * total)) of residual_norm.  ``grads`` maps dy,
+    dresidual, dweight and, with post_weight, gate and scale, dpost_weight, dgate and dscale to
+    dense tensors that are overwritten."""
+    checked = _residual_norm_check(y, weight, post_weight, gate, gate_form, scale)
+    dev, _, D = checked[:3]
+    dt, shape, column = y.dtype, y.shape, (torch.float32, (D,))
+    shapes = {"dy": (dt, shape), "dresidual": (dt, shape), "dweight": column}
+    if post_weight is not None:
+        shapes["dpost_weight"] = column
+    if gate is not None:
+        shapes["dgate"] = (dt, gate.shape)
+    if scale is not None:
+        shapes["dscale"] = column
+    _expect_grads(grads, shapes, dev)
+    return _residual_norm_bwd(checked, dout, y, total, weight, rstd, grads,
+                              _workspace_args(workspace, y.device), dtotal, post_weight, post_rstd,
+                              gate, scale, stream)
 
 
 def residual_norm_bwd(dout, y, total, weight, rstd, *, dtotal=None, post_weight=None,
@@ -1569,15 +1613,14 @@ def residual_norm_bwd(dout, y, total, weight, rstd, *, dtotal=None, post_weight=
     the dict of gradients: dy, dresidual, dweight, and dpost_weight, dgate, dscale for what is
     given.  total, rstd and post_rstd are what residual_norm returned; ``dtotal`` is the gradient
     that reaches total itself."""
-    dev, rows, D, _, gate_rows = _residual_norm_check(y, weight, post_weight, gate, gate_form, scale)
+    checked = _residual_norm_check(y, weight, post_weight, gate, gate_form, scale)
+    _, rows, D, _, gate_rows = checked
     nbytes = _size_of("mssm_residual_norm_bwd_workspace_size", rows, D, gate_rows, _DTYPES[y.dtype])
     with _on(stream):
-        empty = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dev)
-        grads = {"dy": empty(y), "dresidual": empty(y), "dweight": empty(weight)}
+        grads = {"dy": _empty(y), "dresidual": _empty(y), "dweight": _empty(weight)}
         for name, t in (("dpost_weight", post_weight), ("dgate", gate), ("dscale", scale)):
             if t is not None:
-                grads[name] = empty(t)
-        ws = _workspace(nbytes, dev)
-    return mssm_residual_norm_bwd(dout, y, total, weight, rstd, grads, ws, dtotal=dtotal,
-                                  post_weight=post_weight, post_rstd=post_rstd, gate=gate,
-                                  gate_form=gate_form, scale=scale, stream=stream)
+                grads[name] = _empty(t)
+        room, *ws = _room(nbytes, weight)
+    return _residual_norm_bwd(checked, dout, y, total, weight, rstd, grads, ws, dtotal, post_weight,
+                              post_rstd, gate, scale, stream)
