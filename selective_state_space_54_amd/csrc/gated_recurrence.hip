@@ -378,17 +378,20 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
   // (the wavefronts of a block have the same channels: all of them take the same branch)
   auto work = [&](auto near_) __attribute__((always_inline)) {
     constexpr bool kNear = decltype(near_)::value;
-    float sg[S][V], e[S][V], bb[S][V];     // sigmoid(r), the decay; the input term, then h_{t-1}
+    // sigmoid(r), a, sigmoid(i) and that times x, m; the input term, then h_{t-1}
+    float sg[S][V], k[S][V], g[S][V], gx[S][V], m[S][V], bb[S][V];
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         sg[s][v] = sigmoid(gr[s].get(v));
-        e[s][v] = decay_of<kNear>(rate[v] * sg[s][v]);
-        bb[s][v] = sqrt_(one_minus_square<kNear>(e[s][v])) * (sigmoid(gi[s].get(v)) * x[s].get(v));
+        const float q = decay_of<kNear>(rate[v] * sg[s][v]);
+        k[s][v] = decay<kNear>(q);
+        m[s][v] = sqrt_(one_minus_square<kNear>(q));
+        g[s][v] = sigmoid(gi[s].get(v));
+        gx[s][v] = g[s][v] * x[s].get(v);
+        bb[s][v] = m[s][v] * gx[s][v];
       }
-#pragma unroll
-    for (int s = 0; s < S; ++s) x[s].keep(), gi[s].keep();      // widened again below
 
     // The wavefront's maps: of the state, and of psi (from behind its tokens to before them).
     float P[V], H[V], Pf[V], Hf[V];
@@ -399,10 +402,8 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float k = decay<kNear>(e[s][v]);
-          Hf[v] = __builtin_fmaf(k, Hf[v], bb[s][v]), Pf[v] *= k;
-          const float q = decay<kNear>(e[S - 1 - s][v]);
-          H[v] = q * (dh[S - 1 - s].get(v) + H[v]);
+          Hf[v] = __builtin_fmaf(k[s][v], Hf[v], bb[s][v]), Pf[v] *= k[s][v];
+          H[v] = k[S - 1 - s][v] * (dh[S - 1 - s].get(v) + H[v]);
         }
 #pragma unroll
       for (int v = 0; v < V; ++v) P[v] = Pf[v];
@@ -411,18 +412,16 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float k = decay<kNear>(e[s][v]);
-          if (span.first >> s & 1) Pf[v] = 0.0f, Hf[v] = __builtin_fmaf(k, state(s, v), bb[s][v]);
-          else Hf[v] = __builtin_fmaf(k, Hf[v], bb[s][v]), Pf[v] *= k;
+          if (span.first >> s & 1) Pf[v] = 0.0f, Hf[v] = __builtin_fmaf(k[s][v], state(s, v), bb[s][v]);
+          else Hf[v] = __builtin_fmaf(k[s][v], Hf[v], bb[s][v]), Pf[v] *= k[s][v];
         }
 #pragma unroll
       for (int s = S - 1; s >= 0; --s)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float k = decay<kNear>(e[s][v]);
           if (span.last >> s & 1) P[v] = 0.0f, H[v] = dlast(s, v);
-          H[v] = k * (dh[s].get(v) + H[v]);
-          P[v] = P[v] == 0.0f ? 0.0f : P[v] * k;
+          H[v] = k[s][v] * (dh[s].get(v) + H[v]);
+          P[v] = P[v] == 0.0f ? 0.0f : P[v] * k[s][v];
         }
     }
     fwd.put(p, Pf, Hf);
@@ -435,7 +434,7 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
         if (span.borders && (span.first >> s & 1)) h[v] = state(s, v);
         const float b = bb[s][v];
         bb[s][v] = h[v];
-        h[v] = __builtin_fmaf(decay<kNear>(e[s][v]), h[v], b);
+        h[v] = __builtin_fmaf(k[s][v], h[v], b);
       }
     const int step = static_cast<int>(D * sizeof(T));
     const buf_t to_x = rows_from<S>(d.dx, p.t0, step, step), to_i = rows_from<S>(d.di, p.t0, step, step),
@@ -447,15 +446,15 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
       float dx[V], di[V], dr[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float lam = dh[s].get(v) + psi[v];
-        const float k = decay<kNear>(e[s][v]), m2 = one_minus_square<kNear>(e[s][v]);
-        const float w = m2 > 0.0f ? rsqrt_(m2) : 0.0f;              // 1 / m
-        const float lm = lam * (m2 * w), g = sigmoid(gi[s].get(v)), gx = g * x[s].get(v);
-        dx[v] = lm * g;
-        di[v] = lm * gx * (1.0f - g);
-        psi[v] = k * lam;
-        const float es = psi[v] * __builtin_fmaf(-gx * k, w, bb[s][v]) * sg[s][v];
-        dr[v] = es * rate[v] * (1.0f - sg[s][v]);
+        const float lam = dh[s].get(v) + psi[v], a = k[s][v];
+        const float w = m[s][v] > 0.0f ? __builtin_amdgcn_rcpf(m[s][v]) : 0.0f;
+        const float lm = lam * m[s][v], li = lm * gx[s][v];
+        dx[v] = lm * g[s][v];
+        di[v] = __builtin_fmaf(-g[s][v], li, li);
+        psi[v] = a * lam;
+        const float es = psi[v] * __builtin_fmaf(-gx[s][v] * a, w, bb[s][v]) * sg[s][v];
+        const float er = es * rate[v];
+        dr[v] = __builtin_fmaf(-sg[s][v], er, er);
         sum[v] += es;
       }
       Raw<T, V>::store(to_x, at, s * step, dx);

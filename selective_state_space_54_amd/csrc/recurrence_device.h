@@ -103,13 +103,13 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
 }
 __device__ __forceinline__ float sqrt_(float v) { return __builtin_amdgcn_sqrtf(v); }
-__device__ __forceinline__ float rsqrt_(float v) { return __builtin_amdgcn_rsqf(v); }
 
 // The decay a = exp(u), u = A s <= 0, as one number q that keeps both a and 1 - a^2.
 //
 // A state that remembers thousands of tokens has a within 1e-3 of 1, where 1 - a^2 cancels and
 // where a bias of a's last place (the exponential's own rounding) adds up over those tokens.
-// So down to u = -1/4 q is e = exp(u) - 1 <= 0 from its series (the next term is 2e-9 of it): a = 1 + e
+// So down to u = -1/4 q is e = exp(u) - 1 <= 0 from u (1 + u p(u)), p of degree 3 the closest there
+// (6e-9 of e, its rounded coefficients included; the series needs two terms more): a = 1 + e
 // is rounded once, 1 - a^2 = -e (2 + e).  Below, q is a itself, positive; decays forget within a
 // few tokens and the exponential's last place is enough.  (dA of 4 x 8192 x 2048 bf16, whose
 // terms cancel to 1 in 100: off by 1e-5 of its norm with the exponential alone.)
@@ -118,11 +118,9 @@ constexpr float kSeries = -0.25f;
 
 template <bool kNear>
 __device__ __forceinline__ float decay_of(float u) {
-  float e = __builtin_fmaf(u, 1.0f / 5040.0f, 1.0f / 720.0f);
-  e = __builtin_fmaf(e, u, 1.0f / 120.0f);
-  e = __builtin_fmaf(e, u, 1.0f / 24.0f);
-  e = __builtin_fmaf(e, u, 1.0f / 6.0f);
-  e = __builtin_fmaf(e, u, 0.5f);
+  float e = __builtin_fmaf(u, 0.0075347293f, 0.041502327f);
+  e = __builtin_fmaf(e, u, 0.16665322f);
+  e = __builtin_fmaf(e, u, 0.49999964f);
   e = __builtin_fmaf(e, u, 1.0f) * u;
   if constexpr (!kNear) {
     // (a decay below the normal numbers stays positive; NaN goes on as it is)
