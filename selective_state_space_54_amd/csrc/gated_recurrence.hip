@@ -40,7 +40,7 @@ template <typename T>
 struct Forward {
   static constexpr int S = sizeof(T) == 2 ? 16 : 8, W = 8;
 };
-// All tokens in one tile: shorter chains of operations (45 x 2560 bf16: kernel 6.3 us, 10.4 with tiles of 128).
+// All tokens in one tile: shorter chains of operations (45 x 1536 bf16: kernel 6.3 us, 10.4 with tiles of 128).
 template <typename T>
 struct Short {
   static constexpr int S = 4, W = 16;
