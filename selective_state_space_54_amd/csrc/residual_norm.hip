@@ -22,6 +22,10 @@
 // N values, threads past the end repeat it, and rows past the last one repeat the last one.
 // All of those compute the same values again and write them to the same place; only the sums leave
 // them out.  So outputs must not be inputs.
+//
+// bfloat16, every part: 32768 x 2560 169 us (5.0 TB/s; 202 before the loads ahead), its gradient 286 us
+// (4.7 TB/s; 614 with branches and the sums' own pass), 8 rows 7 us; float32 gradient 16384 x 1536 with
+// gates that 2048 rows share 130 us (4.6 TB/s; 295).
 #include <type_traits>
 
 #include "mssm_internal.h"
