@@ -12,8 +12,8 @@
 // batches of rows take turns in registers, the next on its way while one is worked on, and no
 // branch stands around their loads and stores: what is not to be written goes to a buffer
 // of no bytes.  A batch with a border between sequences goes token by token instead.
-// bfloat16, k = 4: packed 32768 x 5120 in 23 sequences 145 us (4.7 TB/s; 184 with branches and a
-// launch of its own for the last states), the gradient of 16 x 2048 x 5120 231 us (4.4 TB/s; 250), one token
+// bfloat16, k = 4: packed 32768 x 5120 in 23 sequences 135 to 141 us (4.9 TB/s; 184 with branches and a
+// launch of its own for the last states), the gradient of 16 x 2048 x 5120 219 us (4.6 TB/s; 250), one token
 // of 256 x 5120 6 us.
 #include <type_traits>
 
@@ -28,10 +28,10 @@ constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kBatch = 8;             // tokens loaded together
 // Bytes a lane holds and tokens a run at most, forward and backward.  Packed 32768 x 5120 bf16: 4 bytes
-// 144 us, 8 bytes 148, 16 bytes 155 (4 bytes and runs of 128 tokens 150).  The gradient of 16 x 2048 x
-// 5120: 8 bytes 230 us, with 4096 or 8192 wavefronts, runs of 64 tokens 233, 16384 wavefronts 240.
+// and runs of 32 tokens 135 us, 64 tokens 138, 128 tokens 143; 8 bytes and 64 tokens 141.  The gradient of
+// 16 x 2048 x 5120: 8 bytes and runs of 64 or 128 tokens 219 us, 256 tokens 231, 32 tokens 255.
 constexpr int kFwdBytes = 4, kBwdBytes = 8;
-constexpr int64_t kFwdRun = 64, kBwdRun = 128;
+constexpr int64_t kFwdRun = 32, kBwdRun = 128;
 constexpr int64_t kWavesWanted = 4096;
 
 struct Lane {
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kBlock, 2) void conv_kernel(ConvArgs a, int64_t gro
   using Batch = Raw<T, V>[kBatch];
   Batch u[2];
   auto load = [&](Batch& to, int64_t tb) __attribute__((always_inline)) {
-    load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, T0, p.c, to);
+    load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, t1, p.c, to);    // (no rows past the run's)
   };
   load(u[0], t0);
   float w[K][V], bias[V], win[K > 1 ? K - 1 : 1][V];
@@ -235,9 +235,11 @@ __global__ __launch_bounds__(kBlock, 2) void conv_bwd_kernel(ConvArgs a, ConvGra
   if (t0 < T0) {
     using Batch = Raw<T, V>[kBatch];
     Batch u[2], g[2];
+    const int64_t stop = t1 + K - 1;            // tokens up to t1 + K - 2 reach back into the run
+    const int64_t end = stop < T0 ? stop : T0;
     auto load = [&](int k, int64_t tb) __attribute__((always_inline)) {
-      load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, T0, p.c, u[k]);
-      load_rows<T, V, kBatch>(d.dy, a.D, a.D, tb, T0, p.c, g[k]);
+      load_rows<T, V, kBatch>(a.u, a.u_row, a.D, tb, end, p.c, u[k]);
+      load_rows<T, V, kBatch>(d.dy, a.D, a.D, tb, end, p.c, g[k]);
     };
     load(0, t0);
     float w[K][V], bias[V], win[K > 1 ? K - 1 : 1][V];
@@ -319,7 +321,6 @@ __global__ __launch_bounds__(kBlock, 2) void conv_bwd_kernel(ConvArgs a, ConvGra
         }
       }
     };
-    const int64_t stop = t1 + K - 1;            // tokens up to t1 + K - 2 reach back into the run
     auto work = [&](int k, int64_t tb) __attribute__((always_inline)) {
       // the row that token tb completes
       const char* du = static_cast<const char*>(d.du) + (tb - (K - 1)) * step;
