@@ -675,7 +675,7 @@ mssm_status mssm_causal_conv1d_bwd(const void *u, const float *weight, const flo
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
  * with the input gate i and the decay gate r before their sigmoids.
  *   x, input_gate, decay_gate : [tokens, D] of `dtype`, rows x_row, i_row, r_row elements apart
- *   A                 : [D] float32, <= 0 (positive rates give NaN)
+ *   A                 : [D] float32, <= 0 (what positive rates give is not specified)
  *   h                 : [tokens, D] of `dtype`, rounded once from the float32 state
  *   state, last_state : [seqs, D] float32, or NULL (zero, not wanted); last_state is not state
  *   saved             : NULL, or mssm_gated_recurrence_saved_size bytes (256-byte aligned) that
