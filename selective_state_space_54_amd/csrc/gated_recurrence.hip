@@ -21,7 +21,7 @@
 //
 // Memory is the floor (5.1 TB/s of a large copy), and what a tile waits for what bounds it: with 127
 // registers two tiles share a compute unit, and while one loads, forms gates or looks back the
-// other does the same.  bfloat16: 1 x 131072 x 2560 645 us (4.2 TB/s; floor 522), packed 32768 x 2048
+// other does the same.  bfloat16: 1 x 131072 x 2560 635 us (4.2 TB/s; floor 522), packed 32768 x 2048
 // with states 172 us (floor 104), the gradient of 4 x 8192 x 2048 269 us (3.5 TB/s; floor 183), one token
 // of 256 x 5120 6 us.
 #include <type_traits>
@@ -40,14 +40,15 @@ constexpr int64_t kTicketStride = 32;     // counters on cache lines of their ow
 
 // A wavefront's tokens and a block's wavefronts.  Forward: tiles of 128 tokens (float32: 64) of 128
 // channels, two blocks a compute unit; what a tile takes is mostly waiting (15 us: ticket 1, loads 3,
-// gates 3, its wavefronts 3, look-back 4), so smaller tiles are no better (131072 x 2560 bf16: 645 us,
+// gates 3, its wavefronts 3, look-back 4), so smaller tiles are no better (131072 x 2560 bf16: 635 us,
 // 850 with four wavefronts, 887 with 8 tokens), nor larger ones (1130 with sixteen wavefronts), nor four
 // channels a lane (1180), nor one block that loads ahead (780).
 template <typename T>
 struct Forward {
   static constexpr int S = sizeof(T) == 2 ? 16 : 8, W = 8;
 };
-// All tokens in one tile: shorter chains of operations (45 x 1536 bf16: kernel 6.3 us, 10.4 with tiles of 128).
+// All tokens in one tile: shorter chains of operations (45 x 1536 bf16: kernel 6.3 us, 10.4 with tiles of
+// 128).
 template <typename T>
 struct Short {
   static constexpr int S = 4, W = 16;
@@ -108,7 +109,8 @@ __device__ __forceinline__ void look_back(uint64_t* slots, int64_t j, int64_t D,
           const uint32_t p = static_cast<uint32_t>(w[i][v]);
           const float u = __uint_as_float(static_cast<uint32_t>(w[i][v] >> 32));
           h[v] = p == kState ? u : join(__uint_as_float(p), u, h[v]);
-          found = (found || p == kState) && p != kEmpty;
+          // (where P = 0, H is the state: 131072 x 2560 bf16 645 -> 635 us)
+          found = (found || p == kState || p == 0) && p != kEmpty;
         }
         known = known && found;
       }
@@ -350,10 +352,9 @@ __global__ __launch_bounds__(64 * W, 4) void recurrence_kernel(RecurrenceArgs a,
 
 // saved: the state before each tile (null: zero); part: [tiles, D] the tiles' sums of dA.
 template <typename T, int V>
-__global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(RecurrenceArgs a, RecurrenceGrads d,
-                                                                int64_t groups, int64_t tiles,
-                                                                uint32_t* tickets, uint64_t* slots,
-                                                                const float* saved, float* part) {
+__global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
+    RecurrenceArgs a, RecurrenceGrads d, int64_t groups, int64_t tiles, uint32_t* tickets,
+    uint64_t* slots, const float* saved, float* part) {
   constexpr int S = Backward<T>::S, W = Backward<T>::W;
   static_assert(S * W == kSavedTokens, "a saved state for each tile");
   __shared__ Maps<V, W> fwd, rev;
@@ -608,7 +609,8 @@ RecurrencePlan plan_recurrence(int64_t tokens, int64_t D, bool backward, bool sa
   // the two directions follow one another and share the counters and slots
   const int64_t links = backward ? p.bwd_tiles : p.tiles;
   if (links > 1) {
-    p.tickets = take(static_cast<size_t>(backward ? p.bwd_groups : p.groups) * kTicketStride * sizeof(uint32_t));
+    p.tickets = take(static_cast<size_t>(backward ? p.bwd_groups : p.groups) * kTicketStride *
+                     sizeof(uint32_t));
     p.slots = take(static_cast<size_t>(links) * D * sizeof(uint64_t));
   }
   if (backward) {

@@ -25,7 +25,7 @@ def wide_stores_with_offset(asm_text):
     return bad
 
 
-def test_checker_flags_a_scalar_offset():
+def test_a_scalar_offset_is_found():
     asm = "\n".join(["\tbuffer_store_dwordx4 v[0:3], v89, s[28:31], s71 offen",
                      "\tbuffer_store_dwordx4 v[0:3], v89, s[28:31], 0 offen",
                      "\tbuffer_store_dwordx2 v[0:1], v89, s[28:31], s71 offen"])
