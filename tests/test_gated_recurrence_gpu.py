@@ -205,6 +205,15 @@ def test_rates_and_gates_at_the_ends(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_tiles_that_forget_what_was_before(dtype, packed):
+    """Several tiles, beside channels of long memory some whose decays over a tile come to zero."""
+    c = make(31, [700, 700], 130, dtype, packed, rates=(1e-4, 200.0))
+    check_forward(c, dtype, with_state=True)
+    check_backward(c, dtype, with_state=True, with_dlast=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_a_rate_of_zero_keeps_the_state(dtype):
     c = make(33, [70], 66, dtype)
     c["A"][:] = 0.0
