@@ -628,7 +628,7 @@ namespace {
 hipError_t prepare(const RecurrencePlan& p, int64_t links, int64_t groups, const Sequences& seqs,
                    const float* from, float* to, int64_t D, char* ws, hipStream_t stream) {
   Prepare a;
-  const bool clear = links > 1, states = to && (seqs.offsets || seqs.L == 0);
+  const bool clear = links > 1, states = to && seqs.n > 0 && (seqs.offsets || seqs.L == 0);
   if (!clear && !states) return hipSuccess;
   a.slots = reinterpret_cast<uint4*>(ws + p.slots);
   a.n = (links * D + 1) / 2;                         // (slots end at a multiple of 256 bytes)
