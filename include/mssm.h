@@ -680,8 +680,8 @@ mssm_status mssm_causal_conv1d_bwd(const void *u, const float *weight, const flo
  *   state, last_state : [seqs, D] float32, or NULL (zero, not wanted); last_state is not state
  *   saved             : NULL, or mssm_gated_recurrence_saved_size bytes (256-byte aligned) that
  *                       receive states for the backward call, about one in every 64 tokens'
- * Where A sigmoid(r) > -1/4, 1 - a^2 and a keep their last place.  A decay that comes to zero in
- * float32 over a few dozen tokens forgets the state completely.
+ * Where A sigmoid(r) > -1/4, 1 - a^2 and a keep their last place.  No decay is zero: a state (a
+ * gradient) that is infinite or NaN reaches every later (earlier) token of its sequence and channel.
  *
  * mssm_gated_recurrence_step: one token for each of `seqs` sequences, the state [seqs, D] read and
  *   overwritten; x, gates, h [seqs, D].  No workspace.

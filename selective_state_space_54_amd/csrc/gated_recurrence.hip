@@ -60,11 +60,16 @@ struct Backward {
   static constexpr int S = 8, W = 8;
 };
 
-// Joins the affine map (P, H) behind state h.  P = 0 stands for a sequence's first token in between
-// (or a decay of nothing): what h was, infinite or NaN too, is forgotten.
+// Joins the affine map (P, H) behind state h.  P = 0 stands for a sequence's first token in between:
+// what h was, infinite or NaN too, is forgotten.
 __device__ __forceinline__ float join(float P, float H, float h) {
   return P == 0.0f ? H : __builtin_fmaf(P, h, H);
 }
+
+// A product of decays within a sequence.  Where float32 rounds it to zero it is the smallest number above
+// instead, 2^-149, which adds at most 5e-7 to a state: what is infinite or NaN goes on through
+// the sequence, as it does token by token.
+__device__ __forceinline__ float within(float P) { return P == 0.0f ? __uint_as_float(1u) : P; }
 
 // A chain's slots, [tiles, D]: a tile's map (P, H) in one word, or its state, marked by P = -1
 // (decays are not negative), or nothing yet (all bits set, which no map is).  A word is written and
@@ -109,7 +114,7 @@ __device__ __forceinline__ void look_back(uint64_t* slots, int64_t j, int64_t D,
           const uint32_t p = static_cast<uint32_t>(w[i][v]);
           const float u = __uint_as_float(static_cast<uint32_t>(w[i][v] >> 32));
           h[v] = p == kState ? u : join(__uint_as_float(p), u, h[v]);
-          // (where P = 0, H is the state: 131072 x 2560 bf16 645 -> 635 us)
+          // (P = 0: a sequence begins in the tile, and H is the state)
           found = (found || p == kState || p == 0) && p != kEmpty;
         }
         known = known && found;
@@ -214,7 +219,7 @@ struct Maps {
         const int w = kReverse ? W - 1 - k : k;
         const float q = p[w][lane * V + v];
         H[v] = join(q, h[w][lane * V + v], H[v]);
-        P[v] = q == 0.0f ? 0.0f : P[v] * q;
+        P[v] = q == 0.0f || P[v] == 0.0f ? 0.0f : within(P[v] * q);
       }
     }
   }
@@ -315,6 +320,10 @@ __global__ __launch_bounds__(64 * W, 4) void recurrence_kernel(RecurrenceArgs a,
         for (int v = 0; v < V; ++v) H[v] = __builtin_fmaf(da[s][v], H[v], b[s][v]), P[v] *= da[s][v];
       }
     }
+  }
+  if (!span.first) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = within(P[v]);
   }
   chain<V, W, false>(p, maps, slots, tiles, D, P, H, h);
   if (!p.active) return;
@@ -432,6 +441,11 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
           H[v] = k[s][v] * (dh[s].get(v) + H[v]);
           P[v] = P[v] == 0.0f ? 0.0f : P[v] * k[s][v];
         }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!span.first) Pf[v] = within(Pf[v]);
+      if (!span.last) P[v] = within(P[v]);
     }
     fwd.put(p, Pf, Hf);
     chain<V, W, true>(p, rev, slots, tiles, D, P, H, psi);     // (its barrier is fwd's too)
