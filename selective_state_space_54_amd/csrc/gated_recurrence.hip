@@ -397,17 +397,17 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
   auto work = [&](auto near_) __attribute__((always_inline)) {
     constexpr bool kNear = decltype(near_)::value;
     // sigmoid(r), a, sigmoid(i) and that times x, m; the input term, then h_{t-1}
-    float sg[S][V], k[S][V], g[S][V], gx[S][V], m[S][V], bb[S][V];
+    Gate sg[S][V], g[S][V];
+    float k[S][V], gx[S][V], m[S][V], bb[S][V];
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        sg[s][v] = sigmoid(gr[s].get(v));
-        const float q = decay_of<kNear>(rate[v] * sg[s][v]);
+        const float open = sg[s][v].make(gr[s].get(v));
+        const float q = decay_of<kNear>(rate[v] * open);
         k[s][v] = decay<kNear>(q);
         m[s][v] = sqrt_(one_minus_square<kNear>(q));
-        g[s][v] = sigmoid(gi[s].get(v));
-        gx[s][v] = g[s][v] * x[s].get(v);
+        gx[s][v] = g[s][v].make(gi[s].get(v)) * x[s].get(v);
         bb[s][v] = m[s][v] * gx[s][v];
       }
 
@@ -472,12 +472,11 @@ __global__ __launch_bounds__(64 * Backward<T>::W, 4) void recurrence_bwd_kernel(
         const float lam = dh[s].get(v) + psi[v], a = k[s][v];
         const float w = m[s][v] > 0.0f ? __builtin_amdgcn_rcpf(m[s][v]) : 0.0f;
         const float lm = lam * m[s][v], li = lm * gx[s][v];
-        dx[v] = lm * g[s][v];
-        di[v] = __builtin_fmaf(-g[s][v], li, li);
+        dx[v] = lm * g[s][v].value();
+        di[v] = li * g[s][v].rest();
         psi[v] = a * lam;
-        const float es = psi[v] * __builtin_fmaf(-gx[s][v] * a, w, bb[s][v]) * sg[s][v];
-        const float er = es * rate[v];
-        dr[v] = __builtin_fmaf(-sg[s][v], er, er);
+        const float es = psi[v] * __builtin_fmaf(-gx[s][v] * a, w, bb[s][v]) * sg[s][v].value();
+        dr[v] = es * rate[v] * sg[s][v].rest();
         sum[v] += es;
       }
       Raw<T, V>::store(to_x, at, s * step, dx);

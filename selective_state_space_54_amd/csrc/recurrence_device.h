@@ -102,6 +102,23 @@ __device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
 }
+
+// s = sigmoid(v) with 1 - s, for a slope s (1 - s), as one number.  Past v = 0, where 1 - s cancels
+// (at 10 only ten of its bits are left), the number is -(1 - s) from the same exponential, e s with
+// e = exp(-v) < 1; elsewhere it is s.  The sign bit says which, of a zero too.
+struct Gate {
+  float q;
+  __device__ __forceinline__ float make(float v) {     // returns s
+    const float e = fast_exp2(-v * kLog2e), s = __builtin_amdgcn_rcpf(1.0f + e);
+    q = e < 1.0f ? -(e * s) : s;
+    asm volatile("" : "+v"(q));       // (as one number from here on: s and 1 - s both kept would spill)
+    return s;
+  }
+  __device__ __forceinline__ bool open() const { return __float_as_int(q) < 0; }
+  __device__ __forceinline__ float value() const { return open() ? 1.0f - fabsf(q) : fabsf(q); }
+  __device__ __forceinline__ float rest() const { return open() ? fabsf(q) : 1.0f - fabsf(q); }
+};
+
 __device__ __forceinline__ float sqrt_(float v) { return __builtin_amdgcn_sqrtf(v); }
 
 // The decay a = exp(u), u = A s <= 0, as one number q that keeps both a and 1 - a^2.
