@@ -735,7 +735,8 @@ mssm_status mssm_gated_recurrence_bwd(const void *x, const void *input_gate,
  * values, with rms(v) = v / sqrt(mean(v^2) + eps):
  *     t   = residual + scale * act(gate) * rms(y) * post_weight       rounded to `dtype`
  *     out = rms(t) * weight
- *   y, residual, out, total : [rows, D] of `dtype`; total receives t.  Outputs are not inputs
+ *   y, residual, out, total : [rows, D] of `dtype`; total receives t.  An output begins at the address of
+ *                       no input and of no other output (MSSM_ERROR_INVALID_VALUE), here and below
  *   weight            : [D] float32
  *   post_weight       : [D] float32, or NULL: y itself takes rms(y) * post_weight's place
  *   gate              : [rows / gate_rows, D] of `dtype`: row r reads gate row r / gate_rows; or NULL.

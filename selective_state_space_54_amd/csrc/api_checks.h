@@ -31,6 +31,19 @@ inline mssm_status check_workspace(const void* ws, size_t have, size_t need) {
   return MSSM_SUCCESS;
 }
 
+// Whether two of the outputs, or an output and an input, begin at one address.
+inline bool same_address(std::initializer_list<const void*> outputs,
+                         std::initializer_list<const void*> inputs = {}) {
+  for (auto a = outputs.begin(); a != outputs.end(); ++a) {
+    if (!*a) continue;
+    for (auto b = a + 1; b != outputs.end(); ++b)
+      if (*a == *b) return true;
+    for (const void* b : inputs)
+      if (*a == b) return true;
+  }
+  return false;
+}
+
 inline mssm_status done(hipError_t e, const char* where) {
   if (e == hipSuccess) return MSSM_SUCCESS;
   set_hip_error(e, where);

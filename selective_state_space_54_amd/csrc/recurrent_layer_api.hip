@@ -8,6 +8,7 @@ using mssm::bad_dtype;
 using mssm::check_workspace;
 using mssm::done;
 using mssm::product;
+using mssm::same_address;
 
 // A row of values, or from one token's to the next one's: sixteen of them are reached in 31 bits.
 constexpr int64_t kMaxRow = int64_t(1) << 24;
@@ -317,8 +318,8 @@ mssm_status mssm_residual_norm_fwd(const void* y, const void* residual, const fl
   if (rows == 0 || D == 0) return MSSM_SUCCESS;
   if (!y || !residual || !weight || !out || !total) return MSSM_ERROR_INVALID_VALUE;
   if (post_rstd && (!rstd || !post_weight)) return MSSM_ERROR_INVALID_VALUE;
-  for (const void* in : {y, residual, gate})
-    if (in && (in == total || in == out)) return MSSM_ERROR_INVALID_VALUE;
+  if (same_address({out, total, rstd, post_rstd}, {y, residual, weight, post_weight, gate, scale}))
+    return MSSM_ERROR_INVALID_VALUE;
   mssm::ResidualNormArgs a;
   a.y = y, a.residual = residual, a.weight = weight, a.post_weight = post_weight;
   a.gate = gate, a.gate_rows = gate ? gate_rows : 1, a.silu = gate_form == MSSM_ACT_SILU;
@@ -355,11 +356,12 @@ mssm_status mssm_residual_norm_bwd(const void* dout, const void* dtotal, const v
     if (!dout || !y || !total || !weight || !rstd || !dy || !dresidual ||
         !post_weight != !post_rstd || !gate != !dgate)
       return MSSM_ERROR_INVALID_VALUE;
-    for (const void* in : {dout, dtotal, y, total, gate})
-      if (in && (in == dy || in == dresidual || in == dgate)) return MSSM_ERROR_INVALID_VALUE;
     st = check_workspace(workspace, workspace_bytes,
                          mssm::residual_norm_bwd_workspace(rows, D, gate_rows, dtype));
     if (st != MSSM_SUCCESS) return st;
+    if (same_address({dy, dresidual, dgate, dweight, dpost_weight, dscale},
+                     {dout, dtotal, y, total, weight, post_weight, gate, scale, rstd, post_rstd}))
+      return MSSM_ERROR_INVALID_VALUE;
   }
   mssm::ResidualNormArgs a;
   a.y = y, a.weight = weight, a.post_weight = post_weight;
