@@ -614,7 +614,9 @@ mssm_status mssm_layer_norm_bwd(const void *dy, const void *dsum, const void *x,
  * its first).  Offsets outside 0 .. L are taken as 0 or L; tokens before the first and behind the
  * last sequence may hold anything, and their outputs and gradients are left as they were.
  * What is not finite in a sequence stays in that sequence and channel.  Any element-aligned
- * address.  D is below 2^24; so are rows, but in the single-token calls.  Sums over tokens or rows run in a fixed order, so results are
+ * address.  Outputs alias neither inputs nor one another (at the same address, where
+ * that gives wrong results: MSSM_ERROR_INVALID_VALUE).  D is below 2^24; so are rows, but in
+ * the single-token calls.  Sums over tokens or rows run in a fixed order, so results are
  * deterministic.  tokens, seqs or D equal to zero are valid: last states and the parameters'
  * gradients are still set.
  */
@@ -735,8 +737,7 @@ mssm_status mssm_gated_recurrence_bwd(const void *x, const void *input_gate,
  * values, with rms(v) = v / sqrt(mean(v^2) + eps):
  *     t   = residual + scale * act(gate) * rms(y) * post_weight       rounded to `dtype`
  *     out = rms(t) * weight
- *   y, residual, out, total : [rows, D] of `dtype`; total receives t.  An output begins at the address of
- *                       no input and of no other output (MSSM_ERROR_INVALID_VALUE), here and below
+ *   y, residual, out, total : [rows, D] of `dtype`; total receives t
  *   weight            : [D] float32
  *   post_weight       : [D] float32, or NULL: y itself takes rms(y) * post_weight's place
  *   gate              : [rows / gate_rows, D] of `dtype`: row r reads gate row r / gate_rows; or NULL.

@@ -214,6 +214,9 @@ mssm_status mssm_causal_conv1d_fwd(const void* u, const float* weight, const flo
     return MSSM_SUCCESS;
   }
   if ((st = conv_sizes(a.seqs, D, false, dtype)) != MSSM_SUCCESS) return st;
+  if (same_address({a.seqs.tokens > 0 ? y : nullptr, k > 1 ? last_state : nullptr},
+                   {u, weight, bias, state}))
+    return MSSM_ERROR_INVALID_VALUE;
   a.D = D, a.k = k;
   a.u = u, a.u_row = u_row, a.weight = weight, a.bias = bias;
   a.silu = act == MSSM_ACT_SILU;
@@ -236,6 +239,10 @@ mssm_status mssm_causal_conv1d_step(const void* u, const float* weight, const fl
   int64_t n;
   if (!product({seqs, D}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (n >= kMaxThreads - 256) return MSSM_ERROR_NOT_SUPPORTED;
+  const void* kept = k > 1 ? state : nullptr;
+  // (a thread reads its own value of a dense u before it writes that of y)
+  if (same_address({y, kept}, {weight, bias}) || (kept && kept == u) || (y == u && u_row != D))
+    return MSSM_ERROR_INVALID_VALUE;
   a.D = D, a.k = k;
   a.u = u, a.u_row = u_row, a.weight = weight, a.bias = bias;
   a.silu = act == MSSM_ACT_SILU;
@@ -277,6 +284,10 @@ mssm_status mssm_causal_conv1d_bwd(const void* u, const float* weight, const flo
   st = check_workspace(workspace, workspace_bytes,
                        mssm::conv_bwd_workspace(a.seqs.tokens, D, k, dtype));
   if (st != MSSM_SUCCESS) return st;
+  if (same_address({a.seqs.tokens > 0 ? du : nullptr, dweight, dbias,
+                    k > 1 && seqs > 0 ? dstate : nullptr},
+                   {u, weight, bias, state, dy, dlast}))
+    return MSSM_ERROR_INVALID_VALUE;
   a.D = D, a.k = k;
   a.u = u, a.u_row = u_row, a.weight = weight, a.bias = bias;
   a.silu = act == MSSM_ACT_SILU;

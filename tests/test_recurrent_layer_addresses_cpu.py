@@ -48,3 +48,32 @@ def test_residual_norm(lib):
 
     refused(call, args, "dy dresidual dgate dweight dpost dscale",
             "dout dtotal y total weight post gate scale rstd post_rstd")
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_convolution(lib, packed):
+    """A run reads rows of the runs beside it, so an output in an input's place would be read again."""
+    without = () if packed else ("offsets",)
+    args = addresses("u weight bias offsets state y last", without)
+
+    def call(k=4, **p):
+        return lib.mssm_causal_conv1d_fwd(*p.values(), 1, 2, 50, 40, k, 40, BF16, None)
+
+    refused(call, args, "y last", "u weight bias state")
+    args = addresses("u weight bias offsets state dy dlast du dweight dbias dstate workspace", without)
+
+    def call(workspace, **p):
+        return lib.mssm_causal_conv1d_bwd(*p.values(), 1, workspace, ROOM, 2, 50, 40, 4, 40, BF16, None)
+
+    refused(call, args, "du dweight dbias dstate", "u weight bias state dy dlast")
+
+
+def test_convolution_of_one_token(lib):
+    args = addresses("u weight bias state y")
+
+    def call(row=40, **p):
+        return lib.mssm_causal_conv1d_step(*p.values(), 1, 2, 40, 4, row, BF16, None)
+
+    refused(call, args, "y state", "weight bias")
+    assert call(**dict(args, state=args["u"])) == INVALID
+    assert call(row=80, **dict(args, y=args["u"])) == INVALID       # other sequences' rows
