@@ -50,6 +50,13 @@ mssm_status recurrence_plan(const mssm::Sequences& s, int64_t D, bool backward, 
   return n < kMaxThreads ? MSSM_SUCCESS : MSSM_ERROR_NOT_SUPPORTED;
 }
 
+// Whether a dense output lies over an input whose rows lie otherwise, so that a row is written while
+// another one is still to be read there.
+bool overwritten(const void* out, int64_t D, const void* x, int64_t x_row, const void* i,
+                 int64_t i_row, const void* r, int64_t r_row) {
+  return (out == x && x_row != D) || (out == i && i_row != D) || (out == r && r_row != D);
+}
+
 mssm_status check_saved(const void* saved, size_t have, size_t need) {
   return check_workspace(saved, have, need);
 }
@@ -106,6 +113,9 @@ mssm_status mssm_gated_recurrence_fwd(const void* x, const void* input_gate,
     return st;
   if (saved && (st = check_saved(saved, saved_bytes, p.saved_bytes)) != MSSM_SUCCESS) return st;
   if ((st = check_workspace(workspace, workspace_bytes, p.bytes)) != MSSM_SUCCESS) return st;
+  if (a.seqs.tokens > 0 &&
+      same_address({h, last_state, saved}, {x, input_gate, decay_gate, A, state}))
+    return MSSM_ERROR_INVALID_VALUE;
   a.D = D;
   a.x = x, a.i = input_gate, a.r = decay_gate, a.A = A;
   a.x_row = x_row, a.i_row = i_row, a.r_row = r_row;
@@ -129,6 +139,9 @@ mssm_status mssm_gated_recurrence_step(const void* x, const void* input_gate,
   int64_t n;
   if (!product({seqs, D}, &n)) return MSSM_ERROR_SIZE_OVERFLOW;
   if (n >= kMaxThreads - 256) return MSSM_ERROR_NOT_SUPPORTED;
+  if (same_address({h, state}, {A}) || same_address({state}, {x, input_gate, decay_gate}) ||
+      overwritten(h, D, x, x_row, input_gate, i_row, decay_gate, r_row))
+    return MSSM_ERROR_INVALID_VALUE;
   a.D = D;
   a.x = x, a.i = input_gate, a.r = decay_gate, a.A = A;
   a.x_row = x_row, a.i_row = i_row, a.r_row = r_row;
@@ -162,6 +175,13 @@ mssm_status mssm_gated_recurrence_bwd(const void* x, const void* input_gate,
     return st;
   if (saved && (st = check_saved(saved, saved_bytes, p.saved_bytes)) != MSSM_SUCCESS) return st;
   if ((st = check_workspace(workspace, workspace_bytes, p.bytes)) != MSSM_SUCCESS) return st;
+  if (a.seqs.tokens > 0) {
+    if (same_address({dx, dinput_gate, ddecay_gate, dA, dstate}, {A, state, saved, dlast}))
+      return MSSM_ERROR_INVALID_VALUE;
+    for (const void* out : {dx, dinput_gate, ddecay_gate})
+      if (overwritten(out, D, x, x_row, input_gate, i_row, decay_gate, r_row))
+        return MSSM_ERROR_INVALID_VALUE;
+  }
   a.D = D;
   a.x = x, a.i = input_gate, a.r = decay_gate, a.A = A;
   a.x_row = x_row, a.i_row = i_row, a.r_row = r_row;

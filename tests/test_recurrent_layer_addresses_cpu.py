@@ -77,3 +77,39 @@ def test_convolution_of_one_token(lib):
     refused(call, args, "y state", "weight bias")
     assert call(**dict(args, state=args["u"])) == INVALID
     assert call(row=80, **dict(args, y=args["u"])) == INVALID       # other sequences' rows
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_recurrence(lib, packed):
+    """The last lanes of a row hold channels of the lanes before them too, which another block may have: h
+    in an input's place would be read there."""
+    without = () if packed else ("offsets",)
+    args = addresses("x i r A offsets state h last saved workspace", without)
+
+    def call(workspace, **p):
+        return lib.mssm_gated_recurrence_fwd(*p.values(), ROOM, workspace, ROOM, 2, 5000, 129, 129, 129,
+                                             129, BF16, None)
+
+    refused(call, args, "h last saved", "x i r A state")
+    args = addresses("x i r A offsets state saved dh dlast dx di dr dA dstate workspace", without)
+
+    def call(x, i, r, A, offsets, state, saved, workspace, row=129, **p):
+        return lib.mssm_gated_recurrence_bwd(x, i, r, A, offsets, state, saved, ROOM, *p.values(), workspace,
+                                             ROOM, 2, 5000, 129, row, row, row, BF16, None)
+
+    refused(call, args, "dx di dr dA dstate", "A state saved dlast")
+    for a in ("dx", "di", "dr"):
+        for b in ("x", "i", "r"):                                   # other tokens' rows
+            assert call(row=130, **dict(args, **{a: args[b]})) == INVALID, (a, b)
+
+
+def test_recurrence_of_one_token(lib):
+    args = addresses("x i r A state h")
+
+    def call(row=40, **p):
+        return lib.mssm_gated_recurrence_step(*p.values(), 2, 40, row, row, row, BF16, None)
+
+    refused(call, args, "h state", "A")
+    for a in ("x", "i", "r"):
+        assert call(**dict(args, state=args[a])) == INVALID, a
+        assert call(row=80, **dict(args, h=args[a])) == INVALID, a  # other sequences' rows
