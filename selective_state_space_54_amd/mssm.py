@@ -1575,6 +1575,9 @@ def _residual_norm_bwd(checked, dout, y, total, weight, rstd, grads, workspace, 
     if post_weight is not None:
         _expect(post_rstd, "post_rstd", torch.float32, shape[:-1], dev)
     g = grads.get
+    if not rows and g("dgate") is not None:     # gate rows that no row shares: a sum of nothing
+        with _on(stream):
+            grads["dgate"].zero_()
     _call("mssm_residual_norm_bwd", dev, stream, dout.data_ptr(), _address(dtotal), y.data_ptr(),
           total.data_ptr(), weight.data_ptr(), _address(post_weight), _address(gate),
           _address(scale), rstd.data_ptr(),
