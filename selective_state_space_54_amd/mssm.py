@@ -1500,10 +1500,10 @@ def _gate_rows(gate, form, y, rows, dev):
     for size in shape[:-1]:
         starts.append(n)
         n *= size
-    if groups < 1 or (rows % groups if len(shape) == 2 else groups not in starts):
+    if (not groups or rows % groups) if len(shape) == 2 else groups not in starts:
         raise ValueError("gate must have y's shape, or be [groups, D] with as many rows as y's "
                          "leading dimensions (a divisor of y's rows where y is [rows, D])")
-    return form, max(rows // groups, 1)
+    return form, max(rows // max(groups, 1), 1)
 
 
 def _residual_norm_check(y, weight, post_weight, gate, gate_form, scale):

@@ -24,3 +24,18 @@ def test_gates_without_rows_have_a_gradient_of_zero(dtype, shape):
     torch.cuda.synchronize()
     for g in (grads, got):
         assert g["dgate"].shape == gate.shape and not g["dgate"].any() and not g["dweight"].any()
+
+
+@pytest.mark.parametrize("shape", [(0, 5, 40), (0, 2, 5, 40)])
+def test_an_empty_batch_has_no_gates(shape):
+    w = torch.ones(40, device="cuda")
+    y, gate = torch.zeros(shape, device="cuda"), torch.zeros(0, 40, device="cuda")
+    out, total, rstd = mssm.residual_norm(y, y, w, gate=gate, return_stats=True)
+    g = mssm.residual_norm_bwd(y, y, total, w, rstd, gate=gate)
+    torch.cuda.synchronize()
+    assert out.shape == total.shape == shape and g["dgate"].shape == (0, 40)
+    assert not g["dweight"].any()
+    some = torch.zeros(3, 40, device="cuda")
+    for full in (some, some.view(3, 1, 40)):
+        with pytest.raises(ValueError, match="gate must have"):
+            mssm.residual_norm(full, full, w, gate=gate)
