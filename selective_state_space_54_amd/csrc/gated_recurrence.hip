@@ -19,11 +19,14 @@
 // first of them waits for none.  A state is always made by the same operations from the one
 // before it, wherever the look-back began: results do not depend on the timing.
 //
-// Memory is the floor (5.1 TB/s of a large copy), and what a tile waits for what bounds it: with 127
-// registers two tiles share a compute unit, and while one loads, forms gates or looks back the
-// other does the same.  bfloat16: 1 x 131072 x 2560 635 us (4.2 TB/s; floor 522), packed 32768 x 2048
-// with states 172 us (floor 104), the gradient of 4 x 8192 x 2048 269 us (3.5 TB/s; floor 183), one token
-// of 256 x 5120 6 us.
+// Memory is the floor (5.1 TB/s of a large copy), and how fast a state goes along a chain what bounds it:
+// kLookBack tiles a poll, which one wavefront makes while its block's others wait.  With every compute
+// unit loading and storing a poll takes near 4 us, and a chain goes on by some 1.6 tiles a microsecond,
+// be it one of 20 (bfloat16, 1 x 131072 x 2560: 1024 tiles in 630 us, 4.3 TB/s; floor 522) or of 16 (packed
+// 32768 x 2048 with states: 256 tiles in 170 us; floor 104).  With one to four chains a poll takes 1.4 us and
+// the time follows the tokens, not the width: 131072 x 64, 128, 256, 512 162, 248, 249, 258 us (floors 13
+// to 104).  The gradient alike, in tiles of 64 tokens: 4 x 8192 x 2048 280 us (3.4 TB/s; floor 183),
+// 1 x 32768 x 128 85 us.  One token of 256 x 5120 6 us.
 #include <type_traits>
 
 #include "mssm_internal.h"
@@ -34,15 +37,16 @@ namespace mssm {
 namespace {
 
 constexpr int kSavedTokens = 64;          // a saved state for every so many tokens
-constexpr int kLookBack = 6;              // tiles looked at together (8, 10 spill: 645, 656, 839 us)
+// Tiles looked at together (131072 x 2560 bf16, 645 us with 6 when these were tried: 8 and 10, which
+// spill, 656 and 839).
+constexpr int kLookBack = 6;
 constexpr int kMaxPolls = 1 << 22;
 constexpr int64_t kTicketStride = 32;     // counters on cache lines of their own
 
 // A wavefront's tokens and a block's wavefronts.  Forward: tiles of 128 tokens (float32: 64) of 128
-// channels, two blocks a compute unit; what a tile takes is mostly waiting (15 us: ticket 1, loads 3,
-// gates 3, its wavefronts 3, look-back 4), so smaller tiles are no better (131072 x 2560 bf16: 635 us,
-// 850 with four wavefronts, 887 with 8 tokens), nor larger ones (1130 with sixteen wavefronts), nor four
-// channels a lane (1180), nor one block that loads ahead (780).
+// channels, two blocks a compute unit.  A tile of 131072 x 2560 bf16 takes 15 us: ticket 1, loads 3, gates
+// 3, its wavefronts 3, look-back 4.  Where that workload took 645 us, four wavefronts took 850, 8 tokens
+// 887, sixteen wavefronts 1130, four channels a lane 1180, and one block that loads ahead 780.
 template <typename T>
 struct Forward {
   static constexpr int S = sizeof(T) == 2 ? 16 : 8, W = 8;
@@ -53,8 +57,8 @@ template <typename T>
 struct Short {
   static constexpr int S = 4, W = 16;
 };
-// Backward: a tile for each saved state (4 tokens by sixteen wavefronts 444 us where this takes 432 in
-// all, tiles and states of 32 tokens 523).
+// Backward: a tile for each saved state (training pass 4 x 8192 x 2048 bf16, 432 us when these were
+// tried: 4 tokens by sixteen wavefronts 444, tiles and states of 32 tokens 523).
 template <typename T>
 struct Backward {
   static constexpr int S = 8, W = 8;

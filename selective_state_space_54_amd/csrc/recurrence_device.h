@@ -105,7 +105,8 @@ __device__ __forceinline__ float sigmoid(float v) {
 
 // s = sigmoid(v) with 1 - s, for a slope s (1 - s), as one number.  Past v = 0, where 1 - s cancels
 // (at 10 only ten of its bits are left), the number is -(1 - s) from the same exponential, e s with
-// e = exp(-v) < 1; elsewhere it is s.  The sign bit says which, of a zero too.
+// e = exp(-v) < 1; elsewhere it is s.  The sign bit says which, of a zero too.  (The gradient of
+// 4 x 8192 x 2048 bf16: 280 us, 270 with slopes from s alone.)
 struct Gate {
   float q;
   __device__ __forceinline__ float make(float v) {     // returns s
@@ -126,11 +127,14 @@ __device__ __forceinline__ float sqrt_(float v) { return __builtin_amdgcn_sqrtf(
 // A state that remembers thousands of tokens has a within 1e-3 of 1, where 1 - a^2 cancels and
 // where a bias of a's last place (the exponential's own rounding) adds up over those tokens.
 // So down to u = -1/4 q is e = exp(u) - 1 <= 0 from u (1 + u p(u)), p of degree 3 the closest there
-// (6e-9 of e, its rounded coefficients included; the series needs two terms more): a = 1 + e
+// (7.2e-9 of e with its rounded coefficients, 1e-7 as float32 evaluates it; the series needs two terms
+// more): a = 1 + e
 // is rounded once, 1 - a^2 = -e (2 + e).  Below, q is a itself, positive; decays forget within a
 // few tokens and the exponential's last place is enough.  (dA of 4 x 8192 x 2048 bf16, whose
 // terms cancel to 1 in 100: off by 1e-5 of its norm with the exponential alone.)
-// kNear: u > -1/4 everywhere.
+// kNear: u > -1/4 everywhere.  With rates from -exp(-4) to -exp(1.5), 131072 x 2560 bf16 takes 628 us where
+// they are in order (half of the wavefronts have one below -1/4) and 650 mixed (all have), 630 without;
+// the training pass 4 x 8192 x 2048 449, 456 and 439.
 constexpr float kSeries = -0.25f;
 
 template <bool kNear>

@@ -569,8 +569,11 @@ hipError_t dispatch(int64_t D, F f) {
 
 // Blocks: what 256 compute units hold at about ten wavefronts each, since more of them only meet
 // in the caches (32768 x 2560 bf16, 5 wavefronts a block: 210, 187, 170 us with 256, 384, 512 blocks and
-// 176, 191 with 768, 1024; 8192 x 4096, 8 wavefronts: 65, 69 us with 256, 512; gradients alike).
-// Narrow rows have up to `most` blocks a unit (30000 x 1001: 131, 92, 81 us with 256, 512, 768).
+// 176, 191 with 768, 1024; 8192 x 4096, 8 wavefronts: 65, 69 us with 256, 512), but not more than `most`.
+// Rows of two and three wavefronts reach `most` before they reach ten, 3 blocks a unit forward and 2
+// backward, which is not their best.  bf16 with 1 to 5 blocks a unit: 30000 x 640 (two wavefronts) 126, 88,
+// 64, 53, 51 us and the gradient 163, 131, 95, 82, 84; 30000 x 1001 (two) 130, 93, 71, 65, 67 and 173, 139,
+// 127, 131, 137; 30000 x 1536 (three; 3 blocks are ten wavefronts) 141, 101, 94 and 178, 156, 162.
 int64_t blocks_for(uint32_t threads, int64_t most) {
   const int64_t fit = 10 / (threads / 64);
   return 256 * (fit < 1 ? 1 : fit > most ? most : fit);
@@ -584,7 +587,7 @@ struct Fwd {
   hipError_t operator()(uint32_t threads) const {
     const int64_t per = TPR ? threads / TPR : 1;
     int64_t blocks = (a.rows + per - 1) / per;
-        const int64_t most = blocks_for(threads, 3);
+    const int64_t most = blocks_for(threads, 3);
     if (blocks > most) blocks = most;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(threads);
     if (a.gate)
